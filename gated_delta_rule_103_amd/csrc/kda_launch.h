@@ -63,6 +63,79 @@ struct OutputGateArgs {
     hipStream_t stream;
 };
 
+struct RecurrentArgs {
+    const void *q, *k, *v;
+    const float *g;
+    const void *beta;
+    float *S;                   // [slots][H][Dv][Dk]
+    void *out;
+    const int32_t *cu;          // [N + 1], device
+    const int32_t *slot_in;     // [N], device, or nullptr (zero states)
+    const int32_t *slot_out;    // [T], device, or nullptr (no state is kept)
+    int N, T, H, Dk, Dv, slots;
+    Dt io, beta_dt, out_dt;
+    hipStream_t stream;
+    bool g_head = false;        // as in PrefillArgs
+    bool qk_norm = false;
+    float norm_eps = 0.f;
+};
+
+struct PrefillBackwardArgs {
+    const void *q, *k, *v;
+    const float *g;
+    const void *beta;
+    const void *dout;
+    const float *S0, *dS_out;   // or nullptr (zero)
+    void *dq, *dk, *dv;
+    float *dg;                  // or nullptr (no gate)
+    void *dbeta;
+    float *dS0;                 // or nullptr (not wanted)
+    const int32_t *cu_seqlens;  // device, or nullptr (dense)
+    int N, B, T, H, Dk, Dv;
+    Dt io, beta_dt, dout_dt;
+    void *ws;
+    hipStream_t stream;
+    bool g_head = false;        // as in PrefillArgs
+    bool qk_norm = false;
+    float norm_eps = 0.f;
+};
+
+struct OutputGateBackwardArgs {
+    const void *o, *gate, *dout;
+    const float *weight;        // [Dv] or nullptr (ones)
+    void *do_, *dgate;
+    float *dweight;             // [Dv] or nullptr (not wanted)
+    int rows, H, Dv;
+    float eps;
+    Dt o_dt, gate_dt, dout_dt;
+    float *ws;
+    hipStream_t stream;
+};
+
+struct LayerNormArgs {
+    const void *x;
+    const float *weight, *bias; // [W] or nullptr
+    void *out;
+    float *mean, *rstd;         // [rows] or nullptr (not wanted)
+    int rows, W;
+    float eps;
+    bool rms;                   // no mean is taken
+    Dt x_dt, out_dt;
+    hipStream_t stream;
+};
+
+struct LayerNormBackwardArgs {
+    const void *x, *dy;
+    const float *mean, *rstd, *weight;
+    void *dx;
+    float *dweight, *dbias;     // [W] or nullptr (not wanted)
+    int rows, W;
+    bool rms;
+    Dt x_dt, dy_dt;
+    float *ws;
+    hipStream_t stream;
+};
+
 // Upper bound on the number of chunks of all sequences (each sequence adds at
 // most one partial chunk).
 inline long long max_chunks(int N, long long T_total, int C) {
@@ -90,5 +163,26 @@ hipError_t launch_decode(const DecodeArgs &a);
 
 // per-head RMS norm and sigmoid output gate of o.
 hipError_t launch_output_gate(const OutputGateArgs &a);
+
+// several tokens per sequence through the recurrence, states in a slot pool.
+bool recurrent_fits(int N, int H, int Dk);   // a launch has fewer than 2^32 threads
+hipError_t launch_recurrent(const RecurrentArgs &a);
+
+// the chunked form's gradient (fp32 arithmetic). fits: whether the launches
+// stay within the runtime's limits.
+size_t prefill_backward_workspace(int N, long long T_total, int H, int Dk);
+bool prefill_backward_fits(int N, long long T_total, int H, int Dk);
+hipError_t launch_prefill_backward(const PrefillBackwardArgs &a);
+
+// the output gate's gradient.
+size_t output_gate_backward_workspace(long long rowheads, int Dv);
+hipError_t launch_output_gate_backward(const OutputGateBackwardArgs &a);
+
+// layer norm and RMS norm of rows of at most kMaxNormWidth channels, and the gradient.
+constexpr int kMaxNormWidth = 16384;
+bool layer_norm_fits(int rows, int W);     // a launch has fewer than 2^32 threads
+hipError_t launch_layer_norm(const LayerNormArgs &a);
+size_t layer_norm_backward_workspace(int rows, int W);
+hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs &a);
 
 }  // namespace kda

@@ -1,0 +1,319 @@
+// layer_norm.hip -- layer norm and RMS norm of rows, and their gradients.
+//
+// Forward, per row x of W values:
+//     mean = sum x / W (0 for RMS),  rstd = 1 / sqrt(sum (x - mean)^2 / W + eps)
+//     y = (x - mean) rstd w + b
+// Backward, with n = (x - mean) rstd and h = dy w:
+//     dx = rstd (h - n mean(h n) - mean(h))        (no mean(h) term for RMS)
+//     dw = sum over rows of dy n,  db = sum over rows of dy
+//
+// Both directions are bound by memory: x (and dy) is read once and held in
+// registers while the row's sums are formed, so nothing is read twice. A row
+// is spread over NW wavefronts, each thread holding K groups of eight
+// channels: consecutive ones, loaded with 16-byte instructions, where every
+// row starts on a 16-byte boundary (W a multiple of 8), else eight channels
+// 64 * NW apart, so that a wavefront's scalar loads stay adjacent. The
+// variance is the mean square of the centred values in registers (a second
+// pass that costs no memory), not a difference of two sums.
+//
+// dw and db reduce over the rows: a thread keeps the same channels for every
+// row that its workgroup takes and sums them in registers; each workgroup
+// writes one partial row to the workspace, and a second kernel adds these in
+// a fixed order, so results repeat bit for bit. No atomics.
+#include "kda_device.h"
+#include "kda_launch.h"
+#include "kda_vec8.h"
+
+namespace kda {
+namespace {
+
+// One group of eight channels: consecutive from `c`, or `step` apart.
+template <bool VEC, typename T>
+__device__ __forceinline__ f32x8 load8(const T *row, int c, int step, int W) {
+    if constexpr (VEC) {
+        return c < W ? vec8<T>::load(row + c) : f32x8{};
+    } else {
+        f32x8 x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = c + i * step < W ? io<T>::load(row, c + i * step) : 0.f;
+        return x;
+    }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T *row, int c, int step, int W, f32x8 x) {
+    if constexpr (VEC) {
+        if (c < W) vec8<T>::store(row + c, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i * step < W) io<T>::store(row, c + i * step, x[i]);
+    }
+}
+
+// How a row lies over the threads of a workgroup: NW wavefronts per row, K
+// groups per thread, 4 / NW rows side by side for NW < 4.
+template <int NW, int K>
+struct Shape {
+    static constexpr int THREADS = NW < 4 ? 256 : 64 * NW;   // per workgroup
+    static constexpr int ROWS = THREADS / (64 * NW);         // rows side by side
+    static constexpr int SPAN = 64 * NW;                     // threads per row
+    static constexpr int MAX_W = SPAN * 8 * K;
+};
+
+// first channel of group k of thread t, and the distance of its channels
+template <bool VEC, int SPAN>
+__device__ __forceinline__ int first_channel(int t, int k) {
+    return VEC ? (k * SPAN + t) * 8 : k * SPAN * 8 + t;
+}
+
+// sum over the NW wavefronts of a row; `part` holds one float per wavefront
+template <int NW>
+__device__ __forceinline__ float row_sum(float x, float *part, int wave_in_row) {
+    x = warp_sum(x);
+    if constexpr (NW > 1) {
+        __syncthreads();                       // the previous sum has been read
+        if ((threadIdx.x & 63) == 0) part[wave_in_row] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) x += part[i];
+    }
+    return x;
+}
+
+template <int NW, int K, bool VEC, typename TI, typename TO>
+__global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_kernel(const TI *__restrict__ x, const float *__restrict__ w,
+                                                                      const float *__restrict__ b, TO *__restrict__ y,
+                                                                      float *__restrict__ mean_out,
+                                                                      float *__restrict__ rstd_out, int rows, int W,
+                                                                      float eps, bool rms) {
+    using S = Shape<NW, K>;
+    __shared__ float part[NW];
+    const int t = threadIdx.x % S::SPAN, wave = t / 64;
+    const int r = blockIdx.x * S::ROWS + threadIdx.x / S::SPAN;
+    if (NW == 1 && r >= rows) return;          // whole wavefronts; NW > 1 has one row per workgroup
+    const TI *row = x + (size_t)r * W;
+    constexpr int STEP = VEC ? 1 : S::SPAN;
+    f32x8 v[K];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k] = load8<VEC>(row, first_channel<VEC, S::SPAN>(t, k), STEP, W);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[k][i];
+    }
+    const float inv = 1.f / W;
+    const float mean = rms ? 0.f : row_sum<NW>(s, part, wave) * inv;
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = first_channel<VEC, S::SPAN>(t, k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = c + i * STEP < W ? v[k][i] - mean : 0.f;
+            v[k][i] = d;
+            ss += d * d;
+        }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<NW>(ss, part, wave) * inv + eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = first_channel<VEC, S::SPAN>(t, k);
+        f32x8 o = v[k] * rstd;
+        if (w) o *= load8<VEC>(w, c, STEP, W);
+        if (b) o += load8<VEC>(b, c, STEP, W);
+        store8<VEC>(y + (size_t)r * W, c, STEP, W, o);
+    }
+    if (t == 0) {
+        if (mean_out) mean_out[r] = mean;
+        if (rstd_out) rstd_out[r] = rstd;
+    }
+}
+
+// part: [gridDim.x][W] of dw, then the same of db (a pointer is null when that
+// gradient is not wanted)
+template <int NW, int K, bool VEC, typename TI, typename TG>
+__global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_backward_kernel(
+    const TI *__restrict__ x, const TG *__restrict__ dy, const float *__restrict__ mean_in,
+    const float *__restrict__ rstd_in, const float *__restrict__ w, TI *__restrict__ dx, float *__restrict__ dw_part,
+    float *__restrict__ db_part, int rows, int W) {
+    using S = Shape<NW, K>;
+    __shared__ float part[NW], part2[NW];
+    __shared__ float fold[S::ROWS > 1 ? (S::ROWS - 1) * S::MAX_W : 1];
+    const int t = threadIdx.x % S::SPAN, wave = t / 64, rg = threadIdx.x / S::SPAN;
+    constexpr int STEP = VEC ? 1 : S::SPAN;
+    f32x8 dw[K] = {}, db[K] = {};
+    const float inv = 1.f / W;
+    // NW > 1: one row per pass, so every thread makes the same number of passes
+    for (long long r = (long long)blockIdx.x * S::ROWS + rg; r < rows; r += (long long)gridDim.x * S::ROWS) {
+        const TI *row = x + (size_t)r * W;
+        const TG *drow = dy + (size_t)r * W;
+        const float mean = mean_in ? mean_in[r] : 0.f, rstd = rstd_in[r];
+        f32x8 n[K], h[K];
+        float shn = 0.f, sh = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = first_channel<VEC, S::SPAN>(t, k);
+            n[k] = load8<VEC>(row, c, STEP, W);
+            h[k] = load8<VEC>(drow, c, STEP, W);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = first_channel<VEC, S::SPAN>(t, k);
+            n[k] = (n[k] - mean) * rstd;       // past the row's end: h is 0 there
+            dw[k] += h[k] * n[k];
+            db[k] += h[k];
+            if (w) h[k] *= load8<VEC>(w, c, STEP, W);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                shn += h[k][i] * n[k][i];
+                sh += h[k][i];
+            }
+        }
+        shn = row_sum<NW>(shn, part, wave) * inv;
+        sh = mean_in ? row_sum<NW>(sh, part2, wave) * inv : 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            store8<VEC>(dx + (size_t)r * W, first_channel<VEC, S::SPAN>(t, k), STEP, W,
+                        (h[k] - n[k] * shn - sh) * rstd);
+    }
+    auto put = [&](f32x8 (&a)[K], float *out) {
+        if constexpr (S::ROWS > 1) {           // the rows side by side, added in a fixed order
+            __syncthreads();
+            if (rg > 0)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    *reinterpret_cast<f32x8 *>(&fold[(rg - 1) * S::MAX_W + (k * S::SPAN + t) * 8]) = a[k];
+            __syncthreads();
+            if (rg > 0) return;
+            for (int g = 0; g < S::ROWS - 1; ++g)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    a[k] += *reinterpret_cast<f32x8 *>(&fold[g * S::MAX_W + (k * S::SPAN + t) * 8]);
+        }
+        // whole partial rows of MAX_W floats would waste traffic: W floats, laid out as the row is
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            store8<VEC>(out + (size_t)blockIdx.x * W, first_channel<VEC, S::SPAN>(t, k), STEP, W, a[k]);
+    };
+    if (dw_part) put(dw, dw_part);
+    if (db_part) put(db, db_part);
+}
+
+// out[c] = sum over g of part[g][c]: 16 threads per channel group of 64, each
+// summing every 16th partial row, then a fixed-order sum over the sixteen.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restrict__ a, float *__restrict__ da,
+                                                          const float *__restrict__ b, float *__restrict__ db, int G,
+                                                          int W) {
+    __shared__ float s[16][64];
+    const float *p = blockIdx.y ? b : a;
+    float *out = blockIdx.y ? db : da;
+    if (!out) return;
+    const int c = blockIdx.x * 64 + (threadIdx.x & 63), j = threadIdx.x >> 6;
+    float x = 0.f;
+    if (c < W)
+        for (int g = j; g < G; g += 16) x += p[(size_t)g * W + c];
+    s[j][threadIdx.x & 63] = x;
+    __syncthreads();
+    if (j == 0 && c < W) {
+        for (int i = 1; i < 16; ++i) x += s[i][threadIdx.x];
+        out[c] = x;
+    }
+}
+
+// rows of the partial sums: as many workgroups as keep the card busy, never
+// more than there are rows for
+int partial_rows(long long rows, int rows_per_wg) {
+    const long long wgs = (rows + rows_per_wg - 1) / rows_per_wg;
+    return static_cast<int>(wgs < 512 ? wgs : 512);
+}
+
+// Calls f with the smallest Shape that holds a row of W channels.
+template <typename F>
+hipError_t with_shape(int W, F f) {
+    if (W <= 512) return f.template operator()<1, 1>();
+    if (W <= 1024) return f.template operator()<1, 2>();
+    if (W <= 2048) return f.template operator()<4, 1>();
+    if (W <= 4096) return f.template operator()<4, 2>();
+    if (W <= 8192) return f.template operator()<8, 2>();
+    return f.template operator()<16, 2>();
+}
+
+bool aligned16(const void *a, const void *b, const void *c, const void *d) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+             reinterpret_cast<uintptr_t>(d)) & 15u) == 0;
+}
+
+template <typename TI, typename TO, bool VEC>
+struct Forward {
+    const LayerNormArgs &a;
+    template <int NW, int K>
+    hipError_t operator()() const {
+        using S = Shape<NW, K>;
+        const unsigned grid = static_cast<unsigned>((a.rows + (long long)S::ROWS - 1) / S::ROWS);
+        hipLaunchKernelGGL((norm_kernel<NW, K, VEC, TI, TO>), dim3(grid), dim3(S::THREADS), 0, a.stream,
+                           static_cast<const TI *>(a.x), a.weight, a.bias, static_cast<TO *>(a.out), a.mean, a.rstd,
+                           a.rows, a.W, a.eps, a.rms);
+        return hipGetLastError();
+    }
+};
+
+template <typename TI, typename TG, bool VEC>
+struct Backward {
+    const LayerNormBackwardArgs &a;
+    template <int NW, int K>
+    hipError_t operator()() const {
+        using S = Shape<NW, K>;
+        const int G = partial_rows(a.rows, S::ROWS);
+        float *dwp = a.dweight ? a.ws : nullptr;
+        float *dbp = a.dbias ? a.ws + (a.dweight ? (size_t)G * a.W : 0) : nullptr;
+        if (G > 0) {
+            hipLaunchKernelGGL((norm_backward_kernel<NW, K, VEC, TI, TG>), dim3(G), dim3(S::THREADS), 0, a.stream,
+                               static_cast<const TI *>(a.x), static_cast<const TG *>(a.dy), a.rms ? nullptr : a.mean,
+                               a.rstd, a.weight, static_cast<TI *>(a.dx), dwp, dbp, a.rows, a.W);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        if (!a.dweight && !a.dbias) return hipSuccess;
+        hipLaunchKernelGGL(column_sum_kernel, dim3((a.W + 63) / 64, 2), dim3(1024), 0, a.stream, dwp, a.dweight, dbp,
+                           a.dbias, G, a.W);
+        return hipGetLastError();
+    }
+};
+
+}  // namespace
+
+size_t layer_norm_backward_workspace(int rows, int W) {
+    // at most 512 partial rows of each gradient, whichever shape is taken
+    return 2 * sizeof(float) * (size_t)partial_rows(rows, 1) * W;
+}
+
+bool layer_norm_fits(int rows, int W) {
+    const unsigned long long threads = W <= 1024 ? 64 : W <= 4096 ? 256 : W <= 8192 ? 512 : 1024;   // per row
+    return ((unsigned long long)rows + 3) * threads < (1ull << 32);
+}
+
+hipError_t launch_layer_norm(const LayerNormArgs &a) {
+    if (a.rows == 0) return hipSuccess;
+    const bool vec = a.W % 8 == 0 && aligned16(a.x, a.out, a.weight, a.bias);
+    auto run = [&](auto in, auto out) {
+        using TI = decltype(in);
+        using TO = decltype(out);
+        return vec ? with_shape(a.W, Forward<TI, TO, true>{a}) : with_shape(a.W, Forward<TI, TO, false>{a});
+    };
+    if (a.x_dt == Dt::F32) return a.out_dt == Dt::F32 ? run(float{}, float{}) : run(float{}, bf16_t{});
+    return a.out_dt == Dt::F32 ? run(bf16_t{}, float{}) : run(bf16_t{}, bf16_t{});
+}
+
+hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs &a) {
+    const bool vec = a.W % 8 == 0 && aligned16(a.x, a.dy, a.dx, a.weight);
+    auto run = [&](auto in, auto grad) {
+        using TI = decltype(in);
+        using TG = decltype(grad);
+        return vec ? with_shape(a.W, Backward<TI, TG, true>{a}) : with_shape(a.W, Backward<TI, TG, false>{a});
+    };
+    if (a.x_dt == Dt::F32) return a.dy_dt == Dt::F32 ? run(float{}, float{}) : run(float{}, bf16_t{});
+    return a.dy_dt == Dt::F32 ? run(bf16_t{}, float{}) : run(bf16_t{}, bf16_t{});
+}
+
+}  // namespace kda

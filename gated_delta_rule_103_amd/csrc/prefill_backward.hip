@@ -1,0 +1,1105 @@
+// prefill_backward.hip -- the gradient of the chunked gated delta rule.
+//
+// Forward, per chunk of C = 64 tokens with start state M = S^T, a the
+// cumulative log-decay inside the chunk, b = beta and
+//     A[t,s] = sum_c k_t k_s exp(a_t - a_s) (s < t),  P[t,s] = sum_c q_t k_s exp(a_t - a_s) (s <= t)
+//     Qd = q exp(a),  Kd = k exp(a),  Kr = k exp(a_last - a),  gam = exp(a_last):
+//     E = (I + A Diag(b))^-1 (V - Kd M),  U = b E,  O = Qd M + P U,  M' = gam M + Kr^T U
+// (E is the error v - S' k of every token). Reverse mode, with dM' the gradient
+// of the state behind the chunk:
+//     Y  = (I + Diag(b) A)^-T (P^T dO + Kr dM'),  dV = b Y,  dbeta = rowsum(Y E)
+//     dM = gam dM' + Qd^T dO - Kd^T dV
+//     dP = tril(dO U^T),  dA = -stril(dV U^T)
+//     dq_t = exp(a_t) (dO M^T)_t + sum_s dP[t,s] exp(a_t - a_s) k_s
+//     dk_t = -exp(a_t) (dV M^T)_t + exp(a_last - a_t) (U dM'^T)_t
+//            + sum_s dA[t,s] exp(a_t - a_s) k_s + sum_s exp(a_s - a_t) (dA[s,t] k_s + dP[s,t] q_s)
+// A decay g_i is passed by everything that joins a token before i to one at or
+// behind it. With row_t = what token t receives (q dq + k dk of the terms that
+// carry +a_t) less what it sends inside the chunk, and out_t = k_t times the
+// Kr term,
+//     dg_i = sum_{t >= i} row_t + sum_{t < i} out_t + gam sum_j M dM'
+// where the s = t terms of P, which no decay touches, stay out of row.
+//
+// Four kernels:
+//   prep    every (chunk, head): P, A, both inverses, Qd, Kd, Kr to a record
+//   scan    every (sequence, head, 16 value channels), once forwards for M and
+//           E and once backwards for dM' and Y. Value channels never meet in
+//           either recurrence, and neither needs the other, so both run in
+//           one launch.
+//   finish  every (chunk, head): all gradients but dS0 from M, dM', E and Y.
+//
+// All products run on fp32 MFMA with fp32 accumulation: gradients arrive in
+// any magnitude, dg is a difference of sums that nearly cancel inside a chunk,
+// and dg and dS0 leave in fp32.
+//
+// Exponents. exp(a_t - a_s) is split where the tokens part in a binary tree over
+// the chunk: blocks of 16, halves of 8, groups of 4. With the border between
+// t's and s's subtrees it is exp(sum from the border to t) exp(sum from s to the
+// border), both summed directly (never as a difference of long sums), so
+// every exponent is <= 0 and good to its own rounding: what is not negligible has
+// a short exponent. Inside a group the three single decays and their products
+// serve. Decays are cut at -104, below which exp is 0 in fp32 (g = -inf wipes a
+// channel).
+//
+// MFMA 16x16x4 operands. Lane l holds A[l % 16][l / 16], B[l / 16][l % 16] and
+// accumulator rows 4 (l / 16) + r of column l % 16. The order of the inner
+// index is free, so four MFMAs take one float4 from each side: MFMA e sums the
+// inner indices 4 (l / 16) + e. An accumulator is then at once a B operand of
+// the next product along its rows, which finish and prep use, and the states
+// and E, Y go to memory as whole accumulators (1 KB per wavefront store) in the
+// order in which finish reads them as operands.
+#include "kda_chunks.h"
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int C = 64, BT = 16, NB = C / BT;   // chunk, block of tokens, blocks
+constexpr int LP = C + 4;                     // LDS row stride of a C x C matrix
+constexpr float MIN_G = -104.f;
+
+__device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 acc) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+    return acc;
+}
+
+// Keeps the computation of x before what follows: without it the compiler sinks
+// whole chains of products towards their uses and holds all their operands.
+__device__ __forceinline__ void settle(f32x4 &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void settle(float &x) { asm volatile("" : "+v"(x)); }
+
+template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
+template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xffff0000u)};
+}
+template <typename T> __device__ __forceinline__ void store4(T *p, f32x4 x);
+template <> __device__ __forceinline__ void store4<float>(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
+template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
+    *reinterpret_cast<uint2 *>(p) = uint2{f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
+                                         f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)};
+}
+__device__ __forceinline__ f32x4 ld4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+// four values `stride` apart
+__device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
+    return f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]};
+}
+
+// What prep leaves for a (chunk, head), in floats.
+template <int D> struct Rec {
+    static constexpr size_t QD = 0, KD = QD + C * D, KR = KD + C * D,   // [C][D]
+        TE = KR + C * D,                                                // (I + A Diag(b))^-1 [C][C]
+        TYT = TE + C * C,                                               // (I + Diag(b) A)^-T [C][C]
+        PT = TYT + C * C,                                               // P^T [C][C]
+        GAM = PT + C * C,                                               // [D]
+        RQ = GAM + D, RK = RQ + C,                                      // 1 / norms of q and k [C]
+        SIZE = RK + C;
+};
+
+typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+
+struct Ws {
+    int32_t *chunk_off;
+    float *rec, *M, *dM, *E, *Y;
+};
+
+struct Common {
+    SeqView sv;
+    Ws ws;
+    const float *g;
+    int H;
+    bool g_head, qk_norm;
+    float norm_eps;
+};
+
+// A (chunk, head) and its tokens: the first one's row of [T_total][H] tensors,
+// rows p.H apart; offsets inside a chunk fit 32 bits.
+struct Item {
+    int Lc;
+    size_t row0;
+    __device__ bool find(const Common &p, size_t item) {
+        const int ci = (int)(item / p.H), h = (int)(item % p.H);
+        if (ci >= p.sv.total_chunks()) return false;
+        const int n = p.sv.seq_of_chunk(ci);
+        const int s0 = p.sv.seq_start(n) + (ci - p.sv.first_chunk(n)) * C;
+        Lc = min(C, p.sv.seq_end(n) - s0);
+        row0 = (size_t)s0 * p.H + h;
+        return true;
+    }
+};
+
+// The rows of one (chunk, head) in a [T_total][H][width] tensor, through a buffer
+// descriptor whose range ends with the chunk's last row: elements of later rows
+// read as 0 and are not written, without a branch. Indices are in elements.
+template <typename T> struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    int row;
+    __device__ Rows(const T *base, const Item &it, int H, int width)
+        : r(buf_rsrc(base ? base + it.row0 * width : nullptr,
+                     base ? ((it.Lc - 1) * H * width + width) * (int)sizeof(T) : 0)),
+          row(H * width) {}
+    __device__ float at(int tau, int c) const {
+        const int off = (tau * row + c) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) return buf_ld_f32(r, off);
+        else return bf16_to_f32(static_cast<bf16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0)));
+    }
+    __device__ f32x4 at4(int tau, int c) const {
+        const int off = (tau * row + c) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) {
+            return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        } else {
+            const auto u = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+            return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u),
+                         __uint_as_float(u[1] << 16), __uint_as_float(u[1] & 0xffff0000u)};
+        }
+    }
+    __device__ void put(int tau, int c, float x) const {
+        const int off = (tau * row + c) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x), r, off, 0, 0);
+    }
+    __device__ void put4(int tau, int c, f32x4 x) const {
+        const int off = (tau * row + c) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32v4, x), r, off, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b64(u32v2{f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
+                                                        f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)},
+                                                  r, off, 0, 0);
+        }
+    }
+};
+
+// Log-decays of a chunk's tokens (0 without a gate and behind the last token).
+struct Decay {
+    Rows<float> g;
+    int col;                  // 1, or 0 for a gate per head
+    __device__ Decay(const Common &p, const Item &it, int D)
+        : g(p.g, it, p.H, p.g_head ? 1 : D), col(p.g_head ? 0 : 1) {}
+    __device__ float at(int tau, int c) const { return fmaxf(g.at(tau, c * col), MIN_G); }
+};
+
+// ---- prep -----------------------------------------------------------------
+
+// The block tiles on and below the diagonal of a lower triangular C x C matrix.
+constexpr int TILES = NB * (NB + 1) / 2, TP = 20;
+typedef float Tile[BT][TP];
+__device__ __forceinline__ constexpr int tile_of(int bi, int bj) { return bi * (bi + 1) / 2 + bj; }
+
+// Thread (blk, c) owns channel c of the 16 tokens of block blk and forms every
+// decay there by itself. The products over channels run half a head (64
+// channels) at a time through the three staging tiles, which keeps two
+// workgroups on a CU.
+template <int D>
+struct PrepLds {
+    float X[3][C][64 + 4];
+    Tile A[TILES], P[TILES];
+    float end[NB][D];                 // log-decay of a whole block
+    float part[D / 16][64];           // in-group products, one row per wavefront
+    float b[C], rq[C], rk[C];
+};
+
+template <int D, typename TI, typename TB>
+__global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p, const TI *__restrict__ q,
+                                                                      const TI *__restrict__ k,
+                                                                      const TB *__restrict__ beta) {
+    using R = Rec<D>;
+    constexpr int THREADS = 4 * D, NW = D / 16, HALVES = D / 64;
+    extern __shared__ char lds_raw[];
+    PrepLds<D> &s = *reinterpret_cast<PrepLds<D> *>(lds_raw);
+    Item it;
+    if (!it.find(p, blockIdx.x)) return;
+    float *rec = p.ws.rec + (size_t)blockIdx.x * R::SIZE;
+    const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
+    const int c = t % D, blk = t / D, ch = c % 64;
+    const Rows<TI> qr(q, it, p.H, D), kr(k, it, p.H, D);
+    const Decay decay(p, it, D);
+
+    float kv[BT], qv[BT], gv[BT];
+#pragma unroll
+    for (int i = 0; i < BT; ++i) {
+        kv[i] = kr.at(blk * BT + i, c);
+        qv[i] = qr.at(blk * BT + i, c);
+        gv[i] = decay.at(blk * BT + i, c);
+    }
+    if (t < C) s.b[t] = Rows<TB>(beta, it, p.H, 1).at(t, 0);
+    for (int i = t; i < TILES * BT * TP; i += THREADS) (&s.A[0][0][0])[i] = (&s.P[0][0][0])[i] = 0.f;
+    if (p.qk_norm) {
+        for (int tau = w; tau < C; tau += NW) {
+            float sq = 0.f, sk = 0.f;
+            for (int i = l; i < D; i += 64) {
+                const float x = qr.at(tau, i), y = kr.at(tau, i);
+                sq += x * x;
+                sk += y * y;
+            }
+            const float rq = 1.f / sqrtf(warp_sum(sq) + p.norm_eps), rk = 1.f / sqrtf(warp_sum(sk) + p.norm_eps);
+            if (l == 0) {
+                rec[R::RQ + tau] = s.rq[tau] = rq;
+                rec[R::RK + tau] = s.rk[tau] = rk;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < BT; ++i) {
+            kv[i] *= s.rk[blk * BT + i];
+            qv[i] *= s.rq[blk * BT + i];
+        }
+    }
+    float G[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) G[j] = (gv[4 * j] + gv[4 * j + 1]) + (gv[4 * j + 2] + gv[4 * j + 3]);
+    s.end[blk][c] = (G[0] + G[1]) + (G[2] + G[3]);
+
+    // Pairs inside groups of four: ten products for P, six for A, summed over the
+    // wavefront's channels. The 16 values of a group are halved lane by lane, so
+    // that lane l ends with the sum of value l % 16.
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int o = 4 * j;
+        const float e10 = __expf(gv[o + 1]), e21 = __expf(gv[o + 2]), e32 = __expf(gv[o + 3]);
+        const float e20 = e21 * e10, e31 = e32 * e21, e30 = e32 * e20;
+        const float k0 = kv[o], k1 = kv[o + 1], k2 = kv[o + 2], k3 = kv[o + 3];
+        const float q1 = qv[o + 1], q2 = qv[o + 2], q3 = qv[o + 3];
+        float v[16] = {qv[o] * k0,      q1 * (e10 * k0), q1 * k1,         q2 * (e20 * k0), q2 * (e21 * k1), q2 * k2,
+                       q3 * (e30 * k0), q3 * (e31 * k1), q3 * (e32 * k2), q3 * k3,         k1 * (e10 * k0), k2 * (e20 * k0),
+                       k2 * (e21 * k1), k3 * (e30 * k0), k3 * (e31 * k1), k3 * (e32 * k2)};
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+            for (int i = 0; i < m; ++i) {
+                const bool up = l & m;
+                const float keep = up ? v[i + m] : v[i], give = up ? v[i] : v[i + m];
+                v[i] = keep + __shfl_xor(give, m, 64);
+            }
+        float x = v[0];
+        x += __shfl_xor(x, 16, 64);
+        x += __shfl_xor(x, 32, 64);
+        settle(x);
+        if (l < 16) s.part[w][16 * j + l] = x;
+    }
+    __syncthreads();
+
+    // block borders: whole blocks before, between and behind
+    float before = 0.f, behind = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const float e = s.end[b][c];
+        before += b < blk ? e : 0.f;
+        behind += b > blk ? e : 0.f;
+    }
+    const float fb = __expf(before), fe = __expf(behind);
+    if (t < 64 * NB) {                                  // in-group products into the diagonal tiles
+        const int b = t / 64, e = t % 16, o = 4 * (l / 16);
+        float x = s.part[b * HALVES][l];
+        if (HALVES == 2) x += s.part[b * HALVES + HALVES - 1][l];
+        const int pr = e < 1 ? 0 : e < 3 ? 1 : e < 6 ? 2 : 3, ar = e < 11 ? 1 : e < 13 ? 2 : 3;
+        if (e < 10) s.P[tile_of(b, b)][o + pr][o + e - pr * (pr + 1) / 2] = x;
+        else s.A[tile_of(b, b)][o + ar][o + e - 10 - ar * (ar - 1) / 2] = x;
+    }
+
+    // Pairs of different blocks: row factor exp(sum from the block's start),
+    // column factor exp(sum to the block's end), whole blocks between on the rows.
+    const __amdgpu_buffer_rsrc_t rr = buf_rsrc(rec, (int)(R::SIZE * sizeof(float)));
+    const int mine = (blk * BT * D + c) * (int)sizeof(float);
+    auto put = [&](size_t at, float x) {                // this thread's channel of a token-major record
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), rr, mine, (int)(at * sizeof(float)), 0);
+    };
+    constexpr int JOBS = (12 + NW - 1) / NW;
+    f32x4 acc[JOBS];
+#pragma unroll
+    for (int i = 0; i < JOBS; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int hf = 0; hf < HALVES; ++hf) {
+        if (hf) __syncthreads();
+        if (c / 64 == hf) {
+            float run = 0.f;
+            settle(run);                                // or both halves' decays are formed ahead of the loop
+#pragma unroll
+            for (int i = 0; i < BT; ++i) {
+                run += gv[i];
+                const float e = __expf(run);
+                const int tau = blk * BT + i;
+                s.X[0][tau][ch] = kv[i] * e;
+                s.X[2][tau][ch] = qv[i] * e;
+                put(R::KD + i * D, kv[i] * e * fb);
+                put(R::QD + i * D, qv[i] * e * fb);
+            }
+            run = 0.f;
+#pragma unroll
+            for (int i = BT - 1; i >= 0; --i) {
+                const float e = __expf(run);
+                const int tau = blk * BT + i;
+                s.X[1][tau][ch] = kv[i] * e;
+                put(R::KR + i * D, kv[i] * e * fe);
+                run += gv[i];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < JOBS; ++i) {
+            const int job = w + i * NW, pr = job >> 1;
+            if (job < 12) {
+                const int bi = pr < 1 ? 1 : pr < 3 ? 2 : 3, bj = pr - bi * (bi - 1) / 2;
+                const float(*rows)[64 + 4] = s.X[job & 1 ? 2 : 0] + 16 * bi, (*cols)[64 + 4] = s.X[1] + 16 * bj;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int x = 16 * kk + 4 * lg;
+                    f32x4 a = ld4(&rows[lr][x]);
+                    if (bi - bj > 1) {
+                        f32x4 f = ld4(&s.end[bj + 1][64 * hf + x]);
+                        if (bi - bj > 2) f += ld4(&s.end[bj + 2][64 * hf + x]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] *= __expf(f[e]);
+                    }
+                    acc[i] = mfma16(a, ld4(&cols[lr][x]), acc[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < JOBS; ++i) {
+        const int job = w + i * NW, pr = job >> 1;
+        if (job < 12) {
+            const int bi = pr < 1 ? 1 : pr < 3 ? 2 : 3, bj = pr - bi * (bi - 1) / 2;
+            Tile &out = job & 1 ? s.P[tile_of(bi, bj)] : s.A[tile_of(bi, bj)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[4 * lg + r][lr] = acc[i][r];
+        }
+    }
+
+    // Pairs of the halves of a block (staging tile 0) and of the group pairs of a
+    // half (tile 1): rows of the later part carry exp(sum from its start), rows
+    // of the earlier exp(sum to its end). One MFMA tile gives A (rows 0-7) and P
+    // (rows 8-15, q in tile 2: later halves, then later groups).
+    constexpr int JOBS2 = 8 / NW;
+    f32x4 acc2[JOBS2];
+#pragma unroll
+    for (int i = 0; i < JOBS2; ++i) acc2[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int hf = 0; hf < HALVES; ++hf) {
+        __syncthreads();
+        if (c / 64 == hf) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float pre[4], suf[4];
+                pre[0] = gv[4 * j];
+                suf[3] = 0.f;
+                settle(pre[0]);
+                settle(suf[3]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + gv[4 * j + i];
+#pragma unroll
+                for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + gv[4 * j + i + 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = 4 * j + i, tau = blk * BT + x;
+                    // within the half: from its start (later half) or to its end (earlier half)
+                    const float e8 = __expf(j == 3 ? G[2] + pre[i] : j == 2 ? pre[i] : j == 1 ? suf[i] : suf[i] + G[1]);
+                    const float e4 = __expf(j & 1 ? pre[i] : suf[i]);
+                    s.X[0][tau][ch] = kv[x] * e8;
+                    s.X[1][tau][ch] = kv[x] * e4;
+                    if (j >= 2) s.X[2][8 * blk + x - 8][ch] = qv[x] * e8;
+                    if (j & 1) s.X[2][32 + 8 * blk + (j >> 1) * 4 + i][ch] = qv[x] * e4;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < JOBS2; ++i) {
+            const int job = w + i * NW, b = job >> 1, four = job & 1, r8 = lr & 7;
+            const int row = four ? (r8 < 4 ? 4 + r8 : 8 + r8) : 8 + r8, col = four ? (r8 < 4 ? r8 : 4 + r8) : r8;
+            const float *rp = lr < 8 ? s.X[four][16 * b + row] : s.X[2][32 * four + 8 * b + r8];
+            const float *cp = s.X[four][16 * b + col];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                acc2[i] = mfma16(ld4(rp + 16 * kk + 4 * lg), ld4(cp + 16 * kk + 4 * lg), acc2[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < JOBS2; ++i) {
+        const int job = w + i * NW, b = job >> 1, four = job & 1;
+        Tile &out = lg < 2 ? s.A[tile_of(b, b)] : s.P[tile_of(b, b)];
+        const int part = lg & 1;                        // rows 0-3 or 4-7 of the later part
+        if (lr < 8 && (!four || (lr >> 2) == part)) {
+            const int row = four ? 4 + 8 * part : 8 + 4 * part, col = four ? (lr < 4 ? lr : 4 + lr) : lr;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[row + r][col] = acc2[i][r];
+        }
+    }
+    __syncthreads();
+
+    // (I + A Diag(b))^-1 in the staging tiles' place: the diagonal blocks by
+    // substitution, one column per lane
+    Tile *X = reinterpret_cast<Tile *>(&s.X[0][0][0]);
+    if (w < NB && l < 16) {
+        const Tile &a = s.A[tile_of(w, w)];
+        Tile &xt = X[tile_of(w, w)];
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == l ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v -= a[i][j] * x[j];
+            xt[i][l] = v;
+            x[i] = v * s.b[16 * w + i];
+        }
+    }
+    __syncthreads();
+    // block row bi, column bj: -X_ii sum_k (A Diag(b))_ik X_kj, by distance from the diagonal
+#pragma unroll 1
+    for (int d = 1; d < NB; ++d) {
+        if (w < NB - d) {
+            const int bj = w, bi = w + d;
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f}, res = sum;
+            for (int bk = bj; bk < bi; ++bk)
+                sum = mfma16(ld4(&s.A[tile_of(bi, bk)][lr][4 * lg]) * ld4(&s.b[16 * bk + 4 * lg]),
+                             ld4s(&X[tile_of(bk, bj)][4 * lg][lr], TP), sum);
+            res = mfma16(ld4(&X[tile_of(bi, bi)][lr][4 * lg]), -sum, res);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) X[tile_of(bi, bj)][4 * lg + r][lr] = res[r];
+        }
+        __syncthreads();
+    }
+    // out: X, and transposed (I + Diag(b) A)^-1 = I - Diag(b) X A and P; blocks
+    // above the diagonal (below it, transposed) are not written and not read
+    for (int i = w; i < TILES; i += NW) {
+        const int bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, bj = i - bi * (bi + 1) / 2;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int bk = bj; bk <= bi; ++bk)
+            sum = mfma16(ld4(&X[tile_of(bi, bk)][lr][4 * lg]), ld4s(&s.A[tile_of(bk, bj)][4 * lg][lr], TP), sum);
+        const int row = 16 * bi + 4 * lg, col = 16 * bj + lr;
+        f32x4 ty;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ty[r] = (row + r == col ? 1.f : 0.f) - s.b[row + r] * sum[r];
+        store4(rec + R::TYT + col * C + row, ty);
+        store4(rec + R::PT + col * C + row, ld4s(&s.P[i][4 * lg][lr], TP));
+        store4(rec + R::TE + (16 * bi + lr) * C + 16 * bj + 4 * lg, ld4(&X[i][lr][4 * lg]));
+    }
+    if (t < D) rec[R::GAM + t] = __expf((s.end[0][t] + s.end[1][t]) + (s.end[2][t] + s.end[3][t]));
+}
+
+// ---- scan -----------------------------------------------------------------
+
+// A workgroup of four wavefronts carries 16 value channels (rows j of S, the
+// accumulators' rows) of one chain; wavefront w owns D / 4 key channels of S
+// and the w-th 16 tokens of a chunk.
+template <int D>
+struct ScanLds {
+    float S[16][D + 4];       // the state, as an A operand
+    float R[16][LP];          // V - Kd M or dU
+    float U[16][LP];          // U or -dV
+    float O[2][16][LP];       // dO^T, two chunks in turn
+};
+
+template <int D, typename TI, typename TB, typename TG>
+__global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__restrict__ v, const TB *__restrict__ beta,
+                                                   const TG *__restrict__ dout, const float *__restrict__ S0,
+                                                   const float *__restrict__ dS_out, float *__restrict__ dS0) {
+    using R = Rec<D>;
+    constexpr int NT = D / 16, CT = D / 64;      // value tiles of a chain, key tiles of a wavefront
+    __shared__ ScanLds<D> s;
+    // the tiles of a chain, which read the same records, run on one XCD
+    // (workgroups go to the eight XCDs in turn)
+    const int slot = blockIdx.x / 8, dir_chain = (slot / NT) * 8 + blockIdx.x % 8, jt = slot % NT;
+    if (dir_chain >= 2 * p.sv.N * p.H) return;
+    const bool back = dir_chain & 1;
+    const int chain = dir_chain >> 1, n = chain / p.H, h = chain % p.H;
+    const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
+    const int j0 = 16 * jt, jr = j0 + 4 * lg;    // this lane's first accumulator row
+    const int begin = p.sv.seq_start(n), len = p.sv.seq_end(n) - begin, chunks = (len + C - 1) / C;
+    const size_t item0 = (size_t)p.sv.first_chunk(n) * p.H + h;
+    auto key = [&](int i) { return (w * CT + i) * 16 + lr; };
+
+    f32x4 st[CT];
+    const float *init = back ? dS_out : S0;
+    const size_t state0 = ((size_t)n * p.H + h) * D;
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[i][r] = init ? init[(state0 + jr + r) * D + key(i)] : 0.f;
+
+    // Operands of a chunk stay in registers from a chunk ahead: each set is
+    // loaded again as soon as its products are done, and the other phases of the
+    // chunk cover the latency.
+    const int tau = 16 * w + lr;                 // this lane's token where tokens are columns
+    auto item_of = [&](int step) { return item0 + (size_t)(back ? chunks - 1 - step : step) * p.H; };
+    auto put_state = [&](size_t item) {
+        float *Mw = (back ? p.ws.dM : p.ws.M) + item * D * D;
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+            store4(Mw + (((w * CT + i) * NT + jt) * 64 + l) * 4, st[i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.S[4 * lg + r][key(i)] = st[i][r];
+        }
+    };
+    auto rows_of = [&](f32x4(&x)[D / 16], const float *m) {           // token rows, all channels
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) x[kk] = ld4(m + tau * D + 16 * kk + 4 * lg);
+    };
+    auto cols_of = [&](f32x4(&x)[CT][NB], const float *m) {           // this wavefront's channels, all tokens
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk) x[i][kk] = ld4s(m + (16 * kk + 4 * lg) * D + key(i), D);
+    };
+    auto gam_of = [&](float(&x)[CT], const float *rec) {
+#pragma unroll
+        for (int i = 0; i < CT; ++i) x[i] = rec[R::GAM + key(i)];
+    };
+    auto beta_of = [&](int step) {
+        const int at = (back ? chunks - 1 - step : step) * C + tau;
+        return at < len ? io<TB>::load(beta, (size_t)(begin + at) * p.H + h) : 0.f;
+    };
+    if (chunks == 0) {
+    } else if (!back) {
+        f32x4 kd[D / 16], te[NB], kr[CT][NB], vt;
+        float b, gam[CT];
+        auto v_of = [&](int step) {
+            const int at = step * C + tau;
+            return at < len ? load4(v + ((size_t)(begin + at) * p.H + h) * D + jr) : f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        auto te_of = [&](const float *rec) {
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk)
+                if (kk <= w) te[kk] = ld4(rec + R::TE + tau * C + 16 * kk + 4 * lg);
+        };
+        {
+            const float *rec = p.ws.rec + item_of(0) * R::SIZE;
+            rows_of(kd, rec + R::KD);
+            vt = v_of(0);
+            te_of(rec);
+            b = beta_of(0);
+            cols_of(kr, rec + R::KR);
+            gam_of(gam, rec);
+        }
+        for (int step = 0; step < chunks; ++step) {
+            const int next = min(step + 1, chunks - 1);
+            const size_t item = item_of(step);
+            const float *rec = p.ws.rec + item_of(next) * R::SIZE;
+            put_state(item);
+            __syncthreads();
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kd[kk], acc);
+            rows_of(kd, rec + R::KD);
+            acc = vt - acc;
+            vt = v_of(next);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.R[4 * lg + r][tau] = acc[r];
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk)
+                if (kk <= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), te[kk], e);
+            te_of(rec);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = b * e[r];
+            store4(p.ws.E + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
+            b = beta_of(next);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                st[i] *= gam[i];
+#pragma unroll
+                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kr[i][kk], st[i]);
+            }
+            cols_of(kr, rec + R::KR);
+            gam_of(gam, rec);
+        }
+    } else {
+        f32x4 kr[D / 16], pt[NB], ty[NB], qd[CT][NB], kd[CT][NB], ov;
+        float b, gam[CT];
+        const int ot = t / 4, oj = (t % 4) * 4;
+        auto o_of = [&](int step) {
+            const int at = (chunks - 1 - step) * C + ot;
+            return at < len ? load4(dout + ((size_t)(begin + at) * p.H + h) * D + j0 + oj) : f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        auto upper_of = [&](f32x4(&x)[NB], const float *m) {
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk)
+                if (kk >= w) x[kk] = ld4(m + tau * C + 16 * kk + 4 * lg);
+        };
+        {
+            const float *rec = p.ws.rec + item_of(0) * R::SIZE;
+            ov = o_of(0);
+            rows_of(kr, rec + R::KR);
+            upper_of(pt, rec + R::PT);
+            cols_of(qd, rec + R::QD);
+            gam_of(gam, rec);
+            upper_of(ty, rec + R::TYT);
+            b = beta_of(0);
+            cols_of(kd, rec + R::KD);
+        }
+        for (int step = 0; step < chunks; ++step) {
+            const int next = min(step + 1, chunks - 1);
+            const size_t item = item_of(step);
+            const float *rec = p.ws.rec + item_of(next) * R::SIZE;
+            float(*O)[LP] = s.O[step & 1];
+            put_state(item);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[oj + r][ot] = ov[r];
+            ov = o_of(next);
+            __syncthreads();
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kr[kk], acc);
+            rows_of(kr, rec + R::KR);
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk)
+                if (kk >= w) acc = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), pt[kk], acc);
+            upper_of(pt, rec + R::PT);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.R[4 * lg + r][tau] = acc[r];
+            // dO's share of the new state waits for nothing
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                st[i] *= gam[i];
+#pragma unroll
+                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), qd[i][kk], st[i]);
+            }
+            cols_of(qd, rec + R::QD);
+            gam_of(gam, rec);
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk)
+                if (kk >= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), ty[kk], e);
+            upper_of(ty, rec + R::TYT);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = -b * e[r];
+            store4(p.ws.Y + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
+            b = beta_of(next);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+#pragma unroll
+                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kd[i][kk], st[i]);
+            cols_of(kd, rec + R::KD);
+        }
+    }
+    if (back && dS0)
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dS0[(state0 + jr + r) * D + key(i)] = st[i][r];
+}
+
+// ---- finish ---------------------------------------------------------------
+
+// D / 16 wavefronts, one for each 16 key channels. LDS tiles O, U, V hold dO,
+// U = b E and dV = b Y as A operands over the value channels: float4 l of
+// (token block, value tile).
+template <int D>
+struct FinishLds {
+    static constexpr int NT = D / 16;
+    float O[C * D], U[C * D], V[C * D];
+    float dP[C][LP], dA[C][LP];       // strictly lower
+    float diag[C];                    // the diagonal of dP
+    float db[C][NT];
+    float rows[2][NT][C];             // sums over a wavefront's channels
+};
+
+template <int D, typename TI, typename TB, typename TG>
+__global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__restrict__ q, const TI *__restrict__ k,
+                                                       const TB *__restrict__ beta, const TG *__restrict__ dout,
+                                                       TI *__restrict__ dq, TI *__restrict__ dk, TI *__restrict__ dv,
+                                                       float *__restrict__ dg, TB *__restrict__ dbeta) {
+    using R = Rec<D>;
+    constexpr int NT = D / 16, THREADS = 4 * D;
+    extern __shared__ char lds_raw[];
+    FinishLds<D> &s = *reinterpret_cast<FinishLds<D> *>(lds_raw);
+    Item it;
+    if (!it.find(p, blockIdx.x)) return;
+    const size_t item = blockIdx.x;
+    const float *rec = p.ws.rec + item * R::SIZE, *M = p.ws.M + item * D * D, *dM = p.ws.dM + item * D * D;
+    const float *E = p.ws.E + item * C * D, *Y = p.ws.Y + item * C * D;
+    const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    const Rows<TI> qr(q, it, p.H, D), kr(k, it, p.H, D), dqr(dq, it, p.H, D), dkr(dk, it, p.H, D), dvr(dv, it, p.H, D);
+    const Rows<TG> dor(dout, it, p.H, D);
+    const Rows<TB> br(beta, it, p.H, 1), dbr(dbeta, it, p.H, 1);
+    const Decay decay(p, it, D);
+
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {                     // wavefront w: value tile w of token block i
+        const int f = ((i * NT + w) * 64 + l) * 4, tau = 16 * i + lr, j = 16 * w + 4 * lg;
+        const f32x4 e = ld4(E + f), y = ld4(Y + f), o = dor.at4(tau, j);
+        const float b = br.at(tau, 0);
+        dvr.put4(tau, j, y * b);
+        store4(&s.O[f], o);
+        store4(&s.U[f], e * b);
+        store4(&s.V[f], y * b);
+        const f32x4 ye = e * y;
+        float x = (ye[0] + ye[1]) + (ye[2] + ye[3]);
+        x += __shfl_xor(x, 16, 64);
+        x += __shfl_xor(x, 32, 64);
+        if (lg == 0) s.db[tau][w] = x;
+    }
+    // q, k and the decays of each block: a lane holds the group lg of its channel
+    const int c = 16 * w + lr;
+    f32x4 qv[NB], kv[NB], gv[NB], ein[NB], eout[NB];
+    float end[NB], grp[NB];                            // the block's and the other group's sum
+    uint32_t wiped = 0;                                // tokens whose decay is 0, of gradient 0
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tau = 16 * b + 4 * lg + r;
+            qv[b][r] = qr.at(tau, c);
+            kv[b][r] = kr.at(tau, c);
+            gv[b][r] = decay.at(tau, c);
+            wiped |= (gv[b][r] <= MIN_G ? 1u : 0u) << (4 * b + r);
+        }
+    }
+    if (p.qk_norm) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            qv[b] *= ld4(rec + R::RQ + 16 * b + 4 * lg);
+            kv[b] *= ld4(rec + R::RK + 16 * b + 4 * lg);
+        }
+    }
+    __syncthreads();
+    if (t < C) {
+        float x = 0.f;
+        for (int i = 0; i < NT; ++i) x += s.db[t][i];
+        dbr.put(t, 0, x);
+    }
+
+    // dP and dA: the ten tiles on and below the diagonal, both matrices
+    for (int job = w; job < 20; job += NT) {
+        const int i = job >> 1, bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, bj = i - bi * (bi + 1) / 2;
+        const float *left = job & 1 ? s.V : s.O;
+        f32x4 acc = zero;
+        for (int kk = 0; kk < NT; ++kk)
+            acc = mfma16(ld4(&left[((bi * NT + kk) * 64 + l) * 4]), ld4(&s.U[((bj * NT + kk) * 64 + l) * 4]), acc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tau = 16 * bi + 4 * lg + r, sig = 16 * bj + lr;
+            if (job & 1) {
+                s.dA[tau][sig] = sig < tau ? -acc[r] : 0.f;
+            } else {
+                s.dP[tau][sig] = sig < tau ? acc[r] : 0.f;
+                if (sig == tau) s.diag[tau] = acc[r];
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const f32x4 g = gv[b];
+        const float own = (g[0] + g[1]) + (g[2] + g[3]);
+        grp[b] = __shfl_xor(own, 16, 64);
+        const float half = own + grp[b], other = __shfl_xor(half, 32, 64);
+        end[b] = half + other;
+        const float in0 = (lg & 1 ? grp[b] : 0.f) + (lg & 2 ? other : 0.f),
+                    out0 = (lg & 1 ? 0.f : grp[b]) + (lg & 2 ? 0.f : other);
+        const f32x4 pre = {g[0], g[0] + g[1], (g[0] + g[1]) + g[2], own};
+        const f32x4 suf = {(g[1] + g[2]) + g[3], g[2] + g[3], g[3], 0.f};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            ein[b][r] = __expf(in0 + pre[r]);          // from the block's start, the token included
+            eout[b][r] = __expf(out0 + suf[r]);        // behind the token to the block's end
+        }
+    }
+    __syncthreads();
+
+    // pairs of tokens of different blocks: what a token receives is scaled by
+    // ein, what it sends by eout, whole blocks between on the operand
+    f32x4 pq[NB], pk[NB], pc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) pq[b] = pk[b] = pc[b] = zero;
+#pragma unroll
+    for (int bi = 1; bi < NB; ++bi) {
+        float between = 0.f;
+#pragma unroll
+        for (int bj = bi - 1; bj >= 0; --bj) {
+            const float f = __expf(between);
+            const f32x4 key = kv[bj] * eout[bj] * f;
+            pq[bi] = mfma16(ld4(&s.dP[16 * bi + lr][16 * bj + 4 * lg]), key, pq[bi]);
+            pk[bi] = mfma16(ld4(&s.dA[16 * bi + lr][16 * bj + 4 * lg]), key, pk[bi]);
+            const f32x4 fe = ein[bi] * f;
+            pc[bj] = mfma16(ld4s(&s.dP[16 * bi + 4 * lg][16 * bj + lr], LP), qv[bi] * fe, pc[bj]);
+            pc[bj] = mfma16(ld4s(&s.dA[16 * bi + 4 * lg][16 * bj + lr], LP), kv[bi] * fe, pc[bj]);
+            between += end[bj];
+            settle(pq[bi]);
+            settle(pk[bi]);
+            settle(pc[bj]);
+        }
+    }
+    // in-block pairs, and the pair terms put together: pq and pk become dq's and
+    // dk's share, pc row's
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        pq[b] *= ein[b];
+        pk[b] *= ein[b];
+        pc[b] *= eout[b];
+        const f32x4 g = gv[b];
+        const f32x4 pre = {g[0], g[0] + g[1], (g[0] + g[1]) + g[2], (g[0] + g[1]) + (g[2] + g[3])};
+        const f32x4 suf = {(g[1] + g[2]) + g[3], g[2] + g[3], g[3], 0.f};
+        // the halves of the block, then the groups of a half: the left operand keeps
+        // only pairs of its level
+#pragma unroll
+        for (int level = 8; level >= 4; level -= 4) {
+            const bool row = level == 8 ? lr >= 8 && lg < 2 : (lr >> 2) == lg + 1 && !(lg & 1);
+            const bool col = level == 8 ? lr < 8 && lg >= 2 : (lr >> 2) + 1 == lg && (lg & 1);
+            const float in0 = level == 8 && (lg & 1) ? grp[b] : 0.f, out0 = level == 8 && !(lg & 1) ? grp[b] : 0.f;
+            f32x4 ei, eo;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                ei[r] = __expf(in0 + pre[r]);
+                eo[r] = __expf(out0 + suf[r]);
+            }
+            const f32x4 prow = ld4(&s.dP[16 * b + lr][16 * b + 4 * lg]), arow = ld4(&s.dA[16 * b + lr][16 * b + 4 * lg]);
+            const f32x4 pcol = ld4s(&s.dP[16 * b + 4 * lg][16 * b + lr], LP),
+                        acol = ld4s(&s.dA[16 * b + 4 * lg][16 * b + lr], LP);
+            const f32x4 key = kv[b] * eo;
+            pq[b] += mfma16(row ? prow : zero, key, zero) * ei;
+            pk[b] += mfma16(row ? arow : zero, key, zero) * ei;
+            pc[b] += mfma16(col ? acol : zero, kv[b] * ei, mfma16(col ? pcol : zero, qv[b] * ei, zero)) * eo;
+            settle(pq[b]);
+            settle(pk[b]);
+            settle(pc[b]);
+        }
+        // inside the group: all in this lane
+        const float e10 = __expf(g[1]), e21 = __expf(g[2]), e32 = __expf(g[3]);
+        const f32x4 ex[3] = {{e10, 0.f, 0.f, 0.f}, {e21 * e10, e21, 0.f, 0.f}, {e32 * e21 * e10, e32 * e21, e32, 0.f}};
+#pragma unroll
+        for (int r = 1; r < 4; ++r) {
+            const f32x4 dp = ld4(&s.dP[16 * b + 4 * lg + r][16 * b + 4 * lg]),
+                        da = ld4(&s.dA[16 * b + 4 * lg + r][16 * b + 4 * lg]);
+#pragma unroll
+            for (int x = 0; x < r; ++x) {
+                const float e = ex[r - 1][x], ek = e * kv[b][x];
+                pq[b][r] += dp[x] * ek;
+                pk[b][r] += da[x] * ek;
+                pc[b][x] += e * (dp[x] * qv[b][r] + da[x] * kv[b][r]);
+            }
+        }
+        const f32x4 dg4 = ld4(&s.diag[16 * b + 4 * lg]), send = pc[b];
+        pc[b] = qv[b] * pq[b] + kv[b] * (pk[b] - send);
+        pq[b] += dg4 * kv[b];
+        pk[b] += send + dg4 * qv[b];
+        settle(pq[b]);
+        settle(pk[b]);
+        settle(pc[b]);
+    }
+
+    // through the states, with the decays from the chunk's start and to its end
+    float before[NB], behind[NB];
+    before[0] = behind[NB - 1] = 0.f;
+#pragma unroll
+    for (int b = 1; b < NB; ++b) {
+        before[b] = before[b - 1] + end[b - 1];
+        behind[NB - 1 - b] = behind[NB - b] + end[NB - b];
+    }
+    f32x4 out[NB];                                     // what a token sends behind the chunk
+    float all;
+    {
+        f32x4 aq[NB], ak[NB], ar[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) aq[b] = ak[b] = ar[b] = zero;
+        float mdm = 0.f;
+#pragma unroll 1
+        for (int jt = 0; jt < NT; ++jt) {
+            const f32x4 m = ld4(M + ((w * NT + jt) * 64 + l) * 4), d = ld4(dM + ((w * NT + jt) * 64 + l) * 4);
+            const f32x4 x = m * d;
+            mdm += (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int f = ((b * NT + jt) * 64 + l) * 4;
+                aq[b] = mfma16(ld4(&s.O[f]), m, aq[b]);
+                ak[b] = mfma16(ld4(&s.V[f]), m, ak[b]);
+                ar[b] = mfma16(ld4(&s.U[f]), d, ar[b]);
+            }
+        }
+        mdm += __shfl_xor(mdm, 16, 64);
+        mdm += __shfl_xor(mdm, 32, 64);
+        all = __expf(before[NB - 1] + end[NB - 1]) * mdm;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const f32x4 fi = ein[b] * __expf(before[b]), fo = eout[b] * __expf(behind[b]);
+            const f32x4 gq = aq[b] * fi, gk = ak[b] * fi, go = ar[b] * fo;
+            pc[b] += qv[b] * gq - kv[b] * gk;
+            out[b] = kv[b] * go;
+            pq[b] += gq;
+            pk[b] += go - gk;
+        }
+    }
+    if (p.qk_norm) {                                   // dx = (dx^ - x^ (x^ . dx^)) / |x|
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x = qv[b][r] * pq[b][r], y = kv[b][r] * pk[b][r];
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) {
+                    x += __shfl_xor(x, m, 64);
+                    y += __shfl_xor(y, m, 64);
+                }
+                if (lr == 0) {
+                    s.rows[0][w][16 * b + 4 * lg + r] = x;
+                    s.rows[1][w][16 * b + 4 * lg + r] = y;
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            f32x4 x = zero, y = zero;
+            for (int i = 0; i < NT; ++i) {
+                x += ld4(&s.rows[0][i][16 * b + 4 * lg]);
+                y += ld4(&s.rows[1][i][16 * b + 4 * lg]);
+            }
+            pq[b] = (pq[b] - qv[b] * x) * ld4(rec + R::RQ + 16 * b + 4 * lg);
+            pk[b] = (pk[b] - kv[b] * y) * ld4(rec + R::RK + 16 * b + 4 * lg);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tau = 16 * b + 4 * lg + r;
+            dqr.put(tau, c, pq[b][r]);
+            dkr.put(tau, c, pk[b][r]);
+        }
+    if (!dg) return;
+    // dg_i = sum_{t >= i} row_t + sum_{t < i} out_t + all
+    float after = 0.f, past = 0.f;
+#pragma unroll
+    for (int b = NB - 1; b >= 0; --b) {                // suffix sums of row
+        f32x4 x = pc[b];
+        x[2] += x[3];
+        x[1] += x[2];
+        x[0] += x[1];
+        const float x0 = __shfl(x[0], lr, 64), x1 = __shfl(x[0], lr + 16, 64), x2 = __shfl(x[0], lr + 32, 64),
+                    x3 = __shfl(x[0], lr + 48, 64);
+        pc[b] = x + (after + (lg == 3 ? 0.f : lg == 2 ? x3 : lg == 1 ? x3 + x2 : (x3 + x2) + x1));
+        after += (x0 + x1) + (x2 + x3);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {                     // prefix sums of out, without the token itself
+        const f32x4 y = out[b];
+        f32x4 x = {0.f, y[0], y[0] + y[1], (y[0] + y[1]) + y[2]};
+        const float tot = x[3] + y[3];
+        const float x0 = __shfl(tot, lr, 64), x1 = __shfl(tot, lr + 16, 64), x2 = __shfl(tot, lr + 32, 64),
+                    x3 = __shfl(tot, lr + 48, 64);
+        pc[b] += x + (past + (lg == 0 ? 0.f : lg == 1 ? x0 : lg == 2 ? x0 + x1 : (x0 + x1) + x2)) + all;
+        past += (x0 + x1) + (x2 + x3);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pc[b][r] = wiped >> (4 * b + r) & 1 ? 0.f : pc[b][r];
+    const Rows<float> dgr(dg, it, p.H, p.g_head ? 1 : D);
+    if (!p.g_head) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dgr.put(16 * b + 4 * lg + r, c, pc[b][r]);
+        return;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float x = pc[b][r];
+#pragma unroll
+            for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m, 64);
+            if (lr == 0) s.rows[0][w][16 * b + 4 * lg + r] = x;
+        }
+    __syncthreads();
+    if (t < C) {
+        float x = 0.f;
+        for (int i = 0; i < NT; ++i) x += s.rows[0][i][t];
+        dgr.put(t, 0, x);
+    }
+}
+
+// ---- host -----------------------------------------------------------------
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D>
+size_t carve(int N, long long T_total, int H, char *base, Ws *ws) {
+    const size_t items = (size_t)max_chunks(N, T_total, C) * H;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *at = base ? base + off : nullptr;
+        off += round256(bytes);
+        return at;
+    };
+    char *plan = take(sizeof(int32_t) * (size_t)(N + 1));
+    float *a[5];
+    const size_t sizes[5] = {Rec<D>::SIZE, (size_t)D * D, (size_t)D * D, (size_t)C * D, (size_t)C * D};
+    for (int i = 0; i < 5; ++i) a[i] = reinterpret_cast<float *>(take(items * sizes[i] * sizeof(float)));
+    if (ws) *ws = Ws{reinterpret_cast<int32_t *>(plan), a[0], a[1], a[2], a[3], a[4]};
+    return off;
+}
+
+template <int D, typename TI, typename TB, typename TG>
+hipError_t launch_t(const PrefillBackwardArgs &a) {
+    Ws ws;
+    carve<D>(a.N, (long long)a.B * a.T, a.H, static_cast<char *>(a.ws), &ws);
+    if (a.cu_seqlens) {
+        const hipError_t e = launch_chunk_plan(a.cu_seqlens, a.N, C, ws.chunk_off, a.stream);
+        if (e != hipSuccess) return e;
+    }
+    const SeqView sv{a.cu_seqlens, ws.chunk_off, a.N, a.T, C};
+    const Common p{sv, ws, a.g, a.H, a.g_head, a.qk_norm, a.norm_eps};
+    const long long chunks = a.cu_seqlens ? max_chunks(a.N, a.T, C) : (long long)a.N * ((a.T + C - 1) / C);
+    const unsigned items = static_cast<unsigned>(chunks * a.H);
+    const TI *q = static_cast<const TI *>(a.q), *k = static_cast<const TI *>(a.k), *v = static_cast<const TI *>(a.v);
+    const TB *beta = static_cast<const TB *>(a.beta);
+    const TG *dout = static_cast<const TG *>(a.dout);
+    const auto prep = prep_kernel<D, TI, TB>;
+    const auto finish = finish_kernel<D, TI, TB, TG>;
+    // set on every call (idempotent; no process-wide flag to race on)
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(prep),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(PrepLds<D>));
+    if (e != hipSuccess) return e;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(finish), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            sizeof(FinishLds<D>));
+    if (e != hipSuccess) return e;
+    if (items > 0) {
+        hipLaunchKernelGGL(prep, dim3(items), dim3(4 * D), sizeof(PrepLds<D>), a.stream, p, q, k, beta);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const unsigned chains = static_cast<unsigned>(2 * a.N * a.H), groups = (chains + 7) / 8;
+    hipLaunchKernelGGL((scan_kernel<D, TI, TB, TG>), dim3(groups * 8 * (D / 16)), dim3(256), 0, a.stream, p, v, beta,
+                       dout, a.S0, a.dS_out, a.dS0);
+    e = hipGetLastError();
+    if (e != hipSuccess || items == 0) return e;
+    hipLaunchKernelGGL(finish, dim3(items), dim3(4 * D), sizeof(FinishLds<D>), a.stream, p, q, k, beta, dout,
+                       static_cast<TI *>(a.dq), static_cast<TI *>(a.dk), static_cast<TI *>(a.dv), a.dg,
+                       static_cast<TB *>(a.dbeta));
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const PrefillBackwardArgs &a) {
+    if (a.io == Dt::F32) return launch_t<D, float, float, float>(a);
+    if (a.beta_dt == Dt::F32)
+        return a.dout_dt == Dt::F32 ? launch_t<D, bf16_t, float, float>(a) : launch_t<D, bf16_t, float, bf16_t>(a);
+    return a.dout_dt == Dt::F32 ? launch_t<D, bf16_t, bf16_t, float>(a) : launch_t<D, bf16_t, bf16_t, bf16_t>(a);
+}
+
+}  // namespace
+
+size_t prefill_backward_workspace(int N, long long T_total, int H, int Dk) {
+    return Dk == 64 ? carve<64>(N, T_total, H, nullptr, nullptr) : carve<128>(N, T_total, H, nullptr, nullptr);
+}
+
+bool prefill_backward_fits(int N, long long T_total, int H, int Dk) {
+    // a launch has fewer than 2^32 threads
+    const unsigned long long items = (unsigned long long)max_chunks(N, T_total, C) * H;
+    const unsigned long long scans = (2ull * N * H + 7) * (Dk / 16);
+    // and one chunk of a tensor at most 2^31 bytes (offsets inside it have 32 bits)
+    return items * 512 < (1ull << 32) && scans * 256 < (1ull << 32) && (unsigned long long)H * Dk * C * 4 < (1ull << 31);
+}
+
+hipError_t launch_prefill_backward(const PrefillBackwardArgs &a) { return a.Dk == 64 ? launch_d<64>(a) : launch_d<128>(a); }
+
+}  // namespace kda

@@ -80,6 +80,23 @@ def load_library() -> ctypes.CDLL:
     lib.kda_decode_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, op, vp]
     lib.kda_output_gate.restype = i
     lib.kda_output_gate.argtypes = [vp, vp, vp, vp, i, i, i, ctypes.c_float, i, i, i, vp]
+    f = ctypes.c_float
+    lib.kda_recurrent.restype = i
+    lib.kda_recurrent.argtypes = [vp] * 10 + [i] * 9 + [op, vp]
+    lib.kda_prefill_backward_workspace_size.restype = sz
+    lib.kda_prefill_backward_workspace_size.argtypes = [i] * 5
+    lib.kda_prefill_backward.restype = i
+    lib.kda_prefill_backward.argtypes = [vp] * 15 + [i] * 9 + [op, vp, sz, vp]
+    lib.kda_output_gate_backward_workspace_size.restype = sz
+    lib.kda_output_gate_backward_workspace_size.argtypes = [i] * 3
+    lib.kda_output_gate_backward.restype = i
+    lib.kda_output_gate_backward.argtypes = [vp] * 7 + [i, i, i, f, i, i, i, vp, sz, vp]
+    lib.kda_layer_norm.restype = i
+    lib.kda_layer_norm.argtypes = [vp] * 6 + [i, i, f, i, i, i, vp]
+    lib.kda_layer_norm_backward_workspace_size.restype = sz
+    lib.kda_layer_norm_backward_workspace_size.argtypes = [i] * 2
+    lib.kda_layer_norm_backward.restype = i
+    lib.kda_layer_norm_backward.argtypes = [vp] * 8 + [i] * 5 + [vp, sz, vp]
     _lib = lib
     return lib
 
@@ -366,3 +383,245 @@ def kda_output_gate(o, gate, weight=None, *, eps: float = 1e-6, out=None,
     if st != 0:
         raise KDAError(st, "kda_output_gate")
     return out
+
+
+def _workspace(need: int, workspace, device):
+    """The caller's workspace, or one of ``need`` bytes."""
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel()
+
+
+def _expect_workspace(workspace):
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.dim() != 1 or
+                                  workspace.dtype != torch.uint8):
+        raise ValueError("workspace must be a 1-D uint8 tensor")
+
+
+def _recurrent(entry, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream, qk_l2norm,
+               l2norm_eps):
+    lib = load_library()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q must be [T, H, Dk] and v [T, H, Dv]")
+    T, H, Dk = q.shape
+    Dv = v.shape[-1]
+    _expect(q, "q", (T, H, Dk), _FLOAT_IO)
+    _expect(k, "k", (T, H, Dk), (q.dtype,))
+    _expect(v, "v", (T, H, Dv), (q.dtype,))
+    g_head = entry == "gdn_recurrent"
+    if g_head:
+        _expect(g, "g", (T, H), (torch.float32,), optional=True)
+    else:
+        _expect(g, "g", (T, H, Dk), (torch.float32,))
+    _expect(beta, "beta", (T, H), _FLOAT_IO)
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        raise ValueError("S must be a pool of states [slots, H, Dv, Dk]")
+    _expect(S, "S", (S.shape[0], H, Dv, Dk), (torch.float32,))
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
+    N = cu_seqlens.numel() - 1
+    _expect(cu_seqlens, "cu_seqlens", (N + 1,), (torch.int32,))
+    _expect(slot_in, "slot_in", (N,), (torch.int32,), optional=True)
+    _expect(slot_out, "slot_out", (T,), (torch.int32,), optional=True)
+    _expect(out, "out", (T, H, Dv), _FLOAT_IO, optional=True)
+    dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, S=S, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out,
+                    out=out)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(T, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
+        opt = Options(gate=GATE_HEAD if g_head else GATE_CHANNEL, qk_l2norm=int(qk_l2norm), l2norm_eps=l2norm_eps)
+        st = lib.kda_recurrent(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(out), _ptr(cu_seqlens),
+                               _ptr(slot_in), _ptr(slot_out), N, T, H, Dk, Dv, S.shape[0], _dt(q), _dt(beta),
+                               _dt(out), ctypes.byref(opt), _stream(stream, dev))
+    if st != 0:
+        raise KDAError(st, entry)
+    return out
+
+
+def kda_recurrent(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, *, out=None,
+                  out_dtype: Optional[torch.dtype] = None, stream=None, qk_l2norm: bool = False,
+                  l2norm_eps: float = 1e-6):
+    """The recurrence over a few tokens per sequence, states in a pool of slots.
+    q, k, g: [T, H, Dk]; v: [T, H, Dv]; beta: [T, H], packed by cu_seqlens (int32 [N+1]);
+    S: [slots, H, Dv, Dk] fp32. slot_in (int32 [N], or None): the slot a sequence starts from,
+    negative = the zero state; slot_out (int32 [T], or None): the slot that receives the state
+    after a token, negative = none. All index tensors on the device. Returns out [T, H, Dv];
+    rows of tokens in no sequence are not written."""
+    return _recurrent("kda_recurrent", q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream,
+                      qk_l2norm, l2norm_eps)
+
+
+def gdn_recurrent(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, *, out=None,
+                  out_dtype: Optional[torch.dtype] = None, stream=None, qk_l2norm: bool = False,
+                  l2norm_eps: float = 1e-6):
+    """kda_recurrent with the scalar gate of Gated DeltaNet: g [T, H] fp32, or None
+    for DeltaNet (no decay)."""
+    return _recurrent("gdn_recurrent", q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream,
+                      qk_l2norm, l2norm_eps)
+
+
+def kda_prefill_backward_workspace_size(N: int, T_total: int, H: int, Dk: int, Dv: int) -> int:
+    return int(load_library().kda_prefill_backward_workspace_size(N, T_total, H, Dk, Dv))
+
+
+def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq, dk, dv, dg, dbeta, dS0, workspace,
+                      stream, qk_l2norm, l2norm_eps):
+    lib = load_library()
+    g_head = entry == "gdn_prefill_backward"
+    _check_prefill(q, k, v, g, beta, S0, None, dS_out, cu_seqlens, workspace, g_head)
+    B, T, H, Dk = q.shape
+    Dv = v.shape[-1]
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _expect(dout, "dout", (B, T, H, Dv), _FLOAT_IO)
+    for name, grad, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dbeta", dbeta, beta)):
+        _expect(grad, name, like.shape, (like.dtype,), optional=True)
+    if g is None:
+        if dg is not None:
+            raise ValueError("dg must be None when there is no gate")
+    else:
+        _expect(dg, "dg", g.shape, (torch.float32,), optional=True)
+    _expect(dS0, "dS0", (N, H, Dv, Dk), (torch.float32,), optional=True)
+    dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, dout=dout, S0=S0, dS_out=dS_out, cu_seqlens=cu_seqlens, dq=dq,
+                    dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0, workspace=workspace)
+    with torch.cuda.device(dev):
+        dq, dk, dv, dbeta = (torch.empty_like(like) if x is None else x
+                             for x, like in ((dq, q), (dk, k), (dv, v), (dbeta, beta)))
+        if dg is None and g is not None:
+            dg = torch.empty_like(g)
+        if dS0 is None and S0 is not None:
+            dS0 = torch.empty_like(S0)
+        workspace, ws_bytes = _workspace(kda_prefill_backward_workspace_size(N, B * T, H, Dk, Dv), workspace, dev)
+        opt = Options(gate=GATE_HEAD if g_head else GATE_CHANNEL, qk_l2norm=int(qk_l2norm), l2norm_eps=l2norm_eps)
+        st = lib.kda_prefill_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(S0),
+                                      _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dS0),
+                                      _ptr(cu_seqlens), N, B, T, H, Dk, Dv, _dt(q), _dt(beta), _dt(dout),
+                                      ctypes.byref(opt), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if st != 0:
+        raise KDAError(st, entry)
+    return dq, dk, dv, dg, dbeta, dS0
+
+
+def kda_prefill_backward(q, k, v, g, beta, dout, S0=None, dS_out=None, *, cu_seqlens=None, dq=None, dk=None, dv=None,
+                         dg=None, dbeta=None, dS0=None, workspace=None, stream=None, qk_l2norm: bool = False,
+                         l2norm_eps: float = 1e-6):
+    """The gradient of kda_prefill: q, k, v, g, beta, S0 and cu_seqlens as given to it, dout
+    [B, T, H, Dv] the gradient of out and dS_out [N, H, Dv, Dk] that of S_out (None: zero).
+    Returns (dq, dk, dv, dg, dbeta, dS0), each of its input's dtype and shape; dS0 is None
+    when neither S0 nor a buffer for it is given."""
+    return _prefill_backward("kda_prefill_backward", q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq, dk, dv, dg,
+                             dbeta, dS0, workspace, stream, qk_l2norm, l2norm_eps)
+
+
+def gdn_prefill_backward(q, k, v, g, beta, dout, S0=None, dS_out=None, *, cu_seqlens=None, dq=None, dk=None, dv=None,
+                         dg=None, dbeta=None, dS0=None, workspace=None, stream=None, qk_l2norm: bool = False,
+                         l2norm_eps: float = 1e-6):
+    """The gradient of gdn_prefill: g and dg [B, T, H] fp32, or None for DeltaNet (no decay).
+    Otherwise as kda_prefill_backward."""
+    return _prefill_backward("gdn_prefill_backward", q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq, dk, dv, dg,
+                             dbeta, dS0, workspace, stream, qk_l2norm, l2norm_eps)
+
+
+def kda_output_gate_backward(o, gate, dout, weight=None, *, eps: float = 1e-6, do=None, dgate=None, dweight=None,
+                             workspace=None, stream=None):
+    """The gradient of kda_output_gate: o, gate, weight and eps as given to it, dout [..., H, Dv]
+    the gradient of its out. Returns (do, dgate, dweight), of the dtypes of o, gate and weight;
+    dweight is None when neither weight nor a buffer for it is given."""
+    lib = load_library()
+    if not isinstance(o, torch.Tensor) or o.dim() < 2:
+        raise ValueError("o must be a tensor [..., H, Dv]")
+    _expect(o, "o", o.shape, _FLOAT_IO)
+    _expect(gate, "gate", o.shape, _FLOAT_IO)
+    _expect(dout, "dout", o.shape, _FLOAT_IO)
+    H, Dv = o.shape[-2], o.shape[-1]
+    rows = o.numel() // (H * Dv) if o.numel() else 0
+    _expect(weight, "weight", (Dv,), (torch.float32,), optional=True)
+    _expect(do, "do", o.shape, (o.dtype,), optional=True)
+    _expect(dgate, "dgate", o.shape, (gate.dtype,), optional=True)
+    _expect(dweight, "dweight", (Dv,), (torch.float32,), optional=True)
+    _expect_workspace(workspace)
+    dev = _same_gpu(o=o, gate=gate, dout=dout, weight=weight, do=do, dgate=dgate, dweight=dweight, workspace=workspace)
+    with torch.cuda.device(dev):
+        do = torch.empty_like(o) if do is None else do
+        dgate = torch.empty_like(gate) if dgate is None else dgate
+        if dweight is None and weight is not None:
+            dweight = torch.empty_like(weight)
+        need = 0 if dweight is None else int(lib.kda_output_gate_backward_workspace_size(rows, H, Dv))
+        workspace, ws_bytes = _workspace(need, workspace, dev)
+        st = lib.kda_output_gate_backward(_ptr(o), _ptr(gate), _ptr(dout), _ptr(weight), _ptr(do), _ptr(dgate),
+                                          _ptr(dweight), rows, H, Dv, float(eps), _dt(o), _dt(gate), _dt(dout),
+                                          _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if st != 0:
+        raise KDAError(st, "kda_output_gate_backward")
+    return do, dgate, dweight
+
+
+def _norm_rows(x):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be a tensor [..., W]")
+    _expect(x, "x", x.shape, _FLOAT_IO)
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def kda_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False, out=None,
+                   out_dtype: Optional[torch.dtype] = None, mean=None, rstd=None, stream=None):
+    """Layer norm over the last axis, or with ``rms`` the RMS norm (no mean): x [..., W], weight
+    and bias [W] fp32 or None. ``out`` may be ``x`` itself when the dtypes match. Returns
+    (out, mean, rstd), the statistics fp32 [...] for the backward pass; mean is None for RMS."""
+    lib = load_library()
+    rows, W = _norm_rows(x)
+    _expect(weight, "weight", (W,), (torch.float32,), optional=True)
+    _expect(bias, "bias", (W,), (torch.float32,), optional=True)
+    _expect(out, "out", x.shape, _FLOAT_IO, optional=True)
+    if rms and mean is not None:
+        raise ValueError("an RMS norm has no mean")
+    _expect(mean, "mean", x.shape[:-1], (torch.float32,), optional=True)
+    _expect(rstd, "rstd", x.shape[:-1], (torch.float32,), optional=True)
+    dev = _same_gpu(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        if mean is None and not rms:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        st = lib.kda_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd), rows, W,
+                                float(eps), int(rms), _dt(x), _dt(out), _stream(stream, dev))
+    if st != 0:
+        raise KDAError(st, "kda_layer_norm")
+    return out, mean, rstd
+
+
+def kda_layer_norm_backward(x, dy, mean, rstd, weight=None, *, bias: bool = False, rms: bool = False, dx=None,
+                            dweight=None, dbias=None, workspace=None, stream=None):
+    """The gradient of kda_layer_norm from dy [..., W], with its x and weight and the mean and
+    rstd that it returned (mean None for RMS). ``bias``: there was one, its gradient is wanted.
+    Returns (dx, dweight, dbias); dweight is None when neither weight nor a buffer for it is
+    given, dbias when neither ``bias`` nor a buffer is."""
+    lib = load_library()
+    rows, W = _norm_rows(x)
+    _expect(dy, "dy", x.shape, _FLOAT_IO)
+    if rms and mean is not None:
+        raise ValueError("an RMS norm has no mean")
+    _expect(mean, "mean", x.shape[:-1], (torch.float32,), optional=rms)
+    _expect(rstd, "rstd", x.shape[:-1], (torch.float32,))
+    _expect(weight, "weight", (W,), (torch.float32,), optional=True)
+    _expect(dx, "dx", x.shape, (x.dtype,), optional=True)
+    _expect(dweight, "dweight", (W,), (torch.float32,), optional=True)
+    _expect(dbias, "dbias", (W,), (torch.float32,), optional=True)
+    _expect_workspace(workspace)
+    dev = _same_gpu(x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dweight, dbias=dbias,
+                    workspace=workspace)
+    with torch.cuda.device(dev):
+        dx = torch.empty_like(x) if dx is None else dx
+        if dweight is None and weight is not None:
+            dweight = torch.empty_like(weight)
+        if dbias is None and bias:
+            dbias = torch.empty(W, dtype=torch.float32, device=x.device)
+        need = 0 if dweight is None and dbias is None else int(lib.kda_layer_norm_backward_workspace_size(rows, W))
+        workspace, ws_bytes = _workspace(need, workspace, dev)
+        st = lib.kda_layer_norm_backward(_ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
+                                         _ptr(dweight), _ptr(dbias), rows, W, int(rms), _dt(x), _dt(dy),
+                                         _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if st != 0:
+        raise KDAError(st, "kda_layer_norm_backward")
+    return dx, dweight, dbias

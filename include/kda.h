@@ -317,6 +317,133 @@ int kda_output_gate(const void *o, const void *gate, const float *weight, void *
                     int Dv, float eps, kda_dtype o_dtype, kda_dtype gate_dtype, kda_dtype out_dtype,
                     void *stream);
 
+/*
+ * kda_recurrent -- the recurrence over a few tokens of each sequence, with the
+ * states in a pool of slots: checking draft tokens (the state after every one
+ * is kept, and decoding goes on from the accepted one), continuing a shared
+ * prefix without copying its state, or a step of ragged length per sequence.
+ *
+ *   q, k   [T_total][H][Dk] io_dtype      v    [T_total][H][Dv] io_dtype
+ *   g      [T_total][H][Dk] fp32, or with opt->gate == KDA_GATE_HEAD
+ *          [T_total][H], NULL = no decay
+ *   beta   [T_total][H] beta_dtype        out  [T_total][H][Dv] out_dtype
+ *   S      [slots][H][Dv][Dk] fp32, the pool, 16-byte aligned
+ *   cu_seqlens  int32 [N+1]: sequence n is tokens cu_seqlens[n] up to
+ *          cu_seqlens[n+1]. It may be empty; out rows (and states) of tokens
+ *          that belong to no sequence are left as they were. Offsets outside
+ *          [0, T_total] are cut to it.
+ *   slot_in   int32 [N]: the slot a sequence starts from; a value outside
+ *          [0, slots), or slot_in NULL: the zero state
+ *   slot_out  int32 [T_total]: the slot that receives the state after a token;
+ *          outside [0, slots), or slot_out NULL: that state is not kept
+ * cu_seqlens, slot_in and slot_out are device arrays. A sequence may keep a
+ * state in the slot it started from (in place), and several sequences may start
+ * from one slot. A slot that one sequence writes must not be the start, nor be
+ * written by, another sequence of the call: those contents are undefined (no
+ * fault). Slots that no token names are not written. If one sequence names a
+ * slot for several tokens, the last one stays.
+ *
+ * Arithmetic in fp32. opt: gate and qk_l2norm as for kda_decode_ex; snapshots
+ * must be NULL; opt may be NULL. Support: Dk == Dv in {64, 128}; N * H * Dk^2 / 16
+ * below 2^32. q, k, v, a per-channel g, S and out 16-byte aligned; out must be none
+ * of the other buffers. T_total == 0 launches nothing.
+ */
+int kda_recurrent(const void *q, const void *k, const void *v, const float *g, const void *beta, float *S,
+                  void *out, const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N,
+                  int T_total, int H, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype,
+                  kda_dtype out_dtype, const kda_options *opt, void *stream);
+
+/*
+ * kda_prefill_backward -- the gradient of kda_prefill (and, with
+ * opt->gate == KDA_GATE_HEAD, of gdn_prefill; with qk_l2norm, through the
+ * normalisation): from dout, the gradient of out, and dS_out, the gradient of
+ * S_out, to those of every input. Nothing of the forward call is needed: the
+ * states at the chunk borders are computed again.
+ *
+ *   q, k, v, g, beta, S0, cu_seqlens, N, B, T, H, Dk, Dv  as for kda_prefill
+ *   dout    [T_total][H][Dv] dout_dtype
+ *   dS_out  [N][H][Dv][Dk] fp32, or NULL: the final state has no gradient
+ *   dq, dk  [T_total][H][Dk], dv [T_total][H][Dv]   io_dtype
+ *   dg      fp32, g's layout; NULL exactly when g is
+ *   dbeta   [T_total][H] beta_dtype
+ *   dS0     [N][H][Dv][Dk] fp32, or NULL to skip it (S0 may be NULL, a zero state)
+ * Rows of tokens behind the last sequence of a packed batch are left as they
+ * were. A sequence of length zero gives dS0 = dS_out.
+ *
+ * Arithmetic, states and their gradients in fp32 (fp32 matrix instructions), for
+ * any magnitude of dout; a bf16 gradient is the rounded fp32 value. g = -inf has
+ * gradient 0. Results repeat bit for bit.
+ * Support: Dk == Dv in {64, 128}; io_dtype KDA_F32 with fp32 beta and dout, or
+ * KDA_BF16 with either; (T_total / 64 + N + 1) * H below 2^23. opt->snapshots
+ * must be NULL; opt may be NULL. All tensors but beta, dbeta and a per-head g, dg
+ * must be 16-byte aligned. No gradient may be any other buffer of the call.
+ * workspace: kda_prefill_backward_workspace_size bytes (about 340 KB per
+ * 64 tokens and head at Dk = 128, 140 KB at 64), 256-byte aligned, its contents
+ * ignored, not used by anything else until the call's work has finished.
+ * The size function returns 0 for sizes that the call rejects.
+ */
+size_t kda_prefill_backward_workspace_size(int N, int T_total, int H, int Dk, int Dv);
+int kda_prefill_backward(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                         const void *dout, const float *S0, const float *dS_out, void *dq, void *dk, void *dv,
+                         float *dg, void *dbeta, float *dS0, const int32_t *cu_seqlens, int N, int B, int T, int H,
+                         int Dk, int Dv, kda_dtype io_dtype, kda_dtype beta_dtype, kda_dtype dout_dtype,
+                         const kda_options *opt, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_output_gate_backward -- the gradient of kda_output_gate. With
+ * r = 1 / sqrt(mean_j o_j^2 + eps), n = o r, s = sigmoid(z) and x = dout s w:
+ *     d_o = r (x - n mean_j(x n)),  dgate = dout n w s (1 - s),
+ *     dweight = sum over rows and heads of dout s n
+ *   o, gate, weight, rows, H, Dv, eps  as for kda_output_gate
+ *   dout [rows][H][Dv] dout_dtype;  d_o o_dtype;  dgate gate_dtype
+ *   dweight [Dv] fp32, or NULL to skip it (weight may be NULL, ones)
+ * fp32 arithmetic; dweight's sum has a fixed order. rows == 0 gives dweight = 0.
+ * No gradient may be any other buffer of the call. Alignment, support and errors
+ * as for kda_output_gate. workspace: kda_output_gate_backward_workspace_size bytes
+ * (at most 1 MiB), 256-byte aligned; may be NULL when dweight is.
+ */
+size_t kda_output_gate_backward_workspace_size(int rows, int H, int Dv);
+int kda_output_gate_backward(const void *o, const void *gate, const void *dout, const float *weight, void *d_o,
+                             void *dgate, float *dweight, int rows, int H, int Dv, float eps, kda_dtype o_dtype,
+                             kda_dtype gate_dtype, kda_dtype dout_dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * kda_layer_norm -- the block's input norm: layer norm of every row of W
+ * channels, or its RMS norm (rms nonzero):
+ *     mean = sum_c x_c / W (0 for RMS),  rstd = 1 / sqrt(sum_c (x_c - mean)^2 / W + eps)
+ *     out_c = (x_c - mean) rstd weight_c + bias_c
+ *   x    [rows][W] x_dtype;  out [rows][W] out_dtype, may be x itself when the
+ *        dtypes are the same
+ *   weight, bias  [W] fp32; NULL = ones, zeros
+ *   mean, rstd    [rows] fp32, kept for the backward pass; NULL to skip (mean
+ *        must be NULL for RMS)
+ *   eps  > 0
+ * fp32 arithmetic; the variance is the mean square of centred values. Any W from 1
+ * to 16384 (above: KDA_ERR_UNSUPPORTED) and any alignment of the element type;
+ * fastest with W a multiple of 8 and 16-byte aligned x, out, weight and bias. Up
+ * to 4,194,300 rows (16,777,200 up to W = 4096). rows == 0 launches nothing.
+ */
+int kda_layer_norm(const void *x, const float *weight, const float *bias, void *out, float *mean, float *rstd,
+                   int rows, int W, float eps, int rms, kda_dtype x_dtype, kda_dtype out_dtype, void *stream);
+
+/*
+ * kda_layer_norm_backward -- its gradient. With n = (x - mean) rstd and h = dy weight:
+ *     dx = rstd (h - n mean_c(h n) - mean_c(h))      (RMS: without the last term)
+ *     dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ *   mean, rstd  as kda_layer_norm left them (mean NULL for RMS)
+ *   dy [rows][W] dy_dtype;  dx [rows][W] x_dtype
+ *   dweight, dbias  [W] fp32, or NULL to skip
+ * The sums over rows have a fixed order. rows == 0 gives zeros. No gradient may be
+ * any other buffer of the call. Sizes and alignment as for kda_layer_norm.
+ * workspace: kda_layer_norm_backward_workspace_size bytes (at most 8 KiB x W),
+ * 256-byte aligned; may be NULL when dweight and dbias are.
+ */
+size_t kda_layer_norm_backward_workspace_size(int rows, int W);
+int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, const float *rstd, const float *weight,
+                            void *dx, float *dweight, float *dbias, int rows, int W, int rms, kda_dtype x_dtype,
+                            kda_dtype dy_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
