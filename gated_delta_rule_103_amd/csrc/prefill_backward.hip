@@ -52,6 +52,8 @@
 #include "kda_device.h"
 #include "kda_launch.h"
 
+#include <type_traits>
+
 namespace kda {
 namespace {
 
@@ -63,6 +65,22 @@ __device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 acc) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
     return acc;
+}
+
+// x of another lane of the same 16: lane 15 - i, 7 - i (in its eight), i ^ 2, i ^ 1
+template <int M> __device__ __forceinline__ float lane_across(float x) {
+    constexpr int ctrl = M == 8 ? 0x140 : M == 4 ? 0x141 : M == 2 ? 0x4e : 0xb1;
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), ctrl, 0xf, 0xf, true));
+}
+// One step of summing 2 M values over 16 lanes: each lane keeps M of them, those
+// of its bit M, and adds what the lane across kept for it.
+template <int M> __device__ __forceinline__ void halve(float *v, int lane) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const bool up = lane & M;
+        const float keep = up ? v[i + M] : v[i], give = up ? v[i] : v[i + M];
+        v[i] = keep + lane_across<M>(give);
+    }
 }
 
 // Keeps the computation of x before what follows: without it the compiler sinks
@@ -143,21 +161,33 @@ template <typename T> struct Rows {
         : r(buf_rsrc(base ? base + it.row0 * width : nullptr,
                      base ? ((it.Lc - 1) * H * width + width) * (int)sizeof(T) : 0)),
           row(H * width) {}
-    __device__ float at(int tau, int c) const {
+    // one element and four as they are in memory, for a load that is used later
+    typedef std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t> Raw;
+    typedef std::conditional_t<sizeof(T) == 4, u32v4, u32v2> Raw4;
+    __device__ Raw raw(int tau, int c) const {
         const int off = (tau * row + c) * (int)sizeof(T);
-        if constexpr (sizeof(T) == 4) return buf_ld_f32(r, off);
-        else return bf16_to_f32(static_cast<bf16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0)));
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
     }
-    __device__ f32x4 at4(int tau, int c) const {
+    __device__ Raw4 raw4(int tau, int c) const {
         const int off = (tau * row + c) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    }
+    __device__ static float value(Raw u) {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(u);
+        else return bf16_to_f32(u);
+    }
+    __device__ static f32x4 value4(Raw4 u) {
         if constexpr (sizeof(T) == 4) {
-            return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+            return __builtin_bit_cast(f32x4, u);
         } else {
-            const auto u = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
             return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u),
                          __uint_as_float(u[1] << 16), __uint_as_float(u[1] & 0xffff0000u)};
         }
     }
+    __device__ float at(int tau, int c) const { return value(raw(tau, c)); }
+    __device__ f32x4 at4(int tau, int c) const { return value4(raw4(tau, c)); }
     __device__ void put(int tau, int c, float x) const {
         const int off = (tau * row + c) * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
@@ -200,7 +230,6 @@ struct PrepLds {
     float X[3][C][64 + 4];
     Tile A[TILES], P[TILES];
     float end[NB][D];                 // log-decay of a whole block
-    float part[D / 16][64];           // in-group products, one row per wavefront
     float b[C], rq[C], rk[C];
 };
 
@@ -255,6 +284,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     for (int j = 0; j < 4; ++j) G[j] = (gv[4 * j] + gv[4 * j + 1]) + (gv[4 * j + 2] + gv[4 * j + 3]);
     s.end[blk][c] = (G[0] + G[1]) + (G[2] + G[3]);
 
+    float(*part)[64] = reinterpret_cast<float(*)[64]>(&s.X[0][0][0]);    // one row per wavefront
     // Pairs inside groups of four: ten products for P, six for A, summed over the
     // wavefront's channels. The 16 values of a group are halved lane by lane, so
     // that lane l ends with the sum of value l % 16.
@@ -268,19 +298,15 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         float v[16] = {qv[o] * k0,      q1 * (e10 * k0), q1 * k1,         q2 * (e20 * k0), q2 * (e21 * k1), q2 * k2,
                        q3 * (e30 * k0), q3 * (e31 * k1), q3 * (e32 * k2), q3 * k3,         k1 * (e10 * k0), k2 * (e20 * k0),
                        k2 * (e21 * k1), k3 * (e30 * k0), k3 * (e31 * k1), k3 * (e32 * k2)};
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-            for (int i = 0; i < m; ++i) {
-                const bool up = l & m;
-                const float keep = up ? v[i + m] : v[i], give = up ? v[i] : v[i + m];
-                v[i] = keep + __shfl_xor(give, m, 64);
-            }
+        halve<8>(v, l);
+        halve<4>(v, l);
+        halve<2>(v, l);
+        halve<1>(v, l);
         float x = v[0];
         x += __shfl_xor(x, 16, 64);
         x += __shfl_xor(x, 32, 64);
         settle(x);
-        if (l < 16) s.part[w][16 * j + l] = x;
+        if (l < 16) part[w][16 * j + l] = x;
     }
     __syncthreads();
 
@@ -295,8 +321,8 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     const float fb = __expf(before), fe = __expf(behind);
     if (t < 64 * NB) {                                  // in-group products into the diagonal tiles
         const int b = t / 64, e = t % 16, o = 4 * (l / 16);
-        float x = s.part[b * HALVES][l];
-        if (HALVES == 2) x += s.part[b * HALVES + HALVES - 1][l];
+        float x = part[b * HALVES][l];
+        if (HALVES == 2) x += part[b * HALVES + HALVES - 1][l];
         const int pr = e < 1 ? 0 : e < 3 ? 1 : e < 6 ? 2 : 3, ar = e < 11 ? 1 : e < 13 ? 2 : 3;
         if (e < 10) s.P[tile_of(b, b)][o + pr][o + e - pr * (pr + 1) / 2] = x;
         else s.A[tile_of(b, b)][o + ar][o + e - 10 - ar * (ar - 1) / 2] = x;
@@ -315,7 +341,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     for (int i = 0; i < JOBS; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int hf = 0; hf < HALVES; ++hf) {
-        if (hf) __syncthreads();
+        __syncthreads();
         if (c / 64 == hf) {
             float run = 0.f;
             settle(run);                                // or both halves' decays are formed ahead of the loop
@@ -503,12 +529,13 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
     using R = Rec<D>;
     constexpr int NT = D / 16, CT = D / 64;      // value tiles of a chain, key tiles of a wavefront
     __shared__ ScanLds<D> s;
-    // the tiles of a chain, which read the same records, run on one XCD
-    // (workgroups go to the eight XCDs in turn)
-    const int slot = blockIdx.x / 8, dir_chain = (slot / NT) * 8 + blockIdx.x % 8, jt = slot % NT;
-    if (dir_chain >= 2 * p.sv.N * p.H) return;
-    const bool back = dir_chain & 1;
-    const int chain = dir_chain >> 1, n = chain / p.H, h = chain % p.H;
+    // The tiles of a chain, which read the same records, run on one XCD (workgroups
+    // go to the eight XCDs in turn); the backward scans, which are longer, come first.
+    const int per_dir = gridDim.x / 16, slot = blockIdx.x / 8, jt = slot % NT;
+    const bool back = slot < per_dir;
+    const int chain = (back ? slot : slot - per_dir) / NT * 8 + blockIdx.x % 8;
+    if (chain >= p.sv.N * p.H) return;
+    const int n = chain / p.H, h = chain % p.H;
     const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
     const int j0 = 16 * jt, jr = j0 + 4 * lg;    // this lane's first accumulator row
     const int begin = p.sv.seq_start(n), len = p.sv.seq_end(n) - begin, chunks = (len + C - 1) / C;
@@ -551,18 +578,18 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
         for (int i = 0; i < CT; ++i) x[i] = rec[R::GAM + key(i)];
     };
-    auto beta_of = [&](int step) {
-        const int at = (back ? chunks - 1 - step : step) * C + tau;
-        return at < len ? io<TB>::load(beta, (size_t)(begin + at) * p.H + h) : 0.f;
+    auto chunk_of = [&](int step) {
+        const int ci = back ? chunks - 1 - step : step;
+        return Item{min(C, len - ci * C), (size_t)(begin + ci * C) * p.H + h};
     };
+    auto beta_of = [&](const Item &it) { return Rows<TB>(beta, it, p.H, 1).raw(tau, 0); };
     if (chunks == 0) {
     } else if (!back) {
-        f32x4 kd[D / 16], te[NB], kr[CT][NB], vt;
-        float b, gam[CT];
-        auto v_of = [&](int step) {
-            const int at = step * C + tau;
-            return at < len ? load4(v + ((size_t)(begin + at) * p.H + h) * D + jr) : f32x4{0.f, 0.f, 0.f, 0.f};
-        };
+        f32x4 kd[D / 16], te[NB], kr[CT][NB];
+        float gam[CT];
+        typename Rows<TI>::Raw4 vt;
+        typename Rows<TB>::Raw b;
+        auto v_of = [&](const Item &it) { return Rows<TI>(v, it, p.H, D).raw4(tau, jr); };
         auto te_of = [&](const float *rec) {
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
@@ -571,14 +598,16 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
             rows_of(kd, rec + R::KD);
-            vt = v_of(0);
+            const Item it = chunk_of(0);
+            vt = v_of(it);
             te_of(rec);
-            b = beta_of(0);
+            b = beta_of(it);
             cols_of(kr, rec + R::KR);
             gam_of(gam, rec);
         }
         for (int step = 0; step < chunks; ++step) {
             const int next = min(step + 1, chunks - 1);
+            const Item it = chunk_of(next);
             const size_t item = item_of(step);
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
             put_state(item);
@@ -587,8 +616,8 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kd[kk], acc);
             rows_of(kd, rec + R::KD);
-            acc = vt - acc;
-            vt = v_of(next);
+            acc = Rows<TI>::value4(vt) - acc;
+            vt = v_of(it);
 #pragma unroll
             for (int r = 0; r < 4; ++r) s.R[4 * lg + r][tau] = acc[r];
             __syncthreads();
@@ -597,9 +626,9 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
                 if (kk <= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), te[kk], e);
             te_of(rec);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = b * e[r];
+            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = Rows<TB>::value(b) * e[r];
             store4(p.ws.E + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
-            b = beta_of(next);
+            b = beta_of(it);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
@@ -611,13 +640,12 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             gam_of(gam, rec);
         }
     } else {
-        f32x4 kr[D / 16], pt[NB], ty[NB], qd[CT][NB], kd[CT][NB], ov;
-        float b, gam[CT];
+        f32x4 kr[D / 16], pt[NB], ty[NB], qd[CT][NB], kd[CT][NB];
+        float gam[CT];
+        typename Rows<TG>::Raw4 ov;
+        typename Rows<TB>::Raw b;
         const int ot = t / 4, oj = (t % 4) * 4;
-        auto o_of = [&](int step) {
-            const int at = (chunks - 1 - step) * C + ot;
-            return at < len ? load4(dout + ((size_t)(begin + at) * p.H + h) * D + j0 + oj) : f32x4{0.f, 0.f, 0.f, 0.f};
-        };
+        auto o_of = [&](const Item &it) { return Rows<TG>(dout, it, p.H, D).raw4(ot, j0 + oj); };
         auto upper_of = [&](f32x4(&x)[NB], const float *m) {
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
@@ -625,24 +653,26 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         };
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
-            ov = o_of(0);
+            const Item it = chunk_of(0);
+            ov = o_of(it);
             rows_of(kr, rec + R::KR);
             upper_of(pt, rec + R::PT);
             cols_of(qd, rec + R::QD);
             gam_of(gam, rec);
             upper_of(ty, rec + R::TYT);
-            b = beta_of(0);
+            b = beta_of(it);
             cols_of(kd, rec + R::KD);
         }
         for (int step = 0; step < chunks; ++step) {
             const int next = min(step + 1, chunks - 1);
+            const Item it = chunk_of(next);
             const size_t item = item_of(step);
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
             float(*O)[LP] = s.O[step & 1];
             put_state(item);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) O[oj + r][ot] = ov[r];
-            ov = o_of(next);
+            for (int r = 0; r < 4; ++r) O[oj + r][ot] = Rows<TG>::value4(ov)[r];
+            ov = o_of(it);
             __syncthreads();
             f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
 #pragma unroll
@@ -669,9 +699,9 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
                 if (kk >= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), ty[kk], e);
             upper_of(ty, rec + R::TYT);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = -b * e[r];
+            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = -Rows<TB>::value(b) * e[r];
             store4(p.ws.Y + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
-            b = beta_of(next);
+            b = beta_of(it);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < CT; ++i)
@@ -1067,8 +1097,8 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const unsigned chains = static_cast<unsigned>(2 * a.N * a.H), groups = (chains + 7) / 8;
-    hipLaunchKernelGGL((scan_kernel<D, TI, TB, TG>), dim3(groups * 8 * (D / 16)), dim3(256), 0, a.stream, p, v, beta,
+    const unsigned groups = (static_cast<unsigned>(a.N * a.H) + 7) / 8;
+    hipLaunchKernelGGL((scan_kernel<D, TI, TB, TG>), dim3(2 * groups * 8 * (D / 16)), dim3(256), 0, a.stream, p, v, beta,
                        dout, a.S0, a.dS_out, a.dS0);
     e = hipGetLastError();
     if (e != hipSuccess || items == 0) return e;
@@ -1095,7 +1125,7 @@ size_t prefill_backward_workspace(int N, long long T_total, int H, int Dk) {
 bool prefill_backward_fits(int N, long long T_total, int H, int Dk) {
     // a launch has fewer than 2^32 threads
     const unsigned long long items = (unsigned long long)max_chunks(N, T_total, C) * H;
-    const unsigned long long scans = (2ull * N * H + 7) * (Dk / 16);
+    const unsigned long long scans = 2 * ((unsigned long long)N * H + 7) * (Dk / 16);
     // and one chunk of a tensor at most 2^31 bytes (offsets inside it have 32 bits)
     return items * 512 < (1ull << 32) && scans * 256 < (1ull << 32) && (unsigned long long)H * Dk * C * 4 < (1ull << 31);
 }
