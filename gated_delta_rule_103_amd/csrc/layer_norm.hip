@@ -24,6 +24,8 @@
 #include "kda_launch.h"
 #include "kda_vec8.h"
 
+#include <type_traits>
+
 namespace kda {
 namespace {
 
@@ -130,48 +132,105 @@ __global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_kernel(const TI 
     }
 }
 
-// part: [gridDim.x][W] of dw, then the same of db (a pointer is null when that
-// gradient is not wanted)
+// One group of eight channels as it lies in memory, so that a row can be loaded
+// ahead in half the registers.
+template <bool VEC, typename T> struct Group {
+    typedef std::conditional_t<sizeof(T) == 4, f32x8, u32x4> Packed;
+    std::conditional_t<VEC, Packed, f32x8> u;
+    __device__ void load(const T *row, int c, int step, int W) {
+        if constexpr (VEC) u = c < W ? *reinterpret_cast<const Packed *>(row + c) : Packed{};
+        else u = load8<false>(row, c, step, W);
+    }
+    __device__ f32x8 value() const {
+        if constexpr (!VEC || sizeof(T) == 4) {
+            return u;
+        } else {
+            f32x8 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+            return x;
+        }
+    }
+};
+
+// dw_part, db_part: [gridDim.x][W], null when that gradient is not wanted. The next
+// row is loaded while the current one is reduced; both of a row's sums cross the
+// wavefronts together, through slots that alternate, so a row takes one barrier.
 template <int NW, int K, bool VEC, typename TI, typename TG>
 __global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_backward_kernel(
     const TI *__restrict__ x, const TG *__restrict__ dy, const float *__restrict__ mean_in,
     const float *__restrict__ rstd_in, const float *__restrict__ w, TI *__restrict__ dx, float *__restrict__ dw_part,
     float *__restrict__ db_part, int rows, int W) {
     using S = Shape<NW, K>;
-    __shared__ float part[NW], part2[NW];
+    __shared__ float part[2][2][NW];
     __shared__ float fold[S::ROWS > 1 ? (S::ROWS - 1) * S::MAX_W : 1];
     const int t = threadIdx.x % S::SPAN, wave = t / 64, rg = threadIdx.x / S::SPAN;
     constexpr int STEP = VEC ? 1 : S::SPAN;
-    f32x8 dw[K] = {}, db[K] = {};
+    f32x8 dw[K] = {}, db[K] = {}, wv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        wv[k] = w ? load8<VEC>(w, first_channel<VEC, S::SPAN>(t, k), STEP, W) : f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
     const float inv = 1.f / W;
+    const long long stride = (long long)gridDim.x * S::ROWS;
+    Group<VEC, TI> xn[K];
+    Group<VEC, TG> dn[K];
+    float mean_n = 0.f, rstd_n = 0.f;
+    auto fetch = [&](long long r) {
+        if (r >= rows) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = first_channel<VEC, S::SPAN>(t, k);
+            xn[k].load(x + (size_t)r * W, c, STEP, W);
+            dn[k].load(dy + (size_t)r * W, c, STEP, W);
+        }
+        mean_n = mean_in ? mean_in[r] : 0.f;
+        rstd_n = rstd_in[r];
+    };
     // NW > 1: one row per pass, so every thread makes the same number of passes
-    for (long long r = (long long)blockIdx.x * S::ROWS + rg; r < rows; r += (long long)gridDim.x * S::ROWS) {
-        const TI *row = x + (size_t)r * W;
-        const TG *drow = dy + (size_t)r * W;
-        const float mean = mean_in ? mean_in[r] : 0.f, rstd = rstd_in[r];
+    long long r = (long long)blockIdx.x * S::ROWS + rg;
+    fetch(r);
+    for (int turn = 0; r < rows; r += stride, turn ^= 1) {
+        const float mean = mean_n, rstd = rstd_n;
         f32x8 n[K], h[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            n[k] = xn[k].value();
+            h[k] = dn[k].value();
+        }
+        fetch(r + stride);
         float shn = 0.f, sh = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = first_channel<VEC, S::SPAN>(t, k);
-            n[k] = load8<VEC>(row, c, STEP, W);
-            h[k] = load8<VEC>(drow, c, STEP, W);
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = first_channel<VEC, S::SPAN>(t, k);
             n[k] = (n[k] - mean) * rstd;       // past the row's end: h is 0 there
             dw[k] += h[k] * n[k];
             db[k] += h[k];
-            if (w) h[k] *= load8<VEC>(w, c, STEP, W);
+            h[k] *= wv[k];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 shn += h[k][i] * n[k][i];
                 sh += h[k][i];
             }
         }
-        shn = row_sum<NW>(shn, part, wave) * inv;
-        sh = mean_in ? row_sum<NW>(sh, part2, wave) * inv : 0.f;
+        shn = warp_sum(shn);
+        if (mean_in) sh = warp_sum(sh);        // uniform
+        if constexpr (NW > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                part[turn][0][wave] = shn;
+                part[turn][1][wave] = sh;
+            }
+            __syncthreads();
+            shn = sh = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                shn += part[turn][0][i];
+                sh += part[turn][1][i];
+            }
+        }
+        shn *= inv;
+        sh = mean_in ? sh * inv : 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             store8<VEC>(dx + (size_t)r * W, first_channel<VEC, S::SPAN>(t, k), STEP, W,
@@ -191,7 +250,6 @@ __global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_backward_kernel(
                 for (int k = 0; k < K; ++k)
                     a[k] += *reinterpret_cast<f32x8 *>(&fold[g * S::MAX_W + (k * S::SPAN + t) * 8]);
         }
-        // whole partial rows of MAX_W floats would waste traffic: W floats, laid out as the row is
 #pragma unroll
         for (int k = 0; k < K; ++k)
             store8<VEC>(out + (size_t)blockIdx.x * W, first_channel<VEC, S::SPAN>(t, k), STEP, W, a[k]);
@@ -211,8 +269,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
     if (!out) return;
     const int c = blockIdx.x * 64 + (threadIdx.x & 63), j = threadIdx.x >> 6;
     float x = 0.f;
-    if (c < W)
+    if (c < W) {
+#pragma unroll 8
         for (int g = j; g < G; g += 16) x += p[(size_t)g * W + c];
+    }
     s[j][threadIdx.x & 63] = x;
     __syncthreads();
     if (j == 0 && c < W) {

@@ -82,18 +82,20 @@ __global__ __launch_bounds__(THREADS) void output_gate_backward_kernel(
     }
 }
 
-// dw[c] = sum over the G partial rows, 1024 / Dv threads per channel
-template <int DV>
-__global__ __launch_bounds__(1024) void dweight_kernel(const float *__restrict__ part, float *__restrict__ dw, int G) {
-    constexpr int J = 1024 / DV;
-    __shared__ float s[J][DV];
-    const int c = threadIdx.x % DV, j = threadIdx.x / DV;
+// dw[c] = sum over the G partial rows: a workgroup takes 16 channels in 64 strands,
+// each adding every 64th row, then adds the strands in a fixed order.
+constexpr int DW_CH = 16, DW_STRANDS = 64;
+__global__ __launch_bounds__(DW_CH *DW_STRANDS) void dweight_kernel(const float *__restrict__ part,
+                                                                   float *__restrict__ dw, int G, int Dv) {
+    __shared__ float s[DW_STRANDS][DW_CH + 1];
+    const int ch = threadIdx.x % DW_CH, j = threadIdx.x / DW_CH, c = blockIdx.x * DW_CH + ch;
     float x = 0.f;
-    for (int g = j; g < G; g += J) x += part[(size_t)g * DV + c];
-    s[j][c] = x;
+#pragma unroll 8
+    for (int g = j; g < G; g += DW_STRANDS) x += part[(size_t)g * Dv + c];
+    s[j][ch] = x;
     __syncthreads();
     if (j == 0) {
-        for (int i = 1; i < J; ++i) x += s[i][c];
+        for (int i = 1; i < DW_STRANDS; ++i) x += s[i][ch];
         dw[c] = x;
     }
 }
@@ -117,7 +119,7 @@ hipError_t launch_t(const OutputGateBackwardArgs &a) {
         if (e != hipSuccess) return e;
     }
     if (!a.dweight) return hipSuccess;
-    hipLaunchKernelGGL(dweight_kernel<DV>, dim3(1), dim3(1024), 0, a.stream, a.ws, a.dweight, G);
+    hipLaunchKernelGGL(dweight_kernel, dim3(DV / DW_CH), dim3(DW_CH * DW_STRANDS), 0, a.stream, a.ws, a.dweight, G, DV);
     return hipGetLastError();
 }
 

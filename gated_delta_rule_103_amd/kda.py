@@ -8,6 +8,7 @@ library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -109,8 +110,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+# torch's own short cut to the current stream's handle (a Stream object takes 2 us to make)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> Optional[int]:
     if stream is None:
+        if _current_raw_stream is not None and device.index is not None:
+            return _current_raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -126,7 +133,7 @@ def _expect(t, name, shape, dtypes, optional=False):
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
@@ -135,19 +142,27 @@ def _expect(t, name, shape, dtypes, optional=False):
 def _same_gpu(**tensors) -> torch.device:
     """Every given tensor is a contiguous GPU tensor on one device; returns that device.
     Checked after shapes and dtypes, so that those errors are reported on any device."""
-    dev = None
+    first, index = None, -1
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor (libkda reads device memory), got {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+        if first is None:
+            first, index = t, t.get_device()
+        elif t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {first.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    return dev
+    return None if first is None else first.device
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(dev):
+    """Makes ``dev`` current for a with block; costs nothing where it is already."""
+    return _HERE_ALREADY if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -221,7 +236,7 @@ def _prefill(entry, q, k, v, g, beta, S0, out, S_out, cu_seqlens, C, out_dtype, 
              return_state, qk_l2norm=False, l2norm_eps=1e-6):
     lib = load_library()
     dev = _check_prefill(q, k, v, g, beta, S0, out, S_out, cu_seqlens, workspace, entry == "gdn_prefill")
-    with torch.cuda.device(dev):
+    with _on(dev):
         (B, T, H, Dk, Dv, N), out, S_out, workspace, ws_bytes = _prefill_buffers(
             lib, q, v, beta, cu_seqlens, C, out, S_out, out_dtype, workspace, return_state)
         args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(out), _ptr(S_out),
@@ -264,7 +279,7 @@ def kda_prefill_noalloc(q, k, v, g, beta, S0=None, *, out=None, S_out=None, cu_s
         out = torch.empty(B, T, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
     if S_out is None and return_state:
         S_out = torch.empty(N, H, Dv, Dk, dtype=torch.float32, device=q.device)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib.kda_prefill_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(out),
                                      _ptr(S_out), _ptr(cu_seqlens), N, B, T, H, Dk, Dv, C, _dt(q), _dt(beta),
                                      _dt(out), _stream(stream, dev))
@@ -299,7 +314,7 @@ def kda_prefill_snapshots(q, k, v, g, beta, S0=None, *, snapshot_every: int, max
                                dtype=torch.float32, device=q.device)
     dev = _check_prefill(q, k, v, g, beta, S0, out, S_out, cu_seqlens, workspace, False, snapshots,
                          max_snapshots)
-    with torch.cuda.device(dev):
+    with _on(dev):
         (B, T, H, Dk, Dv, N), out, S_out, workspace, ws_bytes = _prefill_buffers(
             lib, q, v, beta, cu_seqlens, C, out, S_out, out_dtype, workspace, return_state)
         st = lib.kda_prefill_snapshots(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(out),
@@ -332,7 +347,7 @@ def _decode(entry, q, k, v, g, beta, S, out, out_dtype, stream, qk_l2norm=False,
         out = torch.empty(N, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(out), N, H, Dk, Dv, _dt(q),
             _dt(beta), _dt(out))
-    with torch.cuda.device(dev):
+    with _on(dev):
         if qk_l2norm:
             opt = Options(gate=GATE_HEAD if entry == "gdn_decode" else GATE_CHANNEL, qk_l2norm=1,
                           l2norm_eps=l2norm_eps)
@@ -377,12 +392,26 @@ def kda_output_gate(o, gate, weight=None, *, eps: float = 1e-6, out=None,
     dev = _same_gpu(o=o, gate=gate, weight=weight, out=out)
     if out is None:
         out = torch.empty(o.shape, dtype=out_dtype or o.dtype, device=o.device)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib.kda_output_gate(_ptr(o), _ptr(gate), _ptr(weight), _ptr(out), rows, H, Dv, float(eps),
                                  _dt(o), _dt(gate), _dt(out), _stream(stream, dev))
     if st != 0:
         raise KDAError(st, "kda_output_gate")
     return out
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    """Address of a tensor that _same_gpu has passed (contiguous) or that was allocated here."""
+    return None if t is None else t.data_ptr()
+
+
+_OPTIONS = (Options(gate=GATE_CHANNEL), Options(gate=GATE_HEAD))     # without normalisation; never written
+
+
+def _options(g_head: bool, qk_l2norm: bool, l2norm_eps: float):
+    if not qk_l2norm:
+        return ctypes.byref(_OPTIONS[g_head])
+    return ctypes.byref(Options(gate=GATE_HEAD if g_head else GATE_CHANNEL, qk_l2norm=1, l2norm_eps=l2norm_eps))
 
 
 def _workspace(need: int, workspace, device):
@@ -426,13 +455,12 @@ def _recurrent(entry, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, o
     _expect(out, "out", (T, H, Dv), _FLOAT_IO, optional=True)
     dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, S=S, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out,
                     out=out)
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty(T, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
-        opt = Options(gate=GATE_HEAD if g_head else GATE_CHANNEL, qk_l2norm=int(qk_l2norm), l2norm_eps=l2norm_eps)
-        st = lib.kda_recurrent(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(out), _ptr(cu_seqlens),
-                               _ptr(slot_in), _ptr(slot_out), N, T, H, Dk, Dv, S.shape[0], _dt(q), _dt(beta),
-                               _dt(out), ctypes.byref(opt), _stream(stream, dev))
+        st = lib.kda_recurrent(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(S), _at(out), _at(cu_seqlens),
+                               _at(slot_in), _at(slot_out), N, T, H, Dk, Dv, S.shape[0], _dt(q), _dt(beta),
+                               _dt(out), _options(g_head, qk_l2norm, l2norm_eps), _stream(stream, dev))
     if st != 0:
         raise KDAError(st, entry)
     return out
@@ -483,7 +511,7 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
     _expect(dS0, "dS0", (N, H, Dv, Dk), (torch.float32,), optional=True)
     dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, dout=dout, S0=S0, dS_out=dS_out, cu_seqlens=cu_seqlens, dq=dq,
                     dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         dq, dk, dv, dbeta = (torch.empty_like(like) if x is None else x
                              for x, like in ((dq, q), (dk, k), (dv, v), (dbeta, beta)))
         if dg is None and g is not None:
@@ -491,11 +519,10 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
         if dS0 is None and S0 is not None:
             dS0 = torch.empty_like(S0)
         workspace, ws_bytes = _workspace(kda_prefill_backward_workspace_size(N, B * T, H, Dk, Dv), workspace, dev)
-        opt = Options(gate=GATE_HEAD if g_head else GATE_CHANNEL, qk_l2norm=int(qk_l2norm), l2norm_eps=l2norm_eps)
-        st = lib.kda_prefill_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(S0),
-                                      _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dS0),
-                                      _ptr(cu_seqlens), N, B, T, H, Dk, Dv, _dt(q), _dt(beta), _dt(dout),
-                                      ctypes.byref(opt), _ptr(workspace), ws_bytes, _stream(stream, dev))
+        st = lib.kda_prefill_backward(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(dout), _at(S0),
+                                      _at(dS_out), _at(dq), _at(dk), _at(dv), _at(dg), _at(dbeta), _at(dS0),
+                                      _at(cu_seqlens), N, B, T, H, Dk, Dv, _dt(q), _dt(beta), _dt(dout),
+                                      _options(g_head, qk_l2norm, l2norm_eps), _at(workspace), ws_bytes, _stream(stream, dev))
     if st != 0:
         raise KDAError(st, entry)
     return dq, dk, dv, dg, dbeta, dS0
@@ -540,16 +567,16 @@ def kda_output_gate_backward(o, gate, dout, weight=None, *, eps: float = 1e-6, d
     _expect(dweight, "dweight", (Dv,), (torch.float32,), optional=True)
     _expect_workspace(workspace)
     dev = _same_gpu(o=o, gate=gate, dout=dout, weight=weight, do=do, dgate=dgate, dweight=dweight, workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         do = torch.empty_like(o) if do is None else do
         dgate = torch.empty_like(gate) if dgate is None else dgate
         if dweight is None and weight is not None:
             dweight = torch.empty_like(weight)
         need = 0 if dweight is None else int(lib.kda_output_gate_backward_workspace_size(rows, H, Dv))
         workspace, ws_bytes = _workspace(need, workspace, dev)
-        st = lib.kda_output_gate_backward(_ptr(o), _ptr(gate), _ptr(dout), _ptr(weight), _ptr(do), _ptr(dgate),
-                                          _ptr(dweight), rows, H, Dv, float(eps), _dt(o), _dt(gate), _dt(dout),
-                                          _ptr(workspace), ws_bytes, _stream(stream, dev))
+        st = lib.kda_output_gate_backward(_at(o), _at(gate), _at(dout), _at(weight), _at(do), _at(dgate),
+                                          _at(dweight), rows, H, Dv, float(eps), _dt(o), _dt(gate), _dt(dout),
+                                          _at(workspace), ws_bytes, _stream(stream, dev))
     if st != 0:
         raise KDAError(st, "kda_output_gate_backward")
     return do, dgate, dweight
@@ -577,14 +604,14 @@ def kda_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = 
     _expect(mean, "mean", x.shape[:-1], (torch.float32,), optional=True)
     _expect(rstd, "rstd", x.shape[:-1], (torch.float32,), optional=True)
     dev = _same_gpu(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
         if mean is None and not rms:
             mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         if rstd is None:
             rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        st = lib.kda_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd), rows, W,
+        st = lib.kda_layer_norm(_at(x), _at(weight), _at(bias), _at(out), _at(mean), _at(rstd), rows, W,
                                 float(eps), int(rms), _dt(x), _dt(out), _stream(stream, dev))
     if st != 0:
         raise KDAError(st, "kda_layer_norm")
@@ -611,7 +638,7 @@ def kda_layer_norm_backward(x, dy, mean, rstd, weight=None, *, bias: bool = Fals
     _expect_workspace(workspace)
     dev = _same_gpu(x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dweight, dbias=dbias,
                     workspace=workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         dx = torch.empty_like(x) if dx is None else dx
         if dweight is None and weight is not None:
             dweight = torch.empty_like(weight)
@@ -619,9 +646,9 @@ def kda_layer_norm_backward(x, dy, mean, rstd, weight=None, *, bias: bool = Fals
             dbias = torch.empty(W, dtype=torch.float32, device=x.device)
         need = 0 if dweight is None and dbias is None else int(lib.kda_layer_norm_backward_workspace_size(rows, W))
         workspace, ws_bytes = _workspace(need, workspace, dev)
-        st = lib.kda_layer_norm_backward(_ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
-                                         _ptr(dweight), _ptr(dbias), rows, W, int(rms), _dt(x), _dt(dy),
-                                         _ptr(workspace), ws_bytes, _stream(stream, dev))
+        st = lib.kda_layer_norm_backward(_at(x), _at(dy), _at(mean), _at(rstd), _at(weight), _at(dx),
+                                         _at(dweight), _at(dbias), rows, W, int(rms), _dt(x), _dt(dy),
+                                         _at(workspace), ws_bytes, _stream(stream, dev))
     if st != 0:
         raise KDAError(st, "kda_layer_norm_backward")
     return dx, dweight, dbias
