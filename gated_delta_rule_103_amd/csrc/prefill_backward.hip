@@ -60,6 +60,9 @@ namespace {
 constexpr int C = 64, BT = 16, NB = C / BT;   // chunk, block of tokens, blocks
 constexpr int LP = C + 4;                     // LDS row stride of a C x C matrix
 constexpr float MIN_G = -104.f;
+// the block tiles on and below the diagonal of a lower triangular C x C matrix
+constexpr int TILES = NB * (NB + 1) / 2;
+__device__ __forceinline__ constexpr int tile_of(int bi, int bj) { return bi * (bi + 1) / 2 + bj; }
 
 __device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 acc) {
 #pragma unroll
@@ -107,13 +110,18 @@ __device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
     return f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]};
 }
 
-// What prep leaves for a (chunk, head), in floats.
+// What prep leaves for a (chunk, head), in floats. Operands lie in the order in
+// which the scans load them, 1 KB per wavefront and instruction:
+//   R (rows):    float4 l of (token block, 16 channels): token l % 16, channels 4 (l / 16) + 0..3
+//   T (columns): float4 l of (16 channels, token block): channel l % 16, tokens 4 (l / 16) + 0..3
+//   lower triangular C x C matrices: the ten tiles on and below the diagonal,
+//   float4 l: row l % 16, columns 4 (l / 16) + 0..3, or transposed the reverse
 template <int D> struct Rec {
-    static constexpr size_t QD = 0, KD = QD + C * D, KR = KD + C * D,   // [C][D]
-        TE = KR + C * D,                                                // (I + A Diag(b))^-1 [C][C]
-        TYT = TE + C * C,                                               // (I + Diag(b) A)^-T [C][C]
-        PT = TYT + C * C,                                               // P^T [C][C]
-        GAM = PT + C * C,                                               // [D]
+    static constexpr size_t KDR = 0, KRR = KDR + C * D, KDT = KRR + C * D, KRT = KDT + C * D, QDT = KRT + C * D,
+        TE = QDT + C * D,                                               // (I + A Diag(b))^-1
+        TYT = TE + TILES * 256,                                         // (I + Diag(b) A)^-1, transposed
+        PT = TYT + TILES * 256,                                         // P, transposed
+        GAM = PT + TILES * 256,                                         // [D]
         RQ = GAM + D, RK = RQ + C,                                      // 1 / norms of q and k [C]
         SIZE = RK + C;
 };
@@ -216,10 +224,8 @@ struct Decay {
 
 // ---- prep -----------------------------------------------------------------
 
-// The block tiles on and below the diagonal of a lower triangular C x C matrix.
-constexpr int TILES = NB * (NB + 1) / 2, TP = 20;
+constexpr int TP = 20;                        // LDS row stride of a block tile
 typedef float Tile[BT][TP];
-__device__ __forceinline__ constexpr int tile_of(int bi, int bj) { return bi * (bi + 1) / 2 + bj; }
 
 // Thread (blk, c) owns channel c of the 16 tokens of block blk and forms every
 // decay there by itself. The products over channels run half a head (64
@@ -229,7 +235,7 @@ template <int D>
 struct PrepLds {
     float X[3][C][64 + 4];
     Tile A[TILES], P[TILES];
-    float end[NB][D];                 // log-decay of a whole block
+    float dec[NB][D];                 // decay over a whole block
     float b[C], rq[C], rk[C];
 };
 
@@ -282,7 +288,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     float G[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) G[j] = (gv[4 * j] + gv[4 * j + 1]) + (gv[4 * j + 2] + gv[4 * j + 3]);
-    s.end[blk][c] = (G[0] + G[1]) + (G[2] + G[3]);
+    s.dec[blk][c] = __expf((G[0] + G[1]) + (G[2] + G[3]));
 
     float(*part)[64] = reinterpret_cast<float(*)[64]>(&s.X[0][0][0]);    // one row per wavefront
     // Pairs inside groups of four: ten products for P, six for A, summed over the
@@ -310,15 +316,6 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     }
     __syncthreads();
 
-    // block borders: whole blocks before, between and behind
-    float before = 0.f, behind = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const float e = s.end[b][c];
-        before += b < blk ? e : 0.f;
-        behind += b > blk ? e : 0.f;
-    }
-    const float fb = __expf(before), fe = __expf(behind);
     if (t < 64 * NB) {                                  // in-group products into the diagonal tiles
         const int b = t / 64, e = t % 16, o = 4 * (l / 16);
         float x = part[b * HALVES][l];
@@ -330,11 +327,6 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
 
     // Pairs of different blocks: row factor exp(sum from the block's start),
     // column factor exp(sum to the block's end), whole blocks between on the rows.
-    const __amdgpu_buffer_rsrc_t rr = buf_rsrc(rec, (int)(R::SIZE * sizeof(float)));
-    const int mine = (blk * BT * D + c) * (int)sizeof(float);
-    auto put = [&](size_t at, float x) {                // this thread's channel of a token-major record
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), rr, mine, (int)(at * sizeof(float)), 0);
-    };
     constexpr int JOBS = (12 + NW - 1) / NW;
     f32x4 acc[JOBS];
 #pragma unroll
@@ -349,19 +341,13 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
             for (int i = 0; i < BT; ++i) {
                 run += gv[i];
                 const float e = __expf(run);
-                const int tau = blk * BT + i;
-                s.X[0][tau][ch] = kv[i] * e;
-                s.X[2][tau][ch] = qv[i] * e;
-                put(R::KD + i * D, kv[i] * e * fb);
-                put(R::QD + i * D, qv[i] * e * fb);
+                s.X[0][blk * BT + i][ch] = kv[i] * e;
+                s.X[2][blk * BT + i][ch] = qv[i] * e;
             }
             run = 0.f;
 #pragma unroll
             for (int i = BT - 1; i >= 0; --i) {
-                const float e = __expf(run);
-                const int tau = blk * BT + i;
-                s.X[1][tau][ch] = kv[i] * e;
-                put(R::KR + i * D, kv[i] * e * fe);
+                s.X[1][blk * BT + i][ch] = kv[i] * __expf(run);
                 run += gv[i];
             }
         }
@@ -376,15 +362,32 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
                 for (int kk = 0; kk < 4; ++kk) {
                     const int x = 16 * kk + 4 * lg;
                     f32x4 a = ld4(&rows[lr][x]);
-                    if (bi - bj > 1) {
-                        f32x4 f = ld4(&s.end[bj + 1][64 * hf + x]);
-                        if (bi - bj > 2) f += ld4(&s.end[bj + 2][64 * hf + x]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a[e] *= __expf(f[e]);
-                    }
+                    if (bi - bj > 1) a *= ld4(&s.dec[bj + 1][64 * hf + x]);
+                    if (bi - bj > 2) a *= ld4(&s.dec[bj + 2][64 * hf + x]);
                     acc[i] = mfma16(a, ld4(&cols[lr][x]), acc[i]);
                 }
             }
+        }
+        // the scans' operands, from the staging tiles: whole blocks before (k, q with
+        // their decay from the start) or behind (k with its decay to the end) come in
+        for (int i = w; i < NB * 4; i += NW) {
+            const int tt = i % NB, kk = i / NB, x = 16 * kk + 4 * lg;
+            f32x4 f0 = {1.f, 1.f, 1.f, 1.f}, f1 = f0;
+            for (int b = 0; b < tt; ++b) f0 *= ld4(&s.dec[b][64 * hf + x]);
+            for (int b = tt + 1; b < NB; ++b) f1 *= ld4(&s.dec[b][64 * hf + x]);
+            const int at = ((tt * (D / 16) + 4 * hf + kk) * 64 + l) * 4;
+            store4(rec + R::KDR + at, ld4(&s.X[0][16 * tt + lr][x]) * f0);
+            store4(rec + R::KRR + at, ld4(&s.X[1][16 * tt + lr][x]) * f1);
+        }
+        for (int i = w; i < NB * 4; i += NW) {
+            const int tt = i % NB, ct = i / NB, x = 16 * ct + lr;
+            float f0 = 1.f, f1 = 1.f;
+            for (int b = 0; b < tt; ++b) f0 *= s.dec[b][64 * hf + x];
+            for (int b = tt + 1; b < NB; ++b) f1 *= s.dec[b][64 * hf + x];
+            const int at = (((4 * hf + ct) * NB + tt) * 64 + l) * 4;
+            store4(rec + R::KDT + at, ld4s(&s.X[0][16 * tt + 4 * lg][x], 64 + 4) * f0);
+            store4(rec + R::KRT + at, ld4s(&s.X[1][16 * tt + 4 * lg][x], 64 + 4) * f1);
+            store4(rec + R::QDT + at, ld4s(&s.X[2][16 * tt + 4 * lg][x], 64 + 4) * f0);
         }
     }
 #pragma unroll
@@ -491,8 +494,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         }
         __syncthreads();
     }
-    // out: X, and transposed (I + Diag(b) A)^-1 = I - Diag(b) X A and P; blocks
-    // above the diagonal (below it, transposed) are not written and not read
+    // out: X, and transposed (I + Diag(b) A)^-1 = I - Diag(b) X A and P
     for (int i = w; i < TILES; i += NW) {
         const int bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, bj = i - bi * (bi + 1) / 2;
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
@@ -502,11 +504,11 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         f32x4 ty;
 #pragma unroll
         for (int r = 0; r < 4; ++r) ty[r] = (row + r == col ? 1.f : 0.f) - s.b[row + r] * sum[r];
-        store4(rec + R::TYT + col * C + row, ty);
-        store4(rec + R::PT + col * C + row, ld4s(&s.P[i][4 * lg][lr], TP));
-        store4(rec + R::TE + (16 * bi + lr) * C + 16 * bj + 4 * lg, ld4(&X[i][lr][4 * lg]));
+        store4(rec + R::TYT + (i * 64 + l) * 4, ty);
+        store4(rec + R::PT + (i * 64 + l) * 4, ld4s(&s.P[i][4 * lg][lr], TP));
+        store4(rec + R::TE + (i * 64 + l) * 4, ld4(&X[i][lr][4 * lg]));
     }
-    if (t < D) rec[R::GAM + t] = __expf((s.end[0][t] + s.end[1][t]) + (s.end[2][t] + s.end[3][t]));
+    if (t < D) rec[R::GAM + t] = (s.dec[0][t] * s.dec[1][t]) * (s.dec[2][t] * s.dec[3][t]);
 }
 
 // ---- scan -----------------------------------------------------------------
@@ -564,15 +566,15 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             for (int r = 0; r < 4; ++r) s.S[4 * lg + r][key(i)] = st[i][r];
         }
     };
-    auto rows_of = [&](f32x4(&x)[D / 16], const float *m) {           // token rows, all channels
+    auto rows_of = [&](f32x4(&x)[D / 16], const float *m) {           // this wavefront's tokens, all channels
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) x[kk] = ld4(m + tau * D + 16 * kk + 4 * lg);
+        for (int kk = 0; kk < D / 16; ++kk) x[kk] = ld4(m + ((w * (D / 16) + kk) * 64 + l) * 4);
     };
-    auto cols_of = [&](f32x4(&x)[CT][NB], const float *m) {           // this wavefront's channels, all tokens
+    auto cols_of = [&](f32x4(&x)[CT][NB], const float *m) {           // its channels, all tokens
 #pragma unroll
         for (int i = 0; i < CT; ++i)
 #pragma unroll
-            for (int kk = 0; kk < NB; ++kk) x[i][kk] = ld4s(m + (16 * kk + 4 * lg) * D + key(i), D);
+            for (int kk = 0; kk < NB; ++kk) x[i][kk] = ld4(m + (((w * CT + i) * NB + kk) * 64 + l) * 4);
     };
     auto gam_of = [&](float(&x)[CT], const float *rec) {
 #pragma unroll
@@ -593,16 +595,16 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         auto te_of = [&](const float *rec) {
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
-                if (kk <= w) te[kk] = ld4(rec + R::TE + tau * C + 16 * kk + 4 * lg);
+                if (kk <= w) te[kk] = ld4(rec + R::TE + (tile_of(w, kk) * 64 + l) * 4);
         };
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
-            rows_of(kd, rec + R::KD);
+            rows_of(kd, rec + R::KDR);
             const Item it = chunk_of(0);
             vt = v_of(it);
             te_of(rec);
             b = beta_of(it);
-            cols_of(kr, rec + R::KR);
+            cols_of(kr, rec + R::KRT);
             gam_of(gam, rec);
         }
         for (int step = 0; step < chunks; ++step) {
@@ -615,7 +617,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kd[kk], acc);
-            rows_of(kd, rec + R::KD);
+            rows_of(kd, rec + R::KDR);
             acc = Rows<TI>::value4(vt) - acc;
             vt = v_of(it);
 #pragma unroll
@@ -636,7 +638,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
                 for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kr[i][kk], st[i]);
             }
-            cols_of(kr, rec + R::KR);
+            cols_of(kr, rec + R::KRT);
             gam_of(gam, rec);
         }
     } else {
@@ -649,19 +651,19 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         auto upper_of = [&](f32x4(&x)[NB], const float *m) {
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
-                if (kk >= w) x[kk] = ld4(m + tau * C + 16 * kk + 4 * lg);
+                if (kk >= w) x[kk] = ld4(m + (tile_of(kk, w) * 64 + l) * 4);
         };
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
             const Item it = chunk_of(0);
             ov = o_of(it);
-            rows_of(kr, rec + R::KR);
+            rows_of(kr, rec + R::KRR);
             upper_of(pt, rec + R::PT);
-            cols_of(qd, rec + R::QD);
+            cols_of(qd, rec + R::QDT);
             gam_of(gam, rec);
             upper_of(ty, rec + R::TYT);
             b = beta_of(it);
-            cols_of(kd, rec + R::KD);
+            cols_of(kd, rec + R::KDT);
         }
         for (int step = 0; step < chunks; ++step) {
             const int next = min(step + 1, chunks - 1);
@@ -677,7 +679,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kr[kk], acc);
-            rows_of(kr, rec + R::KR);
+            rows_of(kr, rec + R::KRR);
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
                 if (kk >= w) acc = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), pt[kk], acc);
@@ -691,7 +693,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
                 for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), qd[i][kk], st[i]);
             }
-            cols_of(qd, rec + R::QD);
+            cols_of(qd, rec + R::QDT);
             gam_of(gam, rec);
             __syncthreads();
 #pragma unroll
@@ -707,7 +709,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             for (int i = 0; i < CT; ++i)
 #pragma unroll
                 for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kd[i][kk], st[i]);
-            cols_of(kd, rec + R::KD);
+            cols_of(kd, rec + R::KDT);
         }
     }
     if (back && dS0)
