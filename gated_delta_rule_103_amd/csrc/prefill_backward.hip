@@ -28,9 +28,10 @@
 //           one launch.
 //   finish  every (chunk, head): all gradients but dS0 from M, dM', E and Y.
 //
-// All products run on fp32 MFMA with fp32 accumulation: gradients arrive in
-// any magnitude, dg is a difference of sums that nearly cancel inside a chunk,
-// and dg and dS0 leave in fp32.
+// All products have fp32 operands and accumulation (fp32 MFMA, or the bf16 matrix
+// cores with operands cut in three): gradients arrive in any magnitude, dg is a
+// difference of sums that nearly cancel inside a chunk, and dg and dS0 leave in
+// fp32.
 //
 // Exponents. exp(a_t - a_s) is split where the tokens part in a binary tree over
 // the chunk: blocks of 16, halves of 8, groups of 4. With the border between
@@ -57,6 +58,9 @@
 namespace kda {
 namespace {
 
+typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+
 constexpr int C = 64, BT = 16, NB = C / BT;   // chunk, block of tokens, blocks
 constexpr int LP = C + 4;                     // LDS row stride of a C x C matrix
 constexpr float MIN_G = -104.f;
@@ -75,6 +79,42 @@ template <int M> __device__ __forceinline__ float lane_across(float x) {
     constexpr int ctrl = M == 8 ? 0x140 : M == 4 ? 0x141 : M == 2 ? 0x4e : 0xb1;
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), ctrl, 0xf, 0xf, true));
 }
+// fp32 products on the bf16 matrix cores. A value is cut into three bf16 parts of
+// eight significand bits each, h + m + l, exactly; of the nine products the three
+// below 2^-24 of the whole are left out, so the result is as good as an fp32
+// product's, at 6 / 16 of fp32 MFMA's time (3 / 16 where one side is bf16 already).
+// MFMA 16x16x32: a lane holds row (column) l % 16 and eight inner indices of its
+// lane group l / 16; two float4 of neighbouring 16-wide tiles make one operand.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ void split3(f32x4 a, f32x4 b, u32v4 (&p)[3]) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u0 = __float_as_uint(x[2 * i]), u1 = __float_as_uint(x[2 * i + 1]);
+        p[0][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+        const float r0 = x[2 * i] - __uint_as_float(u0 & 0xffff0000u), r1 = x[2 * i + 1] - __uint_as_float(u1 & 0xffff0000u);
+        u0 = __float_as_uint(r0);
+        u1 = __float_as_uint(r1);
+        p[1][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+        u0 = __float_as_uint(r0 - __uint_as_float(u0 & 0xffff0000u));
+        u1 = __float_as_uint(r1 - __uint_as_float(u1 & 0xffff0000u));
+        p[2][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+    }
+}
+__device__ __forceinline__ f32x4 mfma32(u32v4 a, u32v4 b, f32x4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+}
+template <int PA> __device__ __forceinline__ f32x4 product(const u32v4 (&a)[PA], const u32v4 (&b)[3], f32x4 acc) {
+    acc = mfma32(a[0], b[2], acc);                     // small terms first
+    if constexpr (PA == 3) {
+        acc = mfma32(a[2], b[0], acc);
+        acc = mfma32(a[1], b[1], acc);
+    }
+    acc = mfma32(a[0], b[1], acc);
+    if constexpr (PA == 3) acc = mfma32(a[1], b[0], acc);
+    return mfma32(a[0], b[0], acc);
+}
+
 // One step of summing 2 M values over 16 lanes: each lane keeps M of them, those
 // of its bit M, and adds what the lane across kept for it.
 template <int M> __device__ __forceinline__ void halve(float *v, int lane) {
@@ -125,9 +165,6 @@ template <int D> struct Rec {
         RQ = GAM + D, RK = RQ + C,                                      // 1 / norms of q and k [C]
         SIZE = RK + C;
 };
-
-typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
 
 struct Ws {
     int32_t *chunk_off;
@@ -721,31 +758,36 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 
 // ---- finish ---------------------------------------------------------------
 
-// D / 16 wavefronts, one for each 16 key channels. LDS tiles O, U, V hold dO,
-// U = b E and dV = b Y as A operands over the value channels: float4 l of
-// (token block, value tile).
-template <int D>
+// A workgroup takes CH key channels of a (chunk, head), one wavefront for each 16.
+// CH = 64 leaves room for two workgroups on a CU, which cover each other's loads
+// and barriers (dP and dA are then formed twice at D = 128); where rows are summed
+// over all channels (normalised q and k, a gate per head) CH = D.
+// O, U and V hold dO, U = b E and dV = b Y as split operands over 32 SM value
+// channels at a time: [part][32 channels][token block], lane l's 16 bytes.
+template <int CH, int PO>
 struct FinishLds {
-    static constexpr int NT = D / 16;
-    float O[C * D], U[C * D], V[C * D];
+    static constexpr int NW = CH / 16, SM = NW / 4;
+    u32v4 O[PO][SM][NB][64], U[3][SM][NB][64], V[3][SM][NB][64];
     float dP[C][LP], dA[C][LP];       // strictly lower
     float diag[C];                    // the diagonal of dP
-    float db[C][NT];
-    float rows[2][NT][C];             // sums over a wavefront's channels
+    float db[C][4];
+    float rows[2][NW][C];             // sums over a wavefront's channels
 };
 
-template <int D, typename TI, typename TB, typename TG>
-__global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__restrict__ q, const TI *__restrict__ k,
-                                                       const TB *__restrict__ beta, const TG *__restrict__ dout,
-                                                       TI *__restrict__ dq, TI *__restrict__ dk, TI *__restrict__ dv,
-                                                       float *__restrict__ dg, TB *__restrict__ dbeta) {
+template <int D, int CH, typename TI, typename TB, typename TG>
+__global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *__restrict__ q, const TI *__restrict__ k,
+                                                          const TB *__restrict__ beta, const TG *__restrict__ dout,
+                                                          TI *__restrict__ dq, TI *__restrict__ dk,
+                                                          TI *__restrict__ dv, float *__restrict__ dg,
+                                                          TB *__restrict__ dbeta) {
     using R = Rec<D>;
-    constexpr int NT = D / 16, THREADS = 4 * D;
+    constexpr int NT = D / 16, NW = CH / 16, SM = NW / 4, STAGES = NT / (2 * SM), PO = sizeof(TG) == 2 ? 1 : 3;
     extern __shared__ char lds_raw[];
-    FinishLds<D> &s = *reinterpret_cast<FinishLds<D> *>(lds_raw);
+    FinishLds<CH, PO> &s = *reinterpret_cast<FinishLds<CH, PO> *>(lds_raw);
     Item it;
-    if (!it.find(p, blockIdx.x)) return;
-    const size_t item = blockIdx.x;
+    const size_t item = blockIdx.x / (D / CH);
+    const int part = blockIdx.x % (D / CH);
+    if (!it.find(p, item)) return;
     const float *rec = p.ws.rec + item * R::SIZE, *M = p.ws.M + item * D * D, *dM = p.ws.dM + item * D * D;
     const float *E = p.ws.E + item * C * D, *Y = p.ws.Y + item * C * D;
     const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
@@ -754,24 +796,146 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
     const Rows<TG> dor(dout, it, p.H, D);
     const Rows<TB> br(beta, it, p.H, 1), dbr(dbeta, it, p.H, 1);
     const Decay decay(p, it, D);
+    const int ct = part * NW + w, c = 16 * ct + lr;    // this wavefront's channel tile, this lane's channel
 
+    // Through the states (rows 16 b + 4 lg + r of channel c): dO M^T, dV M^T and
+    // U dM^T; and dP and dA, of each the ten tiles on and below the diagonal. The
+    // next stage's data are on their way while a stage is computed.
+    constexpr int JOBS = (2 * TILES + NW - 1) / NW;
+    f32x4 aq[NB], ak[NB], ar[NB], ap[JOBS];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {                     // wavefront w: value tile w of token block i
-        const int f = ((i * NT + w) * 64 + l) * 4, tau = 16 * i + lr, j = 16 * w + 4 * lg;
-        const f32x4 e = ld4(E + f), y = ld4(Y + f), o = dor.at4(tau, j);
-        const float b = br.at(tau, 0);
-        dvr.put4(tau, j, y * b);
-        store4(&s.O[f], o);
-        store4(&s.U[f], e * b);
-        store4(&s.V[f], y * b);
-        const f32x4 ye = e * y;
-        float x = (ye[0] + ye[1]) + (ye[2] + ye[3]);
-        x += __shfl_xor(x, 16, 64);
-        x += __shfl_xor(x, 32, 64);
-        if (lg == 0) s.db[tau][w] = x;
+    for (int b = 0; b < NB; ++b) aq[b] = ak[b] = ar[b] = zero;
+#pragma unroll
+    for (int i = 0; i < JOBS; ++i) ap[i] = zero;
+    float mdm = 0.f;
+    const int sb = w % NB, sm = w / NB, stau = 16 * sb + lr;   // staging: token block, 32 value channels, token
+    const float be = br.at(stau, 0);
+    f32x4 e0, e1, y0, y1, m0[SM], m1[SM], d0[SM], d1[SM];
+    typename Rows<TG>::Raw4 o0, o1;
+    auto load_rows = [&](int stage) {
+        const int jt = 2 * (stage * SM + sm), f = ((sb * NT + jt) * 64 + l) * 4, j = 16 * jt + 4 * lg;
+        e0 = ld4(E + f);
+        e1 = ld4(E + f + 256);
+        y0 = ld4(Y + f);
+        y1 = ld4(Y + f + 256);
+        o0 = dor.raw4(stau, j);
+        o1 = dor.raw4(stau, j + 16);
+    };
+    auto load_states = [&](int stage, int m) {
+        const int f = ((ct * NT + 2 * (stage * SM + m)) * 64 + l) * 4;
+        m0[m] = ld4(M + f);
+        m1[m] = ld4(M + f + 256);
+        d0[m] = ld4(dM + f);
+        d1[m] = ld4(dM + f + 256);
+    };
+    load_rows(0);
+#pragma unroll
+    for (int m = 0; m < SM; ++m) load_states(0, m);
+    const bool first = part == 0;                      // dv and dbeta are the first workgroup's
+#pragma unroll 1
+    for (int stage = 0; stage < STAGES; ++stage) {
+        const int next = min(stage + 1, STAGES - 1);
+        if (stage) __syncthreads();
+        {
+            const int j = 32 * (stage * SM + sm) + 4 * lg;
+            u32v4 o[PO], u[3], v[3];
+            if constexpr (PO == 1) o[0] = u32v4{o0[0], o0[1], o1[0], o1[1]};
+            else split3(Rows<TG>::value4(o0), Rows<TG>::value4(o1), o);
+            split3(e0 * be, e1 * be, u);
+            split3(y0 * be, y1 * be, v);
+            if (first) {
+                dvr.put4(stau, j, y0 * be);
+                dvr.put4(stau, j + 16, y1 * be);
+            }
+#pragma unroll
+            for (int x = 0; x < PO; ++x) s.O[x][sm][sb][l] = o[x];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                s.U[x][sm][sb][l] = u[x];
+                s.V[x][sm][sb][l] = v[x];
+            }
+            const f32x4 ye = e0 * y0 + e1 * y1;
+            float x = (ye[0] + ye[1]) + (ye[2] + ye[3]);
+            x += __shfl_xor(x, 16, 64);
+            x += __shfl_xor(x, 32, 64);
+            if (lg == 0) s.db[stau][stage * SM + sm] = x;
+        }
+        load_rows(next);
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < SM; ++m) {
+            u32v4 ms[3], ds[3];
+            const f32x4 x = m0[m] * d0[m] + m1[m] * d1[m];
+            mdm += (x[0] + x[1]) + (x[2] + x[3]);
+            split3(m0[m], m1[m], ms);
+            split3(d0[m], d1[m], ds);
+            load_states(next, m);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                u32v4 o[PO], u[3], v[3];
+#pragma unroll
+                for (int x = 0; x < PO; ++x) o[x] = s.O[x][m][b][l];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    v[x] = s.V[x][m][b][l];
+                    u[x] = s.U[x][m][b][l];
+                }
+                aq[b] = product(o, ms, aq[b]);
+                ak[b] = product(v, ms, ak[b]);
+                ar[b] = product(u, ds, ar[b]);
+                settle(aq[b]);
+                settle(ak[b]);
+                settle(ar[b]);
+            }
+#pragma unroll
+            for (int i = 0; i < JOBS; ++i) {
+                const int job = w + i * NW, n = job >> 1;
+                if (job < 2 * TILES) {
+                    const int bi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, bj = n - bi * (bi + 1) / 2;
+                    u32v4 u[3];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) u[x] = s.U[x][m][bj][l];
+                    if (job & 1) {
+                        u32v4 v[3];
+#pragma unroll
+                        for (int x = 0; x < 3; ++x) v[x] = s.V[x][m][bi][l];
+                        ap[i] = product(v, u, ap[i]);
+                    } else {
+                        u32v4 o[PO];
+#pragma unroll
+                        for (int x = 0; x < PO; ++x) o[x] = s.O[x][m][bi][l];
+                        ap[i] = product(o, u, ap[i]);
+                    }
+                }
+            }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < JOBS; ++i) {
+        const int job = w + i * NW, n = job >> 1;
+        if (job < 2 * TILES) {
+            const int bi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, bj = n - bi * (bi + 1) / 2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int tau = 16 * bi + 4 * lg + r, sig = 16 * bj + lr;
+                if (job & 1) {
+                    s.dA[tau][sig] = sig < tau ? -ap[i][r] : 0.f;
+                } else {
+                    s.dP[tau][sig] = sig < tau ? ap[i][r] : 0.f;
+                    if (sig == tau) s.diag[tau] = ap[i][r];
+                }
+            }
+        }
+    }
+    mdm += __shfl_xor(mdm, 16, 64);
+    mdm += __shfl_xor(mdm, 32, 64);
+    if (first && t < C) {
+        float x = 0.f;
+        for (int i = 0; i < NT / 2; ++i) x += s.db[t][i];
+        dbr.put(t, 0, x);
+    }
+
     // q, k and the decays of each block: a lane holds the group lg of its channel
-    const int c = 16 * w + lr;
     f32x4 qv[NB], kv[NB], gv[NB], ein[NB], eout[NB];
     float end[NB], grp[NB];                            // the block's and the other group's sum
     uint32_t wiped = 0;                                // tokens whose decay is 0, of gradient 0
@@ -793,31 +957,6 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
             kv[b] *= ld4(rec + R::RK + 16 * b + 4 * lg);
         }
     }
-    __syncthreads();
-    if (t < C) {
-        float x = 0.f;
-        for (int i = 0; i < NT; ++i) x += s.db[t][i];
-        dbr.put(t, 0, x);
-    }
-
-    // dP and dA: the ten tiles on and below the diagonal, both matrices
-    for (int job = w; job < 20; job += NT) {
-        const int i = job >> 1, bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, bj = i - bi * (bi + 1) / 2;
-        const float *left = job & 1 ? s.V : s.O;
-        f32x4 acc = zero;
-        for (int kk = 0; kk < NT; ++kk)
-            acc = mfma16(ld4(&left[((bi * NT + kk) * 64 + l) * 4]), ld4(&s.U[((bj * NT + kk) * 64 + l) * 4]), acc);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tau = 16 * bi + 4 * lg + r, sig = 16 * bj + lr;
-            if (job & 1) {
-                s.dA[tau][sig] = sig < tau ? -acc[r] : 0.f;
-            } else {
-                s.dP[tau][sig] = sig < tau ? acc[r] : 0.f;
-                if (sig == tau) s.diag[tau] = acc[r];
-            }
-        }
-    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const f32x4 g = gv[b];
@@ -835,7 +974,31 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
             eout[b][r] = __expf(out0 + suf[r]);        // behind the token to the block's end
         }
     }
+    // what came through the states gets its decay from the chunk's start or to its
+    // end: aq and ak become dq's and dk's share, ar what a token sends behind the chunk
+    float all;
+    {
+        float before[NB], behind[NB];
+        before[0] = behind[NB - 1] = 0.f;
+#pragma unroll
+        for (int b = 1; b < NB; ++b) {
+            before[b] = before[b - 1] + end[b - 1];
+            behind[NB - 1 - b] = behind[NB - b] + end[NB - b];
+        }
+        all = __expf(before[NB - 1] + end[NB - 1]) * mdm;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const f32x4 fi = ein[b] * __expf(before[b]);
+            aq[b] *= fi;
+            ak[b] *= -fi;
+            ar[b] *= eout[b] * __expf(behind[b]);
+        }
+    }
     __syncthreads();
+    // ar waits in LDS (U and V are done with) and leaves its registers to the pairs
+    f32x4 *wait = reinterpret_cast<f32x4 *>(&s.U[0][0][0][0]) + t;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wait[b * 4 * CH] = ar[b];
 
     // pairs of tokens of different blocks: what a token receives is scaled by
     // ein, what it sends by eout, whole blocks between on the operand
@@ -910,55 +1073,18 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
             }
         }
         const f32x4 dg4 = ld4(&s.diag[16 * b + 4 * lg]), send = pc[b];
+        pq[b] += aq[b];
+        pk[b] += ak[b];
         pc[b] = qv[b] * pq[b] + kv[b] * (pk[b] - send);
         pq[b] += dg4 * kv[b];
-        pk[b] += send + dg4 * qv[b];
+        const f32x4 sent = wait[b * 4 * CH];
+        pk[b] += send + dg4 * qv[b] + sent;
+        ar[b] = sent * kv[b];
         settle(pq[b]);
         settle(pk[b]);
         settle(pc[b]);
     }
 
-    // through the states, with the decays from the chunk's start and to its end
-    float before[NB], behind[NB];
-    before[0] = behind[NB - 1] = 0.f;
-#pragma unroll
-    for (int b = 1; b < NB; ++b) {
-        before[b] = before[b - 1] + end[b - 1];
-        behind[NB - 1 - b] = behind[NB - b] + end[NB - b];
-    }
-    f32x4 out[NB];                                     // what a token sends behind the chunk
-    float all;
-    {
-        f32x4 aq[NB], ak[NB], ar[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) aq[b] = ak[b] = ar[b] = zero;
-        float mdm = 0.f;
-#pragma unroll 1
-        for (int jt = 0; jt < NT; ++jt) {
-            const f32x4 m = ld4(M + ((w * NT + jt) * 64 + l) * 4), d = ld4(dM + ((w * NT + jt) * 64 + l) * 4);
-            const f32x4 x = m * d;
-            mdm += (x[0] + x[1]) + (x[2] + x[3]);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int f = ((b * NT + jt) * 64 + l) * 4;
-                aq[b] = mfma16(ld4(&s.O[f]), m, aq[b]);
-                ak[b] = mfma16(ld4(&s.V[f]), m, ak[b]);
-                ar[b] = mfma16(ld4(&s.U[f]), d, ar[b]);
-            }
-        }
-        mdm += __shfl_xor(mdm, 16, 64);
-        mdm += __shfl_xor(mdm, 32, 64);
-        all = __expf(before[NB - 1] + end[NB - 1]) * mdm;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const f32x4 fi = ein[b] * __expf(before[b]), fo = eout[b] * __expf(behind[b]);
-            const f32x4 gq = aq[b] * fi, gk = ak[b] * fi, go = ar[b] * fo;
-            pc[b] += qv[b] * gq - kv[b] * gk;
-            out[b] = kv[b] * go;
-            pq[b] += gq;
-            pk[b] += go - gk;
-        }
-    }
     if (p.qk_norm) {                                   // dx = (dx^ - x^ (x^ . dx^)) / |x|
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -979,7 +1105,7 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             f32x4 x = zero, y = zero;
-            for (int i = 0; i < NT; ++i) {
+            for (int i = 0; i < NW; ++i) {
                 x += ld4(&s.rows[0][i][16 * b + 4 * lg]);
                 y += ld4(&s.rows[1][i][16 * b + 4 * lg]);
             }
@@ -1011,8 +1137,8 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
         after += (x0 + x1) + (x2 + x3);
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {                     // prefix sums of out, without the token itself
-        const f32x4 y = out[b];
+    for (int b = 0; b < NB; ++b) {                     // prefix sums of out (ar), without the token itself
+        const f32x4 y = ar[b];
         f32x4 x = {0.f, y[0], y[0] + y[1], (y[0] + y[1]) + y[2]};
         const float tot = x[3] + y[3];
         const float x0 = __shfl(tot, lr, 64), x1 = __shfl(tot, lr + 16, 64), x2 = __shfl(tot, lr + 32, 64),
@@ -1044,7 +1170,7 @@ __global__ __launch_bounds__(4 * D) void finish_kernel(Common p, const TI *__res
     __syncthreads();
     if (t < C) {
         float x = 0.f;
-        for (int i = 0; i < NT; ++i) x += s.rows[0][i][t];
+        for (int i = 0; i < NW; ++i) x += s.rows[0][i][t];
         dgr.put(t, 0, x);
     }
 }
@@ -1086,13 +1212,17 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
     const TB *beta = static_cast<const TB *>(a.beta);
     const TG *dout = static_cast<const TG *>(a.dout);
     const auto prep = prep_kernel<D, TI, TB>;
-    const auto finish = finish_kernel<D, TI, TB, TG>;
+    constexpr int PO = sizeof(TG) == 2 ? 1 : 3;
+    // sums over a row's channels need the whole row in one workgroup
+    const bool whole = D == 64 || a.qk_norm || a.g_head;
+    const auto finish = whole ? finish_kernel<D, D, TI, TB, TG> : finish_kernel<D, 64, TI, TB, TG>;
+    const int ch = whole ? D : 64, finish_lds = whole ? sizeof(FinishLds<D, PO>) : sizeof(FinishLds<64, PO>);
     // set on every call (idempotent; no process-wide flag to race on)
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(prep),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(PrepLds<D>));
     if (e != hipSuccess) return e;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(finish), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            sizeof(FinishLds<D>));
+                            finish_lds);
     if (e != hipSuccess) return e;
     if (items > 0) {
         hipLaunchKernelGGL(prep, dim3(items), dim3(4 * D), sizeof(PrepLds<D>), a.stream, p, q, k, beta);
@@ -1104,7 +1234,7 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
                        dout, a.S0, a.dS_out, a.dS0);
     e = hipGetLastError();
     if (e != hipSuccess || items == 0) return e;
-    hipLaunchKernelGGL(finish, dim3(items), dim3(4 * D), sizeof(FinishLds<D>), a.stream, p, q, k, beta, dout,
+    hipLaunchKernelGGL(finish, dim3(items * (D / ch)), dim3(4 * ch), finish_lds, a.stream, p, q, k, beta, dout,
                        static_cast<TI *>(a.dq), static_cast<TI *>(a.dk), static_cast<TI *>(a.dv), a.dg,
                        static_cast<TB *>(a.dbeta));
     return hipGetLastError();
