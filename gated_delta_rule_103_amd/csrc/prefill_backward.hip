@@ -166,6 +166,13 @@ template <int D> struct Rec {
         SIZE = RK + C;
 };
 
+// block row and column of tile i
+__device__ __forceinline__ void tile_at(int i, int &bi, int &bj) {
+    i = min(i, TILES - 1);
+    bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
+    bj = i - bi * (bi + 1) / 2;
+}
+
 struct Ws {
     int32_t *chunk_off;
     float *rec, *M, *dM, *E, *Y;
@@ -767,9 +774,13 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 template <int CH, int PO>
 struct FinishLds {
     static constexpr int NW = CH / 16, SM = NW / 4;
-    u32v4 O[PO][SM][NB][64], U[3][SM][NB][64], V[3][SM][NB][64];
-    float dP[C][LP], dA[C][LP];       // strictly lower
-    float diag[C];                    // the diagonal of dP
+    union {
+        struct {
+            u32v4 O[PO][SM][NB][64], U[3][SM][NB][64], V[3][SM][NB][64];
+        };
+        f32x4 wait[2][NB][4 * CH];    // each thread's own values, while the pairs need its registers
+    };
+    float dP[C][LP], dA[C][LP];       // tiles on and below the diagonal; above it nothing is used
     float db[C][4];
     float rows[2][NW][C];             // sums over a wavefront's channels
 };
@@ -801,7 +812,10 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     // Through the states (rows 16 b + 4 lg + r of channel c): dO M^T, dV M^T and
     // U dM^T; and dP and dA, of each the ten tiles on and below the diagonal. The
     // next stage's data are on their way while a stage is computed.
+    // every second wavefront has the tiles tile_first, + NW / 2, ..; one behind the
+    // last is the last again
     constexpr int JOBS = (2 * TILES + NW - 1) / NW;
+    const int tile_first = w / 2;
     f32x4 aq[NB], ak[NB], ar[NB], ap[JOBS];
 #pragma unroll
     for (int b = 0; b < NB; ++b) aq[b] = ak[b] = ar[b] = zero;
@@ -870,62 +884,74 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
             split3(m0[m], m1[m], ms);
             split3(d0[m], d1[m], ds);
             load_states(next, m);
+            // operands of the next block are read while this one's products run
+            u32v4 o[2][PO], u[2][3], v[2][3];
+            auto read = [&](int b) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                u32v4 o[PO], u[3], v[3];
-#pragma unroll
-                for (int x = 0; x < PO; ++x) o[x] = s.O[x][m][b][l];
+                for (int x = 0; x < PO; ++x) o[b & 1][x] = s.O[x][m][b][l];
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
-                    v[x] = s.V[x][m][b][l];
-                    u[x] = s.U[x][m][b][l];
+                    v[b & 1][x] = s.V[x][m][b][l];
+                    u[b & 1][x] = s.U[x][m][b][l];
                 }
-                aq[b] = product(o, ms, aq[b]);
-                ak[b] = product(v, ms, ak[b]);
-                ar[b] = product(u, ds, ar[b]);
+            };
+            read(0);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (b + 1 < NB) read(b + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                aq[b] = product(o[b & 1], ms, aq[b]);
+                ak[b] = product(v[b & 1], ms, ak[b]);
+                ar[b] = product(u[b & 1], ds, ar[b]);
                 settle(aq[b]);
                 settle(ak[b]);
                 settle(ar[b]);
             }
+            // even wavefronts have tiles of dP, odd ones of dA
+            auto tiles = [&](auto &left, auto np) {
+                constexpr int PL = decltype(np)::value;
+                u32v4 x[2][PL], y[2][3];
+                auto read_tile = [&](int i) {
+                    int bi, bj;
+                    tile_at(tile_first + i * (NW / 2), bi, bj);
 #pragma unroll
-            for (int i = 0; i < JOBS; ++i) {
-                const int job = w + i * NW, n = job >> 1;
-                if (job < 2 * TILES) {
-                    const int bi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, bj = n - bi * (bi + 1) / 2;
-                    u32v4 u[3];
+                    for (int z = 0; z < PL; ++z) x[i & 1][z] = left[z][m][bi][l];
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) u[x] = s.U[x][m][bj][l];
-                    if (job & 1) {
-                        u32v4 v[3];
+                    for (int z = 0; z < 3; ++z) y[i & 1][z] = s.U[z][m][bj][l];
+                };
+                read_tile(0);
 #pragma unroll
-                        for (int x = 0; x < 3; ++x) v[x] = s.V[x][m][bi][l];
-                        ap[i] = product(v, u, ap[i]);
-                    } else {
-                        u32v4 o[PO];
-#pragma unroll
-                        for (int x = 0; x < PO; ++x) o[x] = s.O[x][m][bi][l];
-                        ap[i] = product(o, u, ap[i]);
-                    }
+                for (int i = 0; i < JOBS; ++i) {
+                    if (i + 1 < JOBS) read_tile(i + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    ap[i] = product(x[i & 1], y[i & 1], ap[i]);
+                    settle(ap[i]);
                 }
-            }
+            };
+            if (w & 1) tiles(s.V, std::integral_constant<int, 3>{});
+            else tiles(s.O, std::integral_constant<int, PO>{});
         }
     }
+    // q, k and the log-decays on their way: a lane holds the group lg
+    // of four tokens of each block, for its channel
+    typename Rows<TI>::Raw qraw[NB][4], kraw[NB][4];
+    f32x4 gv[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tau = 16 * b + 4 * lg + r;
+            qraw[b][r] = qr.raw(tau, c);
+            kraw[b][r] = kr.raw(tau, c);
+            gv[b][r] = decay.g.at(tau, c * decay.col);
+        }
 #pragma unroll
     for (int i = 0; i < JOBS; ++i) {
-        const int job = w + i * NW, n = job >> 1;
-        if (job < 2 * TILES) {
-            const int bi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, bj = n - bi * (bi + 1) / 2;
+        int bi, bj;
+        tile_at(tile_first + i * (NW / 2), bi, bj);
+        float(*out)[LP] = w & 1 ? s.dA : s.dP;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tau = 16 * bi + 4 * lg + r, sig = 16 * bj + lr;
-                if (job & 1) {
-                    s.dA[tau][sig] = sig < tau ? -ap[i][r] : 0.f;
-                } else {
-                    s.dP[tau][sig] = sig < tau ? ap[i][r] : 0.f;
-                    if (sig == tau) s.diag[tau] = ap[i][r];
-                }
-            }
-        }
+        for (int r = 0; r < 4; ++r) out[16 * bi + 4 * lg + r][16 * bj + lr] = w & 1 ? -ap[i][r] : ap[i][r];
     }
     mdm += __shfl_xor(mdm, 16, 64);
     mdm += __shfl_xor(mdm, 32, 64);
@@ -935,18 +961,16 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         dbr.put(t, 0, x);
     }
 
-    // q, k and the decays of each block: a lane holds the group lg of its channel
-    f32x4 qv[NB], kv[NB], gv[NB], ein[NB], eout[NB];
+    f32x4 qv[NB], kv[NB], ein[NB], eout[NB];
     float end[NB], grp[NB];                            // the block's and the other group's sum
     uint32_t wiped = 0;                                // tokens whose decay is 0, of gradient 0
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int tau = 16 * b + 4 * lg + r;
-            qv[b][r] = qr.at(tau, c);
-            kv[b][r] = kr.at(tau, c);
-            gv[b][r] = decay.at(tau, c);
+            qv[b][r] = Rows<TI>::value(qraw[b][r]);
+            kv[b][r] = Rows<TI>::value(kraw[b][r]);
+            gv[b][r] = fmaxf(gv[b][r], MIN_G);
             wiped |= (gv[b][r] <= MIN_G ? 1u : 0u) << (4 * b + r);
         }
     }
@@ -995,41 +1019,61 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         }
     }
     __syncthreads();
-    // ar waits in LDS (U and V are done with) and leaves its registers to the pairs
-    f32x4 *wait = reinterpret_cast<f32x4 *>(&s.U[0][0][0][0]) + t;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) wait[b * 4 * CH] = ar[b];
+    for (int b = 0; b < NB; ++b) {
+        s.wait[0][b][t] = ak[b];
+        s.wait[1][b][t] = ar[b];
+    }
 
     // pairs of tokens of different blocks: what a token receives is scaled by
     // ein, what it sends by eout, whole blocks between on the operand
     f32x4 pq[NB], pk[NB], pc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) pq[b] = pk[b] = pc[b] = zero;
+    // tiles of dP and dA in the order of use, each read as left operands (by rows and
+    // by columns) while the one before it is multiplied
+    constexpr int ORDER[TILES][2] = {{1, 0}, {2, 1}, {2, 0}, {3, 2}, {3, 1}, {3, 0}, {0, 0}, {1, 1}, {2, 2}, {3, 3}};
+    struct Operands {
+        f32x4 prow, arow, pcol, acol;
+    } op[2];
+    auto read = [&](int n) {
+        const int bi = ORDER[n][0], bj = ORDER[n][1];
+        op[n & 1] = Operands{ld4(&s.dP[16 * bi + lr][16 * bj + 4 * lg]), ld4(&s.dA[16 * bi + lr][16 * bj + 4 * lg]),
+                             ld4s(&s.dP[16 * bi + 4 * lg][16 * bj + lr], LP),
+                             ld4s(&s.dA[16 * bi + 4 * lg][16 * bj + lr], LP)};
+    };
+    read(0);
 #pragma unroll
-    for (int bi = 1; bi < NB; ++bi) {
-        float between = 0.f;
-#pragma unroll
-        for (int bj = bi - 1; bj >= 0; --bj) {
-            const float f = __expf(between);
-            const f32x4 key = kv[bj] * eout[bj] * f;
-            pq[bi] = mfma16(ld4(&s.dP[16 * bi + lr][16 * bj + 4 * lg]), key, pq[bi]);
-            pk[bi] = mfma16(ld4(&s.dA[16 * bi + lr][16 * bj + 4 * lg]), key, pk[bi]);
-            const f32x4 fe = ein[bi] * f;
-            pc[bj] = mfma16(ld4s(&s.dP[16 * bi + 4 * lg][16 * bj + lr], LP), qv[bi] * fe, pc[bj]);
-            pc[bj] = mfma16(ld4s(&s.dA[16 * bi + 4 * lg][16 * bj + lr], LP), kv[bi] * fe, pc[bj]);
-            between += end[bj];
-            settle(pq[bi]);
-            settle(pk[bi]);
-            settle(pc[bj]);
-        }
+    for (int n = 0; n < TILES - NB; ++n) {
+        const int bi = ORDER[n][0], bj = ORDER[n][1];
+        read(n + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const Operands &x = op[n & 1];
+        const float f = bi - bj == 1 ? 1.f : __expf(bi - bj == 2 ? end[bj + 1] : end[1] + end[2]);
+        const f32x4 key = kv[bj] * eout[bj] * f, fe = ein[bi] * f;
+        pq[bi] = mfma16(x.prow, key, pq[bi]);
+        pk[bi] = mfma16(x.arow, key, pk[bi]);
+        pc[bj] = mfma16(x.pcol, qv[bi] * fe, pc[bj]);
+        pc[bj] = mfma16(x.acol, kv[bi] * fe, pc[bj]);
+        settle(pq[bi]);
+        settle(pk[bi]);
+        settle(pc[bj]);
     }
-    // in-block pairs, and the pair terms put together: pq and pk become dq's and
-    // dk's share, pc row's
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         pq[b] *= ein[b];
         pk[b] *= ein[b];
         pc[b] *= eout[b];
+        settle(pq[b]);
+        settle(pk[b]);
+        settle(pc[b]);
+    }
+    // in-block pairs, and the pair terms put together: pq and pk become dq's and
+    // dk's share, pc row's
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (b + 1 < NB) read(TILES - NB + b + 1);
+        const Operands &x = op[b & 1];                 // TILES - NB is even
         const f32x4 g = gv[b];
         const f32x4 pre = {g[0], g[0] + g[1], (g[0] + g[1]) + g[2], (g[0] + g[1]) + (g[2] + g[3])};
         const f32x4 suf = {(g[1] + g[2]) + g[3], g[2] + g[3], g[3], 0.f};
@@ -1046,38 +1090,40 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
                 ei[r] = __expf(in0 + pre[r]);
                 eo[r] = __expf(out0 + suf[r]);
             }
-            const f32x4 prow = ld4(&s.dP[16 * b + lr][16 * b + 4 * lg]), arow = ld4(&s.dA[16 * b + lr][16 * b + 4 * lg]);
-            const f32x4 pcol = ld4s(&s.dP[16 * b + 4 * lg][16 * b + lr], LP),
-                        acol = ld4s(&s.dA[16 * b + 4 * lg][16 * b + lr], LP);
             const f32x4 key = kv[b] * eo;
-            pq[b] += mfma16(row ? prow : zero, key, zero) * ei;
-            pk[b] += mfma16(row ? arow : zero, key, zero) * ei;
-            pc[b] += mfma16(col ? acol : zero, kv[b] * ei, mfma16(col ? pcol : zero, qv[b] * ei, zero)) * eo;
+            pq[b] += mfma16(row ? x.prow : zero, key, zero) * ei;
+            pk[b] += mfma16(row ? x.arow : zero, key, zero) * ei;
+            pc[b] += mfma16(col ? x.acol : zero, kv[b] * ei, mfma16(col ? x.pcol : zero, qv[b] * ei, zero)) * eo;
             settle(pq[b]);
             settle(pk[b]);
             settle(pc[b]);
         }
         // inside the group: all in this lane
+        f32x4 dp[3], da[3];                            // the group's rows
+#pragma unroll
+        for (int r = 1; r < 4; ++r) {
+            dp[r - 1] = ld4(&s.dP[16 * b + 4 * lg + r][16 * b + 4 * lg]);
+            da[r - 1] = ld4(&s.dA[16 * b + 4 * lg + r][16 * b + 4 * lg]);
+        }
+        const float diag0 = s.dP[16 * b + 4 * lg][16 * b + 4 * lg];
         const float e10 = __expf(g[1]), e21 = __expf(g[2]), e32 = __expf(g[3]);
         const f32x4 ex[3] = {{e10, 0.f, 0.f, 0.f}, {e21 * e10, e21, 0.f, 0.f}, {e32 * e21 * e10, e32 * e21, e32, 0.f}};
 #pragma unroll
         for (int r = 1; r < 4; ++r) {
-            const f32x4 dp = ld4(&s.dP[16 * b + 4 * lg + r][16 * b + 4 * lg]),
-                        da = ld4(&s.dA[16 * b + 4 * lg + r][16 * b + 4 * lg]);
 #pragma unroll
-            for (int x = 0; x < r; ++x) {
-                const float e = ex[r - 1][x], ek = e * kv[b][x];
-                pq[b][r] += dp[x] * ek;
-                pk[b][r] += da[x] * ek;
-                pc[b][x] += e * (dp[x] * qv[b][r] + da[x] * kv[b][r]);
+            for (int y = 0; y < r; ++y) {
+                const float e = ex[r - 1][y], ek = e * kv[b][y];
+                pq[b][r] += dp[r - 1][y] * ek;
+                pk[b][r] += da[r - 1][y] * ek;
+                pc[b][y] += e * (dp[r - 1][y] * qv[b][r] + da[r - 1][y] * kv[b][r]);
             }
         }
-        const f32x4 dg4 = ld4(&s.diag[16 * b + 4 * lg]), send = pc[b];
+        const f32x4 dg4 = {diag0, dp[0][1], dp[1][2], dp[2][3]}, send = pc[b];
         pq[b] += aq[b];
-        pk[b] += ak[b];
+        pk[b] += s.wait[0][b][t];
         pc[b] = qv[b] * pq[b] + kv[b] * (pk[b] - send);
         pq[b] += dg4 * kv[b];
-        const f32x4 sent = wait[b * 4 * CH];
+        const f32x4 sent = s.wait[1][b][t];
         pk[b] += send + dg4 * qv[b] + sent;
         ar[b] = sent * kv[b];
         settle(pq[b]);
@@ -1114,13 +1160,15 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         }
         __syncthreads();
     }
+    int cs = c;                                        // or the loads' offsets are kept for the stores
+    asm volatile("" : "+v"(cs));
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int tau = 16 * b + 4 * lg + r;
-            dqr.put(tau, c, pq[b][r]);
-            dkr.put(tau, c, pk[b][r]);
+            dqr.put(tau, cs, pq[b][r]);
+            dkr.put(tau, cs, pk[b][r]);
         }
     if (!dg) return;
     // dg_i = sum_{t >= i} row_t + sum_{t < i} out_t + all
@@ -1155,7 +1203,7 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dgr.put(16 * b + 4 * lg + r, c, pc[b][r]);
+            for (int r = 0; r < 4; ++r) dgr.put(16 * b + 4 * lg + r, cs, pc[b][r]);
         return;
     }
 #pragma unroll
