@@ -74,6 +74,15 @@ __device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 acc) {
     return acc;
 }
 
+// Round to nearest even by the conversion instruction (f32_to_bf16 tests for NaN with a
+// branch, which 48 stores per lane feel).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ uint16_t round_bf16(float a) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(a)); }
+
 // x of another lane of the same 16: lane 15 - i, 7 - i (in its eight), i ^ 2, i ^ 1
 template <int M> __device__ __forceinline__ float lane_across(float x) {
     constexpr int ctrl = M == 8 ? 0x140 : M == 4 ? 0x141 : M == 2 ? 0x4e : 0xb1;
@@ -131,19 +140,7 @@ template <int M> __device__ __forceinline__ void halve(float *v, int lane) {
 __device__ __forceinline__ void settle(f32x4 &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void settle(float &x) { asm volatile("" : "+v"(x)); }
 
-template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
-template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                 __uint_as_float(u.y & 0xffff0000u)};
-}
-template <typename T> __device__ __forceinline__ void store4(T *p, f32x4 x);
-template <> __device__ __forceinline__ void store4<float>(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
-template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
-    *reinterpret_cast<uint2 *>(p) = uint2{f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
-                                         f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)};
-}
+__device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
 __device__ __forceinline__ f32x4 ld4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 // four values `stride` apart
 __device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
@@ -243,16 +240,14 @@ template <typename T> struct Rows {
     __device__ void put(int tau, int c, float x) const {
         const int off = (tau * row + c) * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x), r, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(round_bf16(x), r, off, 0, 0);
     }
     __device__ void put4(int tau, int c, f32x4 x) const {
         const int off = (tau * row + c) * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32v4, x), r, off, 0, 0);
         } else {
-            __builtin_amdgcn_raw_buffer_store_b64(u32v2{f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
-                                                        f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)},
-                                                  r, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u32v2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, r, off, 0, 0);
         }
     }
 };
