@@ -409,21 +409,28 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         }
         // the scans' operands, from the staging tiles: whole blocks before (k, q with
         // their decay from the start) or behind (k with its decay to the end) come in
-        for (int i = w; i < NB * 4; i += NW) {
-            const int tt = i % NB, kk = i / NB, x = 16 * kk + 4 * lg;
-            f32x4 f0 = {1.f, 1.f, 1.f, 1.f}, f1 = f0;
-            for (int b = 0; b < tt; ++b) f0 *= ld4(&s.dec[b][64 * hf + x]);
-            for (int b = tt + 1; b < NB; ++b) f1 *= ld4(&s.dec[b][64 * hf + x]);
-            const int at = ((tt * (D / 16) + 4 * hf + kk) * 64 + l) * 4;
+        const int tt = w % NB;                          // this wavefront's token block
+        auto blocks = [&](auto d, auto &f0, auto &f1) {  // products of the blocks' decays before and behind it
+            const auto d0 = d(0), d1 = d(1), d2 = d(2), d3 = d(3);
+            typedef std::decay_t<decltype(f0)> F;
+            f0 = tt == 0 ? (F)1.f : tt == 1 ? d0 : tt == 2 ? d0 * d1 : d0 * d1 * d2;
+            f1 = tt == 3 ? (F)1.f : tt == 2 ? d3 : tt == 1 ? d2 * d3 : d1 * d2 * d3;
+        };
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            if (NW == 8 && (kk & 1) != w / NB) continue;
+            const int x = 16 * kk + 4 * lg, at = ((tt * (D / 16) + 4 * hf + kk) * 64 + l) * 4;
+            f32x4 f0, f1;
+            blocks([&](int b) { return ld4(&s.dec[b][64 * hf + x]); }, f0, f1);
             store4(rec + R::KDR + at, ld4(&s.X[0][16 * tt + lr][x]) * f0);
             store4(rec + R::KRR + at, ld4(&s.X[1][16 * tt + lr][x]) * f1);
         }
-        for (int i = w; i < NB * 4; i += NW) {
-            const int tt = i % NB, ct = i / NB, x = 16 * ct + lr;
-            float f0 = 1.f, f1 = 1.f;
-            for (int b = 0; b < tt; ++b) f0 *= s.dec[b][64 * hf + x];
-            for (int b = tt + 1; b < NB; ++b) f1 *= s.dec[b][64 * hf + x];
-            const int at = (((4 * hf + ct) * NB + tt) * 64 + l) * 4;
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) {
+            if (NW == 8 && (ct & 1) != w / NB) continue;
+            const int x = 16 * ct + lr, at = (((4 * hf + ct) * NB + tt) * 64 + l) * 4;
+            float f0, f1;
+            blocks([&](int b) { return s.dec[b][64 * hf + x]; }, f0, f1);
             store4(rec + R::KDT + at, ld4s(&s.X[0][16 * tt + 4 * lg][x], 64 + 4) * f0);
             store4(rec + R::KRT + at, ld4s(&s.X[1][16 * tt + 4 * lg][x], 64 + 4) * f1);
             store4(rec + R::QDT + at, ld4s(&s.X[2][16 * tt + 4 * lg][x], 64 + 4) * f0);
@@ -1089,9 +1096,6 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
             pq[b] += mfma16(row ? x.prow : zero, key, zero) * ei;
             pk[b] += mfma16(row ? x.arow : zero, key, zero) * ei;
             pc[b] += mfma16(col ? x.acol : zero, kv[b] * ei, mfma16(col ? x.pcol : zero, qv[b] * ei, zero)) * eo;
-            settle(pq[b]);
-            settle(pk[b]);
-            settle(pc[b]);
         }
         // inside the group: all in this lane
         f32x4 dp[3], da[3];                            // the group's rows
