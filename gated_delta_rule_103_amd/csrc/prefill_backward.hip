@@ -53,6 +53,7 @@
 #include "kda_device.h"
 #include "kda_launch.h"
 
+#include <cstddef>
 #include <type_traits>
 
 namespace kda {
@@ -241,6 +242,9 @@ template <typename T> struct Rows {
         const int off = (tau * row + c) * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
         else __builtin_amdgcn_raw_buffer_store_b16(round_bf16(x), r, off, 0, 0);
+    }
+    __device__ void put16(int tau, int c, u32v4 x) const {      // 16 bytes as they are
+        __builtin_amdgcn_raw_buffer_store_b128(x, r, (tau * row + c) * (int)sizeof(T), 0, 0);
     }
     __device__ void put4(int tau, int c, f32x4 x) const {
         const int off = (tau * row + c) * (int)sizeof(T);
@@ -796,7 +800,8 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     using R = Rec<D>;
     constexpr int NT = D / 16, NW = CH / 16, SM = NW / 4, STAGES = NT / (2 * SM), PO = sizeof(TG) == 2 ? 1 : 3;
     extern __shared__ char lds_raw[];
-    FinishLds<CH, PO> &s = *reinterpret_cast<FinishLds<CH, PO> *>(lds_raw);
+    typedef FinishLds<CH, PO> FinishLds_t;
+    FinishLds_t &s = *reinterpret_cast<FinishLds_t *>(lds_raw);
     Item it;
     const size_t item = blockIdx.x / (D / CH);
     const int part = blockIdx.x % (D / CH);
@@ -1159,17 +1164,6 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         }
         __syncthreads();
     }
-    int cs = c;                                        // or the loads' offsets are kept for the stores
-    asm volatile("" : "+v"(cs));
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tau = 16 * b + 4 * lg + r;
-            dqr.put(tau, cs, pq[b][r]);
-            dkr.put(tau, cs, pk[b][r]);
-        }
-    if (!dg) return;
     // dg_i = sum_{t >= i} row_t + sum_{t < i} out_t + all
     float after = 0.f, past = 0.f;
 #pragma unroll
@@ -1197,28 +1191,56 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) pc[b][r] = wiped >> (4 * b + r) & 1 ? 0.f : pc[b][r];
-    const Rows<float> dgr(dg, it, p.H, p.g_head ? 1 : D);
-    if (!p.g_head) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dgr.put(16 * b + 4 * lg + r, cs, pc[b][r]);
-        return;
-    }
+
+    // out through LDS, in whole rows of 16-byte stores
+    constexpr int SI = CH + 16 / (int)sizeof(TI), SG = CH + 4;
+    TI *sq = reinterpret_cast<TI *>(lds_raw), *sk = sq + C * SI;
+    float *sg = reinterpret_cast<float *>(sk + C * SI);
+    static_assert(2 * C * SI * sizeof(TI) + C * SG * sizeof(float) <= offsetof(FinishLds_t, rows), "staging");
+    __syncthreads();                                   // dP, dA and wait are done with
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float x = pc[b][r];
+            const int tau = 16 * b + 4 * lg + r, x = 16 * w + lr;
+            if constexpr (sizeof(TI) == 4) {
+                sq[tau * SI + x] = pq[b][r];
+                sk[tau * SI + x] = pk[b][r];
+            } else {
+                sq[tau * SI + x] = round_bf16(pq[b][r]);
+                sk[tau * SI + x] = round_bf16(pk[b][r]);
+            }
+            if (!p.g_head) {
+                sg[tau * SG + x] = pc[b][r];
+            } else {
+                float y = pc[b][r];
 #pragma unroll
-            for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m, 64);
-            if (lr == 0) s.rows[0][w][16 * b + 4 * lg + r] = x;
+                for (int m = 1; m < 16; m <<= 1) y += __shfl_xor(y, m, 64);
+                if (lr == 0) s.rows[0][w][tau] = y;
+            }
         }
     __syncthreads();
-    if (t < C) {
-        float x = 0.f;
-        for (int i = 0; i < NW; ++i) x += s.rows[0][i][t];
-        dgr.put(t, 0, x);
+    constexpr int PER = 16 / sizeof(TI), CHUNKS = CH / PER;         // elements of a store, stores of a row
+#pragma unroll
+    for (int i = 0; i < C * CHUNKS / (4 * CH); ++i) {
+        const int n = t + i * 4 * CH, tau = n / CHUNKS, x = (n % CHUNKS) * PER;
+        dqr.put16(tau, part * CH + x, *reinterpret_cast<const u32v4 *>(sq + tau * SI + x));
+        dkr.put16(tau, part * CH + x, *reinterpret_cast<const u32v4 *>(sk + tau * SI + x));
+    }
+    if (!dg) return;
+    const Rows<float> dgr(dg, it, p.H, p.g_head ? 1 : D);
+    if (p.g_head) {
+        if (t < C) {
+            float x = 0.f;
+            for (int i = 0; i < NW; ++i) x += s.rows[0][i][t];
+            dgr.put(t, 0, x);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = t + i * 4 * CH, tau = n / (CH / 4), x = (n % (CH / 4)) * 4;
+        dgr.put16(tau, part * CH + x, *reinterpret_cast<const u32v4 *>(sg + tau * SG + x));
     }
 }
 
