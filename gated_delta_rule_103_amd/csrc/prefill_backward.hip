@@ -142,6 +142,8 @@ __device__ __forceinline__ void settle(f32x4 &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void settle(float &x) { asm volatile("" : "+v"(x)); }
 
 __device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
+// what a later kernel reads, from memory by then
+__device__ __forceinline__ void store4_far(float *p, f32x4 x) { __builtin_nontemporal_store(x, reinterpret_cast<f32x4 *>(p)); }
 __device__ __forceinline__ f32x4 ld4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 // four values `stride` apart
 __device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
@@ -180,7 +182,7 @@ struct Common {
     SeqView sv;
     Ws ws;
     const float *g;
-    int H;
+    int H, slots;             // heads; workspace slots of a head, one per chunk
     bool g_head, qk_norm;
     float norm_eps;
 };
@@ -190,6 +192,8 @@ struct Common {
 struct Item {
     int Lc;
     size_t row0;
+    size_t slot;              // in the workspace: chunks of a head lie one behind the other, which
+                              // keeps a scan inside few memory pages
     __device__ bool find(const Common &p, size_t item) {
         const int ci = (int)(item / p.H), h = (int)(item % p.H);
         if (ci >= p.sv.total_chunks()) return false;
@@ -197,6 +201,7 @@ struct Item {
         const int s0 = p.sv.seq_start(n) + (ci - p.sv.first_chunk(n)) * C;
         Lc = min(C, p.sv.seq_end(n) - s0);
         row0 = (size_t)s0 * p.H + h;
+        slot = (size_t)h * p.slots + ci;
         return true;
     }
 };
@@ -292,7 +297,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     PrepLds<D> &s = *reinterpret_cast<PrepLds<D> *>(lds_raw);
     Item it;
     if (!it.find(p, blockIdx.x)) return;
-    float *rec = p.ws.rec + (size_t)blockIdx.x * R::SIZE;
+    float *rec = p.ws.rec + it.slot * R::SIZE;
     const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
     const int c = t % D, blk = t / D, ch = c % 64;
     const Rows<TI> qr(q, it, p.H, D), kr(k, it, p.H, D);
@@ -426,8 +431,8 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
             const int x = 16 * kk + 4 * lg, at = ((tt * (D / 16) + 4 * hf + kk) * 64 + l) * 4;
             f32x4 f0, f1;
             blocks([&](int b) { return ld4(&s.dec[b][64 * hf + x]); }, f0, f1);
-            store4(rec + R::KDR + at, ld4(&s.X[0][16 * tt + lr][x]) * f0);
-            store4(rec + R::KRR + at, ld4(&s.X[1][16 * tt + lr][x]) * f1);
+            store4_far(rec + R::KDR + at, ld4(&s.X[0][16 * tt + lr][x]) * f0);
+            store4_far(rec + R::KRR + at, ld4(&s.X[1][16 * tt + lr][x]) * f1);
         }
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
@@ -435,9 +440,9 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
             const int x = 16 * ct + lr, at = (((4 * hf + ct) * NB + tt) * 64 + l) * 4;
             float f0, f1;
             blocks([&](int b) { return s.dec[b][64 * hf + x]; }, f0, f1);
-            store4(rec + R::KDT + at, ld4s(&s.X[0][16 * tt + 4 * lg][x], 64 + 4) * f0);
-            store4(rec + R::KRT + at, ld4s(&s.X[1][16 * tt + 4 * lg][x], 64 + 4) * f1);
-            store4(rec + R::QDT + at, ld4s(&s.X[2][16 * tt + 4 * lg][x], 64 + 4) * f0);
+            store4_far(rec + R::KDT + at, ld4s(&s.X[0][16 * tt + 4 * lg][x], 64 + 4) * f0);
+            store4_far(rec + R::KRT + at, ld4s(&s.X[1][16 * tt + 4 * lg][x], 64 + 4) * f1);
+            store4_far(rec + R::QDT + at, ld4s(&s.X[2][16 * tt + 4 * lg][x], 64 + 4) * f0);
         }
     }
 #pragma unroll
@@ -554,67 +559,97 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         f32x4 ty;
 #pragma unroll
         for (int r = 0; r < 4; ++r) ty[r] = (row + r == col ? 1.f : 0.f) - s.b[row + r] * sum[r];
-        store4(rec + R::TYT + (i * 64 + l) * 4, ty);
-        store4(rec + R::PT + (i * 64 + l) * 4, ld4s(&s.P[i][4 * lg][lr], TP));
-        store4(rec + R::TE + (i * 64 + l) * 4, ld4(&X[i][lr][4 * lg]));
+        store4_far(rec + R::TYT + (i * 64 + l) * 4, ty);
+        store4_far(rec + R::PT + (i * 64 + l) * 4, ld4s(&s.P[i][4 * lg][lr], TP));
+        store4_far(rec + R::TE + (i * 64 + l) * 4, ld4(&X[i][lr][4 * lg]));
     }
     if (t < D) rec[R::GAM + t] = (s.dec[0][t] * s.dec[1][t]) * (s.dec[2][t] * s.dec[3][t]);
 }
 
 // ---- scan -----------------------------------------------------------------
 
-// A workgroup of four wavefronts carries 16 value channels (rows j of S, the
-// accumulators' rows) of one chain; wavefront w owns D / 4 key channels of S
-// and the w-th 16 tokens of a chunk.
-template <int D>
+// A workgroup of four wavefronts carries TV = 16 JT value channels (rows j of S,
+// the accumulators' rows) of one chain; wavefront w owns D / 4 key channels of S
+// and the w-th 16 tokens of a chunk. Left operands pass through LDS cut in three
+// bf16 parts; right operands come from the record and are cut in registers, once
+// for the JT tiles.
+template <int D, int TV, int PO>
 struct ScanLds {
-    float S[16][D + 4];       // the state, as an A operand
-    float R[16][LP];          // V - Kd M or dU
-    float U[16][LP];          // U or -dV
-    float O[2][16][LP];       // dO^T, two chunks in turn
+    uint16_t S[3][TV][D + 8];         // the state
+    uint16_t R[3][TV][C + 8];         // V - Kd M or dU
+    uint16_t U[3][TV][C + 8];         // U or -dV
+    uint16_t O[2][PO][TV][C + 8];     // dO^T, two chunks in turn
 };
+// Column of inner index k in those: the eight that a lane multiplies (of two
+// neighbouring 16-wide tiles, four each) lie together.
+__device__ __forceinline__ int inner(int k) { return (k & ~31) | (k & 12) << 1 | (k & 16) >> 2 | (k & 3); }
 
-template <int D, typename TI, typename TB, typename TG>
+template <int D, int TV, typename TI, typename TB, typename TG>
 __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__restrict__ v, const TB *__restrict__ beta,
-                                                   const TG *__restrict__ dout, const float *__restrict__ S0,
-                                                   const float *__restrict__ dS_out, float *__restrict__ dS0) {
+                                                      const TG *__restrict__ dout, const float *__restrict__ S0,
+                                                      const float *__restrict__ dS_out, float *__restrict__ dS0) {
     using R = Rec<D>;
+    constexpr int PO = sizeof(TG) == 2 ? 1 : 3, JT = TV / 16;
     constexpr int NT = D / 16, CT = D / 64;      // value tiles of a chain, key tiles of a wavefront
-    __shared__ ScanLds<D> s;
+    __shared__ __align__(16) ScanLds<D, TV, PO> s;
     // The tiles of a chain, which read the same records, run on one XCD (workgroups
     // go to the eight XCDs in turn); the backward scans, which are longer, come first.
-    const int per_dir = gridDim.x / 16, slot = blockIdx.x / 8, jt = slot % NT;
+    const int per_dir = gridDim.x / 16, slot = blockIdx.x / 8;
     const bool back = slot < per_dir;
-    const int chain = (back ? slot : slot - per_dir) / NT * 8 + blockIdx.x % 8;
+    const int chain = (back ? slot : slot - per_dir) / (D / TV) * 8 + blockIdx.x % 8;
     if (chain >= p.sv.N * p.H) return;
     const int n = chain / p.H, h = chain % p.H;
     const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
-    const int j0 = 16 * jt, jr = j0 + 4 * lg;    // this lane's first accumulator row
+    const int j0 = slot % (D / TV) * TV, jt = j0 / 16;   // the workgroup's first value channel and tile
+    const int jr = j0 + 4 * lg;                          // this lane's first accumulator row
     const int begin = p.sv.seq_start(n), len = p.sv.seq_end(n) - begin, chunks = (len + C - 1) / C;
-    const size_t item0 = (size_t)p.sv.first_chunk(n) * p.H + h;
+    const size_t item0 = (size_t)h * p.slots + p.sv.first_chunk(n);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     auto key = [&](int i) { return (w * CT + i) * 16 + lr; };
 
-    f32x4 st[CT];
+    f32x4 st[JT][CT];
     const float *init = back ? dS_out : S0;
     const size_t state0 = ((size_t)n * p.H + h) * D;
 #pragma unroll
-    for (int i = 0; i < CT; ++i)
+    for (int y = 0; y < JT; ++y)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) st[i][r] = init ? init[(state0 + jr + r) * D + key(i)] : 0.f;
+        for (int i = 0; i < CT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st[y][i][r] = init ? init[(state0 + jr + 16 * y + r) * D + key(i)] : 0.f;
 
     // Operands of a chunk stay in registers from a chunk ahead: each set is
     // loaded again as soon as its products are done, and the other phases of the
     // chunk cover the latency.
-    const int tau = 16 * w + lr;                 // this lane's token where tokens are columns
-    auto item_of = [&](int step) { return item0 + (size_t)(back ? chunks - 1 - step : step) * p.H; };
+    const int tau = 16 * w + lr, tau_col = inner(tau);   // this lane's token where tokens are columns
+    auto item_of = [&](int step) { return item0 + (back ? chunks - 1 - step : step); };
+    // an accumulator (rows 4 lg + r of tile y) into column `col` of an LDS matrix
+    auto put = [&](auto &m, int y, int col, f32x4 x) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float f = x[r];
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+                const uint32_t u = __float_as_uint(f);
+                m[z][16 * y + 4 * lg + r][col] = static_cast<uint16_t>(u >> 16);
+                f -= __uint_as_float(u & 0xffff0000u);
+            }
+        }
+    };
+    // rows of tile y as a left operand over the inner indices 32 m ..
+    auto left = [&](auto &m, int y, int at, auto &a) {
+#pragma unroll
+        for (int z = 0; z < (int)(sizeof(a) / sizeof(a[0])); ++z)
+            a[z] = *reinterpret_cast<const u32v4 *>(&m[z][16 * y + lr][32 * at + 8 * lg]);
+    };
     auto put_state = [&](size_t item) {
         float *Mw = (back ? p.ws.dM : p.ws.M) + item * D * D;
 #pragma unroll
-        for (int i = 0; i < CT; ++i) {
-            store4(Mw + (((w * CT + i) * NT + jt) * 64 + l) * 4, st[i]);
+        for (int y = 0; y < JT; ++y)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.S[4 * lg + r][key(i)] = st[i][r];
-        }
+            for (int i = 0; i < CT; ++i) {
+                store4_far(Mw + (((w * CT + i) * NT + jt + y) * 64 + l) * 4, st[y][i]);
+                put(s.S, y, inner(key(i)), st[y][i]);
+            }
     };
     auto rows_of = [&](f32x4(&x)[D / 16], const float *m) {           // this wavefront's tokens, all channels
 #pragma unroll
@@ -632,26 +667,77 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
     };
     auto chunk_of = [&](int step) {
         const int ci = back ? chunks - 1 - step : step;
-        return Item{min(C, len - ci * C), (size_t)(begin + ci * C) * p.H + h};
+        return Item{min(C, len - ci * C), (size_t)(begin + ci * C) * p.H + h, item0 + ci};
     };
     auto beta_of = [&](const Item &it) { return Rows<TB>(beta, it, p.H, 1).raw(tau, 0); };
+    // state times rows: S Kd^T or dS Kr^T, for this wavefront's tokens
+    auto times_rows = [&](const f32x4(&x)[D / 16], f32x4(&acc)[JT]) {
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+            u32v4 b[3];
+            split3(x[2 * m], x[2 * m + 1], b);
+#pragma unroll
+            for (int y = 0; y < JT; ++y) {
+                u32v4 a[3];
+                left(s.S, y, m, a);
+                acc[y] = product(a, b, acc[y]);
+            }
+        }
+    };
+    // a matrix over tokens times a triangular one: the pairs of token blocks that
+    // have a block at or before (behind) this wavefront's
+    auto times_tri = [&](auto &mat, const f32x4(&x)[NB], f32x4(&acc)[JT], auto parts) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (back ? 2 * m + 1 >= w : 2 * m <= w) {
+                u32v4 b[3];
+                split3(x[2 * m], x[2 * m + 1], b);
+#pragma unroll
+                for (int y = 0; y < JT; ++y) {
+                    u32v4 a[decltype(parts)::value];
+                    left(mat, y, m, a);
+                    acc[y] = product(a, b, acc[y]);
+                }
+            }
+    };
+    // its product over the tokens with this wavefront's channels, onto the state
+    auto onto_state = [&](auto &mat, const f32x4(&x)[CT][NB], auto parts) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            u32v4 a[JT][decltype(parts)::value];
+#pragma unroll
+            for (int y = 0; y < JT; ++y) left(mat, y, m, a[y]);
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                u32v4 b[3];
+                split3(x[i][2 * m], x[i][2 * m + 1], b);
+#pragma unroll
+                for (int y = 0; y < JT; ++y) st[y][i] = product(a[y], b, st[y][i]);
+            }
+        }
+    };
+    typedef std::integral_constant<int, 3> Three;
     if (chunks == 0) {
     } else if (!back) {
-        f32x4 kd[D / 16], te[NB], kr[CT][NB];
+        f32x4 kd[D / 16], te[NB] = {zero, zero, zero, zero}, kr[CT][NB];
         float gam[CT];
-        typename Rows<TI>::Raw4 vt;
+        typename Rows<TI>::Raw4 vt[JT];
         typename Rows<TB>::Raw b;
-        auto v_of = [&](const Item &it) { return Rows<TI>(v, it, p.H, D).raw4(tau, jr); };
-        auto te_of = [&](const float *rec) {
+        auto v_of = [&](const Item &it) {
+            const Rows<TI> r(v, it, p.H, D);
+#pragma unroll
+            for (int y = 0; y < JT; ++y) vt[y] = r.raw4(tau, jr + 16 * y);
+        };
+        auto te_of = [&](const float *rec) {               // blocks behind w stay zero
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
                 if (kk <= w) te[kk] = ld4(rec + R::TE + (tile_of(w, kk) * 64 + l) * 4);
         };
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
-            rows_of(kd, rec + R::KDR);
             const Item it = chunk_of(0);
-            vt = v_of(it);
+            rows_of(kd, rec + R::KDR);
+            v_of(it);
             te_of(rec);
             b = beta_of(it);
             cols_of(kr, rec + R::KRT);
@@ -664,41 +750,45 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
             put_state(item);
             __syncthreads();
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
+            f32x4 acc[JT], e[JT];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kd[kk], acc);
+            for (int y = 0; y < JT; ++y) acc[y] = e[y] = zero;
+            times_rows(kd, acc);
             rows_of(kd, rec + R::KDR);
-            acc = Rows<TI>::value4(vt) - acc;
-            vt = v_of(it);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.R[4 * lg + r][tau] = acc[r];
+            for (int y = 0; y < JT; ++y) put(s.R, y, tau_col, Rows<TI>::value4(vt[y]) - acc[y]);
+            v_of(it);
             __syncthreads();
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk)
-                if (kk <= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), te[kk], e);
+            times_tri(s.R, te, e, Three{});
             te_of(rec);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = Rows<TB>::value(b) * e[r];
-            store4(p.ws.E + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
+            for (int y = 0; y < JT; ++y) {
+                put(s.U, y, tau_col, e[y] * Rows<TB>::value(b));
+                store4_far(p.ws.E + item * C * D + ((w * NT + jt + y) * 64 + l) * 4, e[y]);
+            }
             b = beta_of(it);
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                st[i] *= gam[i];
+            for (int i = 0; i < CT; ++i)
 #pragma unroll
-                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kr[i][kk], st[i]);
-            }
+                for (int y = 0; y < JT; ++y) st[y][i] *= gam[i];
+            onto_state(s.U, kr, Three{});
             cols_of(kr, rec + R::KRT);
             gam_of(gam, rec);
         }
     } else {
-        f32x4 kr[D / 16], pt[NB], ty[NB], qd[CT][NB], kd[CT][NB];
+        f32x4 kr[D / 16], pt[NB] = {zero, zero, zero, zero}, ty[NB] = {zero, zero, zero, zero}, qd[CT][NB], kd[CT][NB];
         float gam[CT];
-        typename Rows<TG>::Raw4 ov;
+        typename Rows<TG>::Raw4 ov[JT];
         typename Rows<TB>::Raw b;
-        const int ot = t / 4, oj = (t % 4) * 4;
-        auto o_of = [&](const Item &it) { return Rows<TG>(dout, it, p.H, D).raw4(ot, j0 + oj); };
-        auto upper_of = [&](f32x4(&x)[NB], const float *m) {
+        typedef std::integral_constant<int, PO> Parts;
+        const int ot = t / 4, oj = t % 4 * 4;
+        auto o_of = [&](const Item &it) {
+            const Rows<TG> r(dout, it, p.H, D);
+#pragma unroll
+            for (int y = 0; y < JT; ++y) ov[y] = r.raw4(ot, j0 + 16 * y + oj);
+        };
+        auto upper_of = [&](f32x4(&x)[NB], const float *m) {   // blocks before w stay zero
 #pragma unroll
             for (int kk = 0; kk < NB; ++kk)
                 if (kk >= w) x[kk] = ld4(m + (tile_of(kk, w) * 64 + l) * 4);
@@ -706,7 +796,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
             const Item it = chunk_of(0);
-            ov = o_of(it);
+            o_of(it);
             rows_of(kr, rec + R::KRR);
             upper_of(pt, rec + R::PT);
             cols_of(qd, rec + R::QDT);
@@ -720,53 +810,64 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             const Item it = chunk_of(next);
             const size_t item = item_of(step);
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
-            float(*O)[LP] = s.O[step & 1];
+            auto &O = s.O[step & 1];
             put_state(item);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) O[oj + r][ot] = Rows<TG>::value4(ov)[r];
-            ov = o_of(it);
+            for (int y = 0; y < JT; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (PO == 1) {
+                        O[0][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(ov[y][r / 2] >> 16 * (r % 2));
+                    } else {
+                        float f = Rows<TG>::value4(ov[y])[r];
+#pragma unroll
+                        for (int z = 0; z < 3; ++z) {
+                            const uint32_t u = __float_as_uint(f);
+                            O[z][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(u >> 16);
+                            f -= __uint_as_float(u & 0xffff0000u);
+                        }
+                    }
+                }
+            o_of(it);
             __syncthreads();
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, e = acc;
+            f32x4 acc[JT], e[JT];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) acc = mfma16(ld4(&s.S[lr][16 * kk + 4 * lg]), kr[kk], acc);
+            for (int y = 0; y < JT; ++y) acc[y] = e[y] = zero;
+            times_rows(kr, acc);
             rows_of(kr, rec + R::KRR);
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk)
-                if (kk >= w) acc = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), pt[kk], acc);
+            times_tri(O, pt, acc, Parts{});
             upper_of(pt, rec + R::PT);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s.R[4 * lg + r][tau] = acc[r];
+            for (int y = 0; y < JT; ++y) put(s.R, y, tau_col, acc[y]);
             // dO's share of the new state waits for nothing
-#pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                st[i] *= gam[i];
-#pragma unroll
-                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&O[lr][16 * kk + 4 * lg]), qd[i][kk], st[i]);
-            }
-            cols_of(qd, rec + R::QDT);
-            gam_of(gam, rec);
-            __syncthreads();
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk)
-                if (kk >= w) e = mfma16(ld4(&s.R[lr][16 * kk + 4 * lg]), ty[kk], e);
-            upper_of(ty, rec + R::TYT);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s.U[4 * lg + r][tau] = -Rows<TB>::value(b) * e[r];
-            store4(p.ws.Y + item * C * D + ((w * NT + jt) * 64 + l) * 4, e);
-            b = beta_of(it);
-            __syncthreads();
 #pragma unroll
             for (int i = 0; i < CT; ++i)
 #pragma unroll
-                for (int kk = 0; kk < NB; ++kk) st[i] = mfma16(ld4(&s.U[lr][16 * kk + 4 * lg]), kd[i][kk], st[i]);
+                for (int y = 0; y < JT; ++y) st[y][i] *= gam[i];
+            onto_state(O, qd, Parts{});
+            cols_of(qd, rec + R::QDT);
+            gam_of(gam, rec);
+            __syncthreads();
+            times_tri(s.R, ty, e, Three{});
+            upper_of(ty, rec + R::TYT);
+#pragma unroll
+            for (int y = 0; y < JT; ++y) {
+                put(s.U, y, tau_col, e[y] * -Rows<TB>::value(b));
+                store4_far(p.ws.Y + item * C * D + ((w * NT + jt + y) * 64 + l) * 4, e[y]);
+            }
+            b = beta_of(it);
+            __syncthreads();
+            onto_state(s.U, kd, Three{});
             cols_of(kd, rec + R::KDT);
         }
     }
     if (back && dS0)
 #pragma unroll
-        for (int i = 0; i < CT; ++i)
+        for (int y = 0; y < JT; ++y)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dS0[(state0 + jr + r) * D + key(i)] = st[i][r];
+            for (int i = 0; i < CT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dS0[(state0 + jr + 16 * y + r) * D + key(i)] = st[y][i][r];
 }
 
 // ---- finish ---------------------------------------------------------------
@@ -797,15 +898,15 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
                                                           TI *__restrict__ dq, TI *__restrict__ dk,
                                                           TI *__restrict__ dv, float *__restrict__ dg,
                                                           TB *__restrict__ dbeta) {
-    using R = Rec<D>;
     constexpr int NT = D / 16, NW = CH / 16, SM = NW / 4, STAGES = NT / (2 * SM), PO = sizeof(TG) == 2 ? 1 : 3;
+    using R = Rec<D>;
     extern __shared__ char lds_raw[];
     typedef FinishLds<CH, PO> FinishLds_t;
     FinishLds_t &s = *reinterpret_cast<FinishLds_t *>(lds_raw);
     Item it;
-    const size_t item = blockIdx.x / (D / CH);
     const int part = blockIdx.x % (D / CH);
-    if (!it.find(p, item)) return;
+    if (!it.find(p, blockIdx.x / (D / CH))) return;
+    const size_t item = it.slot;
     const float *rec = p.ws.rec + item * R::SIZE, *M = p.ws.M + item * D * D, *dM = p.ws.dM + item * D * D;
     const float *E = p.ws.E + item * C * D, *Y = p.ws.Y + item * C * D;
     const int t = threadIdx.x, w = t / 64, l = t % 64, lr = l % 16, lg = l / 16;
@@ -1267,6 +1368,7 @@ size_t carve(int N, long long T_total, int H, char *base, Ws *ws) {
 
 template <int D, typename TI, typename TB, typename TG>
 hipError_t launch_t(const PrefillBackwardArgs &a) {
+    constexpr int PO = sizeof(TG) == 2 ? 1 : 3;
     Ws ws;
     carve<D>(a.N, (long long)a.B * a.T, a.H, static_cast<char *>(a.ws), &ws);
     if (a.cu_seqlens) {
@@ -1274,14 +1376,13 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
         if (e != hipSuccess) return e;
     }
     const SeqView sv{a.cu_seqlens, ws.chunk_off, a.N, a.T, C};
-    const Common p{sv, ws, a.g, a.H, a.g_head, a.qk_norm, a.norm_eps};
     const long long chunks = a.cu_seqlens ? max_chunks(a.N, a.T, C) : (long long)a.N * ((a.T + C - 1) / C);
+    const Common p{sv, ws, a.g, a.H, (int)chunks, a.g_head, a.qk_norm, a.norm_eps};
     const unsigned items = static_cast<unsigned>(chunks * a.H);
     const TI *q = static_cast<const TI *>(a.q), *k = static_cast<const TI *>(a.k), *v = static_cast<const TI *>(a.v);
     const TB *beta = static_cast<const TB *>(a.beta);
     const TG *dout = static_cast<const TG *>(a.dout);
     const auto prep = prep_kernel<D, TI, TB>;
-    constexpr int PO = sizeof(TG) == 2 ? 1 : 3;
     // sums over a row's channels need the whole row in one workgroup
     const bool whole = D == 64 || a.qk_norm || a.g_head;
     const auto finish = whole ? finish_kernel<D, D, TI, TB, TG> : finish_kernel<D, 64, TI, TB, TG>;
@@ -1299,8 +1400,20 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
         if (e != hipSuccess) return e;
     }
     const unsigned groups = (static_cast<unsigned>(a.N * a.H) + 7) / 8;
-    hipLaunchKernelGGL((scan_kernel<D, TI, TB, TG>), dim3(2 * groups * 8 * (D / 16)), dim3(256), 0, a.stream, p, v, beta,
-                       dout, a.S0, a.dS_out, a.dS0);
+    // 32 value channels per workgroup load each operand half as often, but leave one
+    // workgroup a CU at half the chains: they win where two fit on every CU
+    // (8 x 1024 tokens x 32 heads: 1150 against 1293 us for the whole call; one
+    // sequence of 8192, one workgroup a CU: 1285 and 1296) and, since the longest of
+    // packed sequences decides when a CU is free, three for those (64 chains of 1 to
+    // 2048 tokens: 311 against 268 us; 96: 399 and 406).
+    int dev = 0, cus = 0;
+    if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
+    if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
+    const long long wide = 2ll * a.N * a.H * (D / 32);
+    const int tv = wide >= (a.cu_seqlens && a.N > 1 ? 3ll : 2ll) * cus ? 32 : 16;
+    const auto scan = tv == 32 ? scan_kernel<D, 32, TI, TB, TG> : scan_kernel<D, 16, TI, TB, TG>;
+    hipLaunchKernelGGL(scan, dim3(2 * groups * 8 * (D / tv)), dim3(256), 0, a.stream, p, v, beta, dout, a.S0,
+                       a.dS_out, a.dS0);
     e = hipGetLastError();
     if (e != hipSuccess || items == 0) return e;
     hipLaunchKernelGGL(finish, dim3(items * (D / ch)), dim3(4 * ch), finish_lds, a.stream, p, q, k, beta, dout,

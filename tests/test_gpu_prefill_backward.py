@@ -226,3 +226,10 @@ def test_refusals():
         kda_prefill_backward(d.q, d.k, d.v, d.g, d.beta, do, qk_l2norm=True, l2norm_eps=0.0)
     with pytest.raises(ValueError, match="dg must be None"):
         gdn_prefill_backward(d.q, d.k, d.v, None, d.beta, do, dg=d.g[..., 0].contiguous())
+
+
+@pytest.mark.parametrize("D,io", [(128, "bf16"), (128, "f32"), (64, "bf16")])
+def test_many_chains(D, io):
+    """Enough chains for the scan that takes 32 value channels a workgroup, dense and packed."""
+    run(H=40 if D == 128 else 80, D=D, B=4, T=70, io=io, shift=-1.0, seed=18)
+    run(H=40 if D == 128 else 80, D=D, lengths=[70, 1, 0, 33, 64, 10], io=io, shift=-1.0, seed=19)
