@@ -496,21 +496,24 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
                       stream, qk_l2norm, l2norm_eps):
     lib = load_library()
     g_head = entry == "gdn_prefill_backward"
-    _check_prefill(q, k, v, g, beta, S0, None, dS_out, cu_seqlens, workspace, g_head)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q must be a 4-D tensor [B, T, H, Dk] and v [B, T, H, Dv]")
     B, T, H, Dk = q.shape
     Dv = v.shape[-1]
-    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    N = B if not isinstance(cu_seqlens, torch.Tensor) else cu_seqlens.numel() - 1
     _expect(dout, "dout", (B, T, H, Dv), _FLOAT_IO)
+    _expect(dS_out, "dS_out", (N, H, Dv, Dk), (torch.float32,), optional=True)
     for name, grad, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dbeta", dbeta, beta)):
-        _expect(grad, name, like.shape, (like.dtype,), optional=True)
-    if g is None:
-        if dg is not None:
-            raise ValueError("dg must be None when there is no gate")
-    else:
-        _expect(dg, "dg", g.shape, (torch.float32,), optional=True)
+        if grad is not None:
+            _expect(like, name[1:], getattr(like, "shape", None), _FLOAT_IO)
+            _expect(grad, name, like.shape, (like.dtype,))
+    if g is None and dg is not None:
+        raise ValueError("dg must be None when there is no gate")
+    if dg is not None:
+        _expect(dg, "dg", g.shape, (torch.float32,))
     _expect(dS0, "dS0", (N, H, Dv, Dk), (torch.float32,), optional=True)
-    dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, dout=dout, S0=S0, dS_out=dS_out, cu_seqlens=cu_seqlens, dq=dq,
-                    dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0, workspace=workspace)
+    _check_prefill(q, k, v, g, beta, S0, None, None, cu_seqlens, workspace, g_head)
+    dev = _same_gpu(q=q, dout=dout, dS_out=dS_out, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0)
     with _on(dev):
         dq, dk, dv, dbeta = (torch.empty_like(like) if x is None else x
                              for x, like in ((dq, q), (dk, k), (dv, v), (dbeta, beta)))

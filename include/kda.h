@@ -436,7 +436,7 @@ int kda_layer_norm(const void *x, const float *weight, const float *bias, void *
  *   dweight, dbias  [W] fp32, or NULL to skip
  * The sums over rows have a fixed order. rows == 0 gives zeros. No gradient may be
  * any other buffer of the call. Sizes and alignment as for kda_layer_norm.
- * workspace: kda_layer_norm_backward_workspace_size bytes (at most 8 KiB x W),
+ * workspace: kda_layer_norm_backward_workspace_size bytes (at most 4 KiB x W),
  * 256-byte aligned; may be NULL when dweight and dbias are.
  */
 size_t kda_layer_norm_backward_workspace_size(int rows, int W);
