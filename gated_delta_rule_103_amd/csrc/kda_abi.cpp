@@ -406,7 +406,7 @@ int kda_layer_norm(const void *x, const float *weight, const float *bias, void *
     if (rows > 0 && out == x && out_dtype != x_dtype) return KDA_ERR_INVALID_ARG;
     if (among(out, weight, bias, mean, rstd) || among(mean, x, weight, bias, rstd) || among(rstd, x, weight, bias))
         return KDA_ERR_INVALID_ARG;
-    if (W > kda::kMaxNormWidth || !kda::layer_norm_fits(rows, W)) return KDA_ERR_UNSUPPORTED;
+    if (W > kda::kMaxNormWidth) return KDA_ERR_UNSUPPORTED;
     kda::LayerNormArgs a;
     a.x = x; a.weight = weight; a.bias = bias; a.out = out; a.mean = mean; a.rstd = rstd;
     a.rows = rows; a.W = W; a.eps = eps; a.rms = rms != 0;

@@ -180,7 +180,6 @@ hipError_t launch_output_gate_backward(const OutputGateBackwardArgs &a);
 
 // layer norm and RMS norm of rows of at most kMaxNormWidth channels, and the gradient.
 constexpr int kMaxNormWidth = 16384;
-bool layer_norm_fits(int rows, int W);     // a launch has fewer than 2^32 threads
 hipError_t launch_layer_norm(const LayerNormArgs &a);
 size_t layer_norm_backward_workspace(int rows, int W);
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs &a);

@@ -83,55 +83,6 @@ __device__ __forceinline__ float row_sum(float x, float *part, int wave_in_row) 
     return x;
 }
 
-template <int NW, int K, bool VEC, typename TI, typename TO>
-__global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_kernel(const TI *__restrict__ x, const float *__restrict__ w,
-                                                                      const float *__restrict__ b, TO *__restrict__ y,
-                                                                      float *__restrict__ mean_out,
-                                                                      float *__restrict__ rstd_out, int rows, int W,
-                                                                      float eps, bool rms) {
-    using S = Shape<NW, K>;
-    __shared__ float part[NW];
-    const int t = threadIdx.x % S::SPAN, wave = t / 64;
-    const int r = blockIdx.x * S::ROWS + threadIdx.x / S::SPAN;
-    if (NW == 1 && r >= rows) return;          // whole wavefronts; NW > 1 has one row per workgroup
-    const TI *row = x + (size_t)r * W;
-    constexpr int STEP = VEC ? 1 : S::SPAN;
-    f32x8 v[K];
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        v[k] = load8<VEC>(row, first_channel<VEC, S::SPAN>(t, k), STEP, W);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[k][i];
-    }
-    const float inv = 1.f / W;
-    const float mean = rms ? 0.f : row_sum<NW>(s, part, wave) * inv;
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = first_channel<VEC, S::SPAN>(t, k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = c + i * STEP < W ? v[k][i] - mean : 0.f;
-            v[k][i] = d;
-            ss += d * d;
-        }
-    }
-    const float rstd = 1.f / sqrtf(row_sum<NW>(ss, part, wave) * inv + eps);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = first_channel<VEC, S::SPAN>(t, k);
-        f32x8 o = v[k] * rstd;
-        if (w) o *= load8<VEC>(w, c, STEP, W);
-        if (b) o += load8<VEC>(b, c, STEP, W);
-        store8<VEC>(y + (size_t)r * W, c, STEP, W, o);
-    }
-    if (t == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
-    }
-}
-
 // One group of eight channels as it lies in memory, so that a row can be loaded
 // ahead in half the registers.
 template <bool VEC, typename T> struct Group {
@@ -155,6 +106,70 @@ template <bool VEC, typename T> struct Group {
         }
     }
 };
+
+// A workgroup takes every gridDim.x-th row (group of ROWS rows) and loads the next
+// while it reduces one.
+template <int NW, int K, bool VEC, typename TI, typename TO>
+__global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_kernel(const TI *x, const float *__restrict__ w,
+                                                                      const float *__restrict__ b, TO *y,
+                                                                      float *__restrict__ mean_out,
+                                                                      float *__restrict__ rstd_out, int rows, int W,
+                                                                      float eps, bool rms) {
+    using S = Shape<NW, K>;
+    __shared__ float part[NW];
+    const int t = threadIdx.x % S::SPAN, wave = t / 64;
+    constexpr int STEP = VEC ? 1 : S::SPAN;
+    const float inv = 1.f / W;
+    const long long stride = (long long)gridDim.x * S::ROWS;
+    long long r = (long long)blockIdx.x * S::ROWS + threadIdx.x / S::SPAN;
+    Group<VEC, TI> ahead[K];
+    auto fetch = [&](long long row) {
+        if (row >= rows) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k) ahead[k].load(x + (size_t)row * W, first_channel<VEC, S::SPAN>(t, k), STEP, W);
+    };
+    fetch(r);
+    // NW > 1: one row per pass, so every thread makes the same number of passes
+    for (; r < rows; r += stride) {
+        f32x8 v[K];
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = ahead[k].value();
+        fetch(r + stride);
+        float mean = 0.f;
+        if (!rms) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += v[k][i];
+            mean = row_sum<NW>(s, part, wave) * inv;
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = first_channel<VEC, S::SPAN>(t, k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = c + i * STEP < W ? v[k][i] - mean : 0.f;
+                v[k][i] = d;
+                ss += d * d;
+            }
+        }
+        const float rstd = 1.f / sqrtf(row_sum<NW>(ss, part, wave) * inv + eps);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = first_channel<VEC, S::SPAN>(t, k);
+            f32x8 o = v[k] * rstd;
+            if (w) o *= load8<VEC>(w, c, STEP, W);
+            if (b) o += load8<VEC>(b, c, STEP, W);
+            store8<VEC>(y + (size_t)r * W, c, STEP, W, o);
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+    }
+}
 
 // dw_part, db_part: [gridDim.x][W], null when that gradient is not wanted. The next
 // row is loaded while the current one is reduced; both of a row's sums cross the
@@ -283,7 +298,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
 
 // rows of the partial sums: as many workgroups as keep the card busy, never
 // more than there are rows for
+// and one for a few rows, whose sums then are the gradients themselves
 int partial_rows(long long rows, int rows_per_wg) {
+    if (rows > 0 && rows <= 4 * rows_per_wg) return 1;
     const long long wgs = (rows + rows_per_wg - 1) / rows_per_wg;
     return static_cast<int>(wgs < 512 ? wgs : 512);
 }
@@ -304,13 +321,16 @@ bool aligned16(const void *a, const void *b, const void *c, const void *d) {
              reinterpret_cast<uintptr_t>(d)) & 15u) == 0;
 }
 
+constexpr int FORWARD_GRID = 2048;
+
 template <typename TI, typename TO, bool VEC>
 struct Forward {
     const LayerNormArgs &a;
     template <int NW, int K>
     hipError_t operator()() const {
         using S = Shape<NW, K>;
-        const unsigned grid = static_cast<unsigned>((a.rows + (long long)S::ROWS - 1) / S::ROWS);
+        const long long groups = (a.rows + (long long)S::ROWS - 1) / S::ROWS;
+        const unsigned grid = static_cast<unsigned>(groups < FORWARD_GRID ? groups : FORWARD_GRID);
         hipLaunchKernelGGL((norm_kernel<NW, K, VEC, TI, TO>), dim3(grid), dim3(S::THREADS), 0, a.stream,
                            static_cast<const TI *>(a.x), a.weight, a.bias, static_cast<TO *>(a.out), a.mean, a.rstd,
                            a.rows, a.W, a.eps, a.rms);
@@ -325,8 +345,8 @@ struct Backward {
     hipError_t operator()() const {
         using S = Shape<NW, K>;
         const int G = partial_rows(a.rows, S::ROWS);
-        float *dwp = a.dweight ? a.ws : nullptr;
-        float *dbp = a.dbias ? a.ws + (a.dweight ? (size_t)G * a.W : 0) : nullptr;
+        float *dwp = !a.dweight ? nullptr : G == 1 ? a.dweight : a.ws;
+        float *dbp = !a.dbias ? nullptr : G == 1 ? a.dbias : a.ws + (a.dweight ? (size_t)G * a.W : 0);
         if (G > 0) {
             hipLaunchKernelGGL((norm_backward_kernel<NW, K, VEC, TI, TG>), dim3(G), dim3(S::THREADS), 0, a.stream,
                                static_cast<const TI *>(a.x), static_cast<const TG *>(a.dy), a.rms ? nullptr : a.mean,
@@ -334,7 +354,7 @@ struct Backward {
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
-        if (!a.dweight && !a.dbias) return hipSuccess;
+        if (G == 1 || (!a.dweight && !a.dbias)) return hipSuccess;
         hipLaunchKernelGGL(column_sum_kernel, dim3((a.W + 63) / 64, 2), dim3(1024), 0, a.stream, dwp, a.dweight, dbp,
                            a.dbias, G, a.W);
         return hipGetLastError();
@@ -344,13 +364,9 @@ struct Backward {
 }  // namespace
 
 size_t layer_norm_backward_workspace(int rows, int W) {
-    // at most 512 partial rows of each gradient, whichever shape is taken
-    return 2 * sizeof(float) * (size_t)partial_rows(rows, 1) * W;
-}
-
-bool layer_norm_fits(int rows, int W) {
-    const unsigned long long threads = W <= 1024 ? 64 : W <= 4096 ? 256 : W <= 8192 ? 512 : 1024;   // per row
-    return ((unsigned long long)rows + 3) * threads < (1ull << 32);
+    // partial rows of each gradient: no shape has more than the one with a row per workgroup
+    const int G = partial_rows(rows, 1);
+    return G == 1 ? 0 : 2 * sizeof(float) * (size_t)G * W;
 }
 
 hipError_t launch_layer_norm(const LayerNormArgs &a) {
@@ -366,7 +382,7 @@ hipError_t launch_layer_norm(const LayerNormArgs &a) {
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs &a) {
-    const bool vec = a.W % 8 == 0 && aligned16(a.x, a.dy, a.dx, a.weight);
+    const bool vec = a.W % 8 == 0 && aligned16(a.x, a.dy, a.dx, a.weight) && aligned16(a.dweight, a.dbias, nullptr, nullptr);
     auto run = [&](auto in, auto grad) {
         using TI = decltype(in);
         using TG = decltype(grad);

@@ -100,8 +100,11 @@ __global__ __launch_bounds__(DW_CH *DW_STRANDS) void dweight_kernel(const float 
     }
 }
 
+// Workgroups of a launch. A few rows are one workgroup's, whose sum is dw itself: a
+// second launch would cost more than the four turns of its loop.
 int parts(long long rowheads, int Dv) {
     const int rpb = THREADS / (Dv / 8);
+    if (rowheads > 0 && rowheads <= 4 * rpb) return 1;
     const long long g = (rowheads + rpb - 1) / rpb;
     return static_cast<int>(g < MAX_PARTS ? g : MAX_PARTS);
 }
@@ -114,11 +117,12 @@ hipError_t launch_t(const OutputGateBackwardArgs &a) {
         hipLaunchKernelGGL((output_gate_backward_kernel<DV, TO, TZ, TG>), dim3(G), dim3(THREADS), 0, a.stream,
                            static_cast<const TO *>(a.o), static_cast<const TZ *>(a.gate),
                            static_cast<const TG *>(a.dout), a.weight, static_cast<TO *>(a.do_),
-                           static_cast<TZ *>(a.dgate), a.dweight ? a.ws : nullptr, rowheads, a.eps);
+                           static_cast<TZ *>(a.dgate), G == 1 ? a.dweight : a.dweight ? a.ws : nullptr, rowheads,
+                           a.eps);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (!a.dweight) return hipSuccess;
+    if (!a.dweight || G == 1) return hipSuccess;
     hipLaunchKernelGGL(dweight_kernel, dim3(DV / DW_CH), dim3(DW_CH * DW_STRANDS), 0, a.stream, a.ws, a.dweight, G, DV);
     return hipGetLastError();
 }
@@ -141,7 +145,8 @@ hipError_t launch_o(const OutputGateBackwardArgs &a) {
 }  // namespace
 
 size_t output_gate_backward_workspace(long long rowheads, int Dv) {
-    return sizeof(float) * (size_t)parts(rowheads, Dv) * Dv;
+    const int G = parts(rowheads, Dv);
+    return G == 1 ? 0 : sizeof(float) * (size_t)G * Dv;
 }
 
 hipError_t launch_output_gate_backward(const OutputGateBackwardArgs &a) {

@@ -131,6 +131,8 @@ def _expect(t, name, shape, dtypes, optional=False):
         if optional:
             return
         raise ValueError(f"{name} is required")
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes:
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -588,8 +590,10 @@ def kda_output_gate_backward(o, gate, dout, weight=None, *, eps: float = 1e-6, d
 def _norm_rows(x):
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be a tensor [..., W]")
-    _expect(x, "x", x.shape, _FLOAT_IO)
-    return x.numel() // x.shape[-1], x.shape[-1]
+    if x.dtype not in _FLOAT_IO:
+        raise ValueError(f"x must be one of {[str(d) for d in _FLOAT_IO]}, got {x.dtype}")
+    W = x.shape[-1]
+    return x.numel() // W, W
 
 
 def kda_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False, out=None,
@@ -599,21 +603,22 @@ def kda_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = 
     (out, mean, rstd), the statistics fp32 [...] for the backward pass; mean is None for RMS."""
     lib = load_library()
     rows, W = _norm_rows(x)
+    lead = x.shape[:-1]
     _expect(weight, "weight", (W,), (torch.float32,), optional=True)
     _expect(bias, "bias", (W,), (torch.float32,), optional=True)
     _expect(out, "out", x.shape, _FLOAT_IO, optional=True)
     if rms and mean is not None:
         raise ValueError("an RMS norm has no mean")
-    _expect(mean, "mean", x.shape[:-1], (torch.float32,), optional=True)
-    _expect(rstd, "rstd", x.shape[:-1], (torch.float32,), optional=True)
+    _expect(mean, "mean", lead, (torch.float32,), optional=True)
+    _expect(rstd, "rstd", lead, (torch.float32,), optional=True)
     dev = _same_gpu(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
     with _on(dev):
         if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+            out = torch.empty_like(x, dtype=out_dtype)
         if mean is None and not rms:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            mean = torch.empty(lead, dtype=torch.float32, device=dev)
         if rstd is None:
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
         st = lib.kda_layer_norm(_at(x), _at(weight), _at(bias), _at(out), _at(mean), _at(rstd), rows, W,
                                 float(eps), int(rms), _dt(x), _dt(out), _stream(stream, dev))
     if st != 0:

@@ -400,7 +400,7 @@ int kda_prefill_backward(const void *q, const void *k, const void *v, const floa
  * fp32 arithmetic; dweight's sum has a fixed order. rows == 0 gives dweight = 0.
  * No gradient may be any other buffer of the call. Alignment, support and errors
  * as for kda_output_gate. workspace: kda_output_gate_backward_workspace_size bytes
- * (at most 1 MiB), 256-byte aligned; may be NULL when dweight is.
+ * (at most 1 MiB), 256-byte aligned; may be NULL when that is 0 or dweight is NULL.
  */
 size_t kda_output_gate_backward_workspace_size(int rows, int H, int Dv);
 int kda_output_gate_backward(const void *o, const void *gate, const void *dout, const float *weight, void *d_o,
@@ -421,8 +421,8 @@ int kda_output_gate_backward(const void *o, const void *gate, const void *dout, 
  *   eps  > 0
  * fp32 arithmetic; the variance is the mean square of centred values. Any W from 1
  * to 16384 (above: KDA_ERR_UNSUPPORTED) and any alignment of the element type;
- * fastest with W a multiple of 8 and 16-byte aligned x, out, weight and bias. Up
- * to 4,194,300 rows (16,777,200 up to W = 4096). rows == 0 launches nothing.
+ * fastest with W a multiple of 8 and 16-byte aligned x, out, weight and bias.
+ * rows == 0 launches nothing.
  */
 int kda_layer_norm(const void *x, const float *weight, const float *bias, void *out, float *mean, float *rstd,
                    int rows, int W, float eps, int rms, kda_dtype x_dtype, kda_dtype out_dtype, void *stream);
@@ -437,7 +437,7 @@ int kda_layer_norm(const void *x, const float *weight, const float *bias, void *
  * The sums over rows have a fixed order. rows == 0 gives zeros. No gradient may be
  * any other buffer of the call. Sizes and alignment as for kda_layer_norm.
  * workspace: kda_layer_norm_backward_workspace_size bytes (at most 4 KiB x W),
- * 256-byte aligned; may be NULL when dweight and dbias are.
+ * 256-byte aligned; may be NULL when that is 0 or dweight and dbias are NULL.
  */
 size_t kda_layer_norm_backward_workspace_size(int rows, int W);
 int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, const float *rstd, const float *weight,

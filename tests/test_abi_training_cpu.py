@@ -80,7 +80,7 @@ def test_recurrent(lib, kw, status):
 
 
 def _gate(lib, **kw):
-    a = dict(o=P[0], z=P[1], d=P[2], w=P[3], do=P[4], dz=P[5], dw=P[6], rows=4, H=2, Dv=64, eps=1e-6, od=1, zd=1, dd=1,
+    a = dict(o=P[0], z=P[1], d=P[2], w=P[3], do=P[4], dz=P[5], dw=P[6], rows=400, H=2, Dv=64, eps=1e-6, od=1, zd=1, dd=1,
              ws=None, wsb=0)
     a.update(kw)
     return lib.kda_output_gate_backward(*(a[n] for n in ("o", "z", "d", "w", "do", "dz", "dw", "rows", "H", "Dv", "eps",
@@ -110,14 +110,14 @@ def _norm(lib, **kw):
     (dict(eps=float("nan")), INVALID), (dict(xd=2), INVALID), (dict(yd=-1), INVALID), (dict(rms=1), INVALID),   # a mean for RMS
     (dict(x=ctypes.c_void_p(1)), INVALID), (dict(y=ctypes.c_void_p(2), yd=0), INVALID), (dict(w=ctypes.c_void_p(2)), INVALID),
     (dict(y=P[0], yd=0), INVALID), (dict(y=P[1]), INVALID), (dict(m=P[0]), INVALID), (dict(m=P[5]), INVALID),
-    (dict(W=16385), UNSUPPORTED), (dict(W=16384, rows=2 ** 23), UNSUPPORTED),
+    (dict(W=16385), UNSUPPORTED),
 ])
 def test_layer_norm(lib, kw, status):
     assert _norm(lib, **kw) == status
 
 
 def _norm_back(lib, **kw):
-    a = dict(x=P[0], dy=P[1], m=P[2], r=P[3], w=P[4], dx=P[5], dw=P[6], db=P[7], rows=4, W=10, rms=0, xd=1, yd=1, ws=None, wsb=0)
+    a = dict(x=P[0], dy=P[1], m=P[2], r=P[3], w=P[4], dx=P[5], dw=P[6], db=P[7], rows=400, W=10, rms=0, xd=1, yd=1, ws=None, wsb=0)
     a.update(kw)
     return lib.kda_layer_norm_backward(*(a[n] for n in ("x", "dy", "m", "r", "w", "dx", "dw", "db", "rows", "W", "rms",
                                                         "xd", "yd", "ws", "wsb")), None)
@@ -139,6 +139,8 @@ def test_small_workspaces(lib):
     assert lib.kda_output_gate_backward_workspace_size(1, 1, 96) == 0 and lib.kda_output_gate_backward_workspace_size(-1, 1, 64) == 0
     assert 0 < lib.kda_layer_norm_backward_workspace_size(2 ** 20, 4096) <= 4096 * 4096
     assert lib.kda_layer_norm_backward_workspace_size(4, 16385) == 0
+    # a few rows are one workgroup's, which needs none
+    assert lib.kda_output_gate_backward_workspace_size(1, 1, 128) == 0 and lib.kda_layer_norm_backward_workspace_size(4, 100) == 0
 
 
 def test_binding_refuses():
