@@ -402,6 +402,31 @@ def kda_output_gate(o, gate, weight=None, *, eps: float = 1e-6, out=None,
     return out
 
 
+class _On:
+    """A with block in which ``dev`` and, where one is given, ``stream`` are current: buffers
+    allocated inside then belong to the stream that the kernels run on, and neither earlier
+    work of the caller's stream nor a later free can touch them too soon."""
+
+    def __init__(self, dev, stream):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        self.dev, self.stream = _on(dev), None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.dev.__exit__(*exc)
+
+
+def _running(dev, stream):
+    return _on(dev) if stream is None else _On(dev, stream)
+
+
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     """Address of a tensor that _same_gpu has passed (contiguous) or that was allocated here."""
     return None if t is None else t.data_ptr()
@@ -457,7 +482,7 @@ def _recurrent(entry, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, o
     _expect(out, "out", (T, H, Dv), _FLOAT_IO, optional=True)
     dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, S=S, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out,
                     out=out)
-    with _on(dev):
+    with _running(dev, stream):
         if out is None:
             out = torch.empty(T, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
         st = lib.kda_recurrent(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(S), _at(out), _at(cu_seqlens),
@@ -516,7 +541,7 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
     _expect(dS0, "dS0", (N, H, Dv, Dk), (torch.float32,), optional=True)
     _check_prefill(q, k, v, g, beta, S0, None, None, cu_seqlens, workspace, g_head)
     dev = _same_gpu(q=q, dout=dout, dS_out=dS_out, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0)
-    with _on(dev):
+    with _running(dev, stream):
         dq, dk, dv, dbeta = (torch.empty_like(like) if x is None else x
                              for x, like in ((dq, q), (dk, k), (dv, v), (dbeta, beta)))
         if dg is None and g is not None:
@@ -572,7 +597,7 @@ def kda_output_gate_backward(o, gate, dout, weight=None, *, eps: float = 1e-6, d
     _expect(dweight, "dweight", (Dv,), (torch.float32,), optional=True)
     _expect_workspace(workspace)
     dev = _same_gpu(o=o, gate=gate, dout=dout, weight=weight, do=do, dgate=dgate, dweight=dweight, workspace=workspace)
-    with _on(dev):
+    with _running(dev, stream):
         do = torch.empty_like(o) if do is None else do
         dgate = torch.empty_like(gate) if dgate is None else dgate
         if dweight is None and weight is not None:
@@ -612,7 +637,7 @@ def kda_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = 
     _expect(mean, "mean", lead, (torch.float32,), optional=True)
     _expect(rstd, "rstd", lead, (torch.float32,), optional=True)
     dev = _same_gpu(x=x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
-    with _on(dev):
+    with _running(dev, stream):
         if out is None:
             out = torch.empty_like(x, dtype=out_dtype)
         if mean is None and not rms:
@@ -646,7 +671,7 @@ def kda_layer_norm_backward(x, dy, mean, rstd, weight=None, *, bias: bool = Fals
     _expect_workspace(workspace)
     dev = _same_gpu(x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dweight, dbias=dbias,
                     workspace=workspace)
-    with _on(dev):
+    with _running(dev, stream):
         dx = torch.empty_like(x) if dx is None else dx
         if dweight is None and weight is not None:
             dweight = torch.empty_like(weight)

@@ -370,15 +370,17 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
  * Rows of tokens behind the last sequence of a packed batch are left as they
  * were. A sequence of length zero gives dS0 = dS_out.
  *
- * Arithmetic, states and their gradients in fp32 (fp32 matrix instructions), for
- * any magnitude of dout; a bf16 gradient is the rounded fp32 value. g = -inf has
- * gradient 0. Results repeat bit for bit.
+ * Arithmetic, states and their gradients in fp32 (matrix products on fp32
+ * instructions, or on bf16 ones with every operand cut in three), for any magnitude
+ * of dout; a bf16 gradient is the rounded fp32 value. A log-decay of -104 or less
+ * (exp is 0 in fp32; -inf wipes a channel) has gradient 0. Results repeat bit for
+ * bit.
  * Support: Dk == Dv in {64, 128}; io_dtype KDA_F32 with fp32 beta and dout, or
  * KDA_BF16 with either; (T_total / 64 + N + 1) * H below 2^23. opt->snapshots
  * must be NULL; opt may be NULL. All tensors but beta, dbeta and a per-head g, dg
  * must be 16-byte aligned. No gradient may be any other buffer of the call.
- * workspace: kda_prefill_backward_workspace_size bytes (about 340 KB per
- * 64 tokens and head at Dk = 128, 140 KB at 64), 256-byte aligned, its contents
+ * workspace: kda_prefill_backward_workspace_size bytes (about 390 KB per
+ * 64 tokens and head at Dk = 128, 180 KB at 64), 256-byte aligned, its contents
  * ignored, not used by anything else until the call's work has finished.
  * The size function returns 0 for sizes that the call rejects.
  */

@@ -95,3 +95,25 @@ def test_drafts_checked_and_continued():
     for got, want, bar in ((out.view(N, drafts, H, D)[:, :accepted], long_out[:, T:T + accepted], 2e-2),
                            (nxt, long_out[:, -1], 2e-2), (taken, long_S, 5e-3)):
         assert (got - want).abs().max() <= bar * want.square().mean().sqrt()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_buffers_belong_to_the_given_stream(raw):
+    """The caller's stream still has to fill (and has already freed) memory of the sizes that the
+    calls allocate: a call on another stream must not be given that memory."""
+    x = torch.randn(512, 512, device="cuda")
+    o, z, d = (torch.randn(512, 4, 128, device="cuda") for _ in range(3))
+    w = torch.ones(128, device="cuda")
+    want = kda_layer_norm(x), kda_output_gate_backward(o, z, d, w)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)
+        junk = [torch.full(s, float("nan"), device="cuda") for s in ((512, 512), (512,), (512,), o.shape, o.shape, (128,))]
+        junk.append(torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda"))
+        del junk
+        stream = st.cuda_stream if raw else st
+        got = kda_layer_norm(x, stream=stream), kda_output_gate_backward(o, z, d, w, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, t in zip(got, want) for a, b in zip(g, t))
+        del got
