@@ -157,10 +157,9 @@ __device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
 //   lower triangular C x C matrices: the ten tiles on and below the diagonal,
 //   float4 l: row l % 16, columns 4 (l / 16) + 0..3, or transposed the reverse
 template <int D> struct Rec {
-    static constexpr size_t KDR = 0, KRR = KDR + C * D, KDT = KRR + C * D, KRT = KDT + C * D, QDT = KRT + C * D,
-        TE = QDT + C * D,                                               // (I + A Diag(b))^-1
-        TYT = TE + TILES * 256,                                         // (I + Diag(b) A)^-1, transposed
-        PT = TYT + TILES * 256,                                         // P, transposed
+    static constexpr size_t KDR = 0, KRT = KDR + C * D, TE = KRT + C * D,   // the forward scan's; TE (I + A Diag(b))^-1
+        KRR = TE + TILES * 256, KDT = KRR + C * D, QDT = KDT + C * D,        // the backward scan's
+        TYT = QDT + C * D, PT = TYT + TILES * 256,                           // (I + Diag(b) A)^-1 and P, transposed
         GAM = PT + TILES * 256,                                         // [D]
         RQ = GAM + D, RK = RQ + C,                                      // 1 / norms of q and k [C]
         SIZE = RK + C;
@@ -716,6 +715,16 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             }
         }
     };
+    // The chain's workgroups together touch every 128-byte line of the record two
+    // chunks ahead, so that it is in L2 when their operand loads are issued (8k
+    // gradient 1297 -> 1278 us).
+    const size_t region = back ? R::KRR : 0, lines = ((back ? R::GAM : R::KRR) - region) / 32;
+    const size_t line = region + 32 * min((size_t)(((slot % (D / TV)) * 4 + w) * 64 + l), lines - 1);
+    float touched = 0.f;
+    auto touch = [&](int step) {
+        settle(touched);
+        touched = p.ws.rec[item_of(min(step, chunks - 1)) * R::SIZE + line];
+    };
     typedef std::integral_constant<int, 3> Three;
     if (chunks == 0) {
     } else if (!back) {
@@ -749,6 +758,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             const size_t item = item_of(step);
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
             put_state(item);
+            touch(step + 2);
             __syncthreads();
             f32x4 acc[JT], e[JT];
 #pragma unroll
@@ -812,6 +822,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
             auto &O = s.O[step & 1];
             put_state(item);
+            touch(step + 2);
 #pragma unroll
             for (int y = 0; y < JT; ++y)
 #pragma unroll
@@ -1400,17 +1411,17 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
         if (e != hipSuccess) return e;
     }
     const unsigned groups = (static_cast<unsigned>(a.N * a.H) + 7) / 8;
-    // 32 value channels per workgroup load each operand half as often, but leave one
-    // workgroup a CU at half the chains: they win where two fit on every CU
-    // (8 x 1024 tokens x 32 heads: 1150 against 1293 us for the whole call; one
-    // sequence of 8192, one workgroup a CU: 1285 and 1296) and, since the longest of
-    // packed sequences decides when a CU is free, three for those (64 chains of 1 to
-    // 2048 tokens: 311 against 268 us; 96: 399 and 406).
+    // 32 value channels per workgroup load each operand half as often, but on half
+    // the workgroups. Whole calls at 32 / 16 channels, D = 128: one workgroup a CU (one
+    // sequence of 8192 tokens, 32 heads) 1248 / 1278 us, two (2 x 4096) 1141 / 1279 us,
+    // a quarter (8192 tokens, 8 heads) 733 / 585 us. The longest of packed sequences
+    // decides when a call ends: 64 chains of 1 to 2048 tokens (two a CU) 303 / 261 us, 96
+    // (three) 394 / 398 us, 384 1196 / 1307 us.
     int dev = 0, cus = 0;
     if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
     if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
     const long long wide = 2ll * a.N * a.H * (D / 32);
-    const int tv = wide >= (a.cu_seqlens && a.N > 1 ? 3ll : 2ll) * cus ? 32 : 16;
+    const int tv = wide >= (a.cu_seqlens && a.N > 1 ? 3ll : 1ll) * cus ? 32 : 16;
     const auto scan = tv == 32 ? scan_kernel<D, 32, TI, TB, TG> : scan_kernel<D, 16, TI, TB, TG>;
     hipLaunchKernelGGL(scan, dim3(2 * groups * 8 * (D / tv)), dim3(256), 0, a.stream, p, v, beta, dout, a.S0,
                        a.dS_out, a.dS0);
