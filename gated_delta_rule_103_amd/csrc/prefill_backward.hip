@@ -915,8 +915,11 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     typedef FinishLds<CH, PO> FinishLds_t;
     FinishLds_t &s = *reinterpret_cast<FinishLds_t *>(lds_raw);
     Item it;
-    const int part = blockIdx.x % (D / CH);
-    if (!it.find(p, blockIdx.x / (D / CH))) return;
+    // the parts of an item, which read the same rows, run on one XCD (workgroups go
+    // to the eight XCDs in turn)
+    constexpr unsigned PARTS = D / CH;
+    const int part = blockIdx.x / 8 % PARTS;
+    if (!it.find(p, blockIdx.x / (8 * PARTS) * 8 + blockIdx.x % 8)) return;
     const size_t item = it.slot;
     const float *rec = p.ws.rec + item * R::SIZE, *M = p.ws.M + item * D * D, *dM = p.ws.dM + item * D * D;
     const float *E = p.ws.E + item * C * D, *Y = p.ws.Y + item * C * D;
@@ -1427,7 +1430,7 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
                        a.dS_out, a.dS0);
     e = hipGetLastError();
     if (e != hipSuccess || items == 0) return e;
-    hipLaunchKernelGGL(finish, dim3(items * (D / ch)), dim3(4 * ch), finish_lds, a.stream, p, q, k, beta, dout,
+    hipLaunchKernelGGL(finish, dim3((items + 7) / 8 * 8 * (D / ch)), dim3(4 * ch), finish_lds, a.stream, p, q, k, beta, dout,
                        static_cast<TI *>(a.dq), static_cast<TI *>(a.dk), static_cast<TI *>(a.dv), a.dg,
                        static_cast<TB *>(a.dbeta));
     return hipGetLastError();
@@ -1452,7 +1455,7 @@ bool prefill_backward_fits(int N, long long T_total, int H, int Dk) {
     const unsigned long long items = (unsigned long long)max_chunks(N, T_total, C) * H;
     const unsigned long long scans = 2 * ((unsigned long long)N * H + 7) * (Dk / 16);
     // and one chunk of a tensor at most 2^31 bytes (offsets inside it have 32 bits)
-    return items * 512 < (1ull << 32) && scans * 256 < (1ull << 32) && (unsigned long long)H * Dk * C * 4 < (1ull << 31);
+    return (items + 8) * 512 < (1ull << 32) && scans * 256 < (1ull << 32) && (unsigned long long)H * Dk * C * 4 < (1ull << 31);
 }
 
 hipError_t launch_prefill_backward(const PrefillBackwardArgs &a) { return a.Dk == 64 ? launch_d<64>(a) : launch_d<128>(a); }
