@@ -181,7 +181,7 @@ __device__ __forceinline__ void tile_at(int i, int &bi, int &bj) {
 }
 
 struct Ws {
-    int32_t *chunk_off;
+    int32_t *cut, *chunk_off;
     float *rec, *M, *dM, *E, *Y;
 };
 
@@ -274,8 +274,41 @@ struct Decay {
     int col;                  // 1, or 0 for a gate per head
     __device__ Decay(const Common &p, const Item &it, int D)
         : g(p.g, it, p.H, p.g_head ? 1 : D), col(p.g_head ? 0 : 1) {}
-    __device__ float at(int tau, int c) const { return fmaxf(g.at(tau, c * col), MIN_G); }
+    __device__ float at(int tau, int c) const { return cut(g.at(tau, c * col)); }
+    __device__ static float cut(float x) { return x < MIN_G ? MIN_G : x; }      // NaN stays
 };
+
+// ---- plan -----------------------------------------------------------------
+
+// Packed offsets, cut so that they rise and stay inside the T rows, and how many
+// chunks lie before each sequence. The device's own copy: no offset that a caller
+// leaves there can lead a kernel outside its buffers.
+__global__ __launch_bounds__(256) void plan_kernel(const int32_t *__restrict__ cu, int N, int T, int32_t *cut,
+                                                   int32_t *chunk_off) {
+    __shared__ int32_t part[256];
+    const int t = threadIdx.x, per = N / 256 + 1;
+    const int lo = min(N + 1, t * per), hi = min(N + 1, lo + per);
+    int32_t top = 0;
+    for (int n = lo; n < hi; ++n) top = max(top, min(cu[n], T));
+    part[t] = top;
+    __syncthreads();
+    top = 0;
+    for (int i = 0; i < t; ++i) top = max(top, part[i]);
+    for (int n = lo; n < hi; ++n) cut[n] = top = max(top, min(cu[n], T));
+    __syncthreads();
+    // chunks of sequence n, which ends at offset n + 1
+    auto chunks = [&](int n) { return n < N ? (cut[n + 1] - cut[n] + C - 1) / C : 0; };
+    int32_t sum = 0;
+    for (int n = lo; n < hi; ++n) sum += chunks(n);
+    part[t] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int i = 0; i < t; ++i) sum += part[i];
+    for (int n = lo; n < hi; ++n) {
+        chunk_off[n] = sum;
+        sum += chunks(n);
+    }
+}
 
 // ---- prep -----------------------------------------------------------------
 
@@ -1100,7 +1133,7 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         for (int r = 0; r < 4; ++r) {
             qv[b][r] = Rows<TI>::value(qraw[b][r]);
             kv[b][r] = Rows<TI>::value(kraw[b][r]);
-            gv[b][r] = fmaxf(gv[b][r], MIN_G);
+            gv[b][r] = Decay::cut(gv[b][r]);
             wiped |= (gv[b][r] <= MIN_G ? 1u : 0u) << (4 * b + r);
         }
     }
@@ -1380,11 +1413,12 @@ size_t carve(int N, long long T_total, int H, char *base, Ws *ws) {
         off += round256(bytes);
         return at;
     };
-    char *plan = take(sizeof(int32_t) * (size_t)(N + 1));
+    int32_t *plan[2];
+    for (int i = 0; i < 2; ++i) plan[i] = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * (size_t)(N + 1)));
     float *a[5];
     const size_t sizes[5] = {Rec<D>::SIZE, (size_t)D * D, (size_t)D * D, (size_t)C * D, (size_t)C * D};
     for (int i = 0; i < 5; ++i) a[i] = reinterpret_cast<float *>(take(items * sizes[i] * sizeof(float)));
-    if (ws) *ws = Ws{reinterpret_cast<int32_t *>(plan), a[0], a[1], a[2], a[3], a[4]};
+    if (ws) *ws = Ws{plan[0], plan[1], a[0], a[1], a[2], a[3], a[4]};
     return off;
 }
 
@@ -1394,10 +1428,11 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
     Ws ws;
     carve<D>(a.N, (long long)a.B * a.T, a.H, static_cast<char *>(a.ws), &ws);
     if (a.cu_seqlens) {
-        const hipError_t e = launch_chunk_plan(a.cu_seqlens, a.N, C, ws.chunk_off, a.stream);
+        hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(256), 0, a.stream, a.cu_seqlens, a.N, a.T, ws.cut, ws.chunk_off);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const SeqView sv{a.cu_seqlens, ws.chunk_off, a.N, a.T, C};
+    const SeqView sv{a.cu_seqlens ? ws.cut : nullptr, ws.chunk_off, a.N, a.T, C};
     const long long chunks = a.cu_seqlens ? max_chunks(a.N, a.T, C) : (long long)a.N * ((a.T + C - 1) / C);
     const Common p{sv, ws, a.g, a.H, (int)chunks, a.g_head, a.qk_norm, a.norm_eps};
     const unsigned items = static_cast<unsigned>(chunks * a.H);

@@ -360,15 +360,17 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
  * S_out, to those of every input. Nothing of the forward call is needed: the
  * states at the chunk borders are computed again.
  *
- *   q, k, v, g, beta, S0, cu_seqlens, N, B, T, H, Dk, Dv  as for kda_prefill
+ *   q, k, v, g, beta, S0, cu_seqlens, N, B, T, H, Dk, Dv  as for kda_prefill;
+ *          cu_seqlens may end before T_total, offsets below the one before them or
+ *          outside [0, T_total] are cut
  *   dout    [T_total][H][Dv] dout_dtype
  *   dS_out  [N][H][Dv][Dk] fp32, or NULL: the final state has no gradient
  *   dq, dk  [T_total][H][Dk], dv [T_total][H][Dv]   io_dtype
  *   dg      fp32, g's layout; NULL exactly when g is
  *   dbeta   [T_total][H] beta_dtype
  *   dS0     [N][H][Dv][Dk] fp32, or NULL to skip it (S0 may be NULL, a zero state)
- * Rows of tokens behind the last sequence of a packed batch are left as they
- * were. A sequence of length zero gives dS0 = dS_out.
+ * Rows of tokens in no sequence of a packed batch are left as they were. A
+ * sequence of length zero gives dS0 = dS_out.
  *
  * Arithmetic, states and their gradients in fp32 (matrix products on fp32
  * instructions, or on bf16 ones with every operand cut in three), for any magnitude

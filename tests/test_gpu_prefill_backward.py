@@ -233,3 +233,33 @@ def test_many_chains(D, io):
     """Enough chains for the scan that takes 32 value channels a workgroup, dense and packed."""
     run(H=40 if D == 128 else 80, D=D, B=4, T=70, io=io, shift=-1.0, seed=18)
     run(H=40 if D == 128 else 80, D=D, lengths=[70, 1, 0, 33, 64, 10], io=io, shift=-1.0, seed=19)
+
+
+def test_offsets_are_cut_and_rows_of_no_sequence_do_not_count():
+    """Offsets that fall or leave the rows name what remains when they are cut; NaN in rows of no
+    sequence reaches nothing, and their gradients stay as they were."""
+    p, dout, dS, first = run(H=2, D=64, lengths=[37, 0, 50], io="bf16", seed=20)
+    d, T = to_dev(p), p.num_tokens
+    edge = lambda t, n: torch.full((1, n, *t.shape[2:]), float("nan"), dtype=t.dtype, device="cuda")
+    for cu, behind in (([3, 40, 20, 500], 0), ([3, 40, -2 ** 31, 90], 70), ([3, 40, 40, 90], 1)):
+        pad = lambda t: torch.cat([edge(t, 3), t.cuda(), edge(t, behind)], 1).contiguous()
+        ins = [pad(t) for t in (d.q, d.k, d.v, d.g, d.beta, dout)]
+        bufs = {n: torch.full_like(t, 3.0) for n, t in zip(("dq", "dk", "dv", "dg", "dbeta"), ins)}
+        got = kda_prefill_backward(*ins, d.S0, dS.cuda(), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), **bufs)
+        torch.cuda.synchronize()
+        for n, x in zip(NAMES, got):
+            if n == "dS0":
+                assert torch.equal(x, first[n]), cu
+            else:
+                assert torch.equal(x[:, 3:3 + T], first[n]) and (x[:, :3] == 3.0).all() and (x[:, 3 + T:] == 3.0).all(), (cu, n)
+    none = kda_prefill_backward(*ins, d.S0, dS.cuda(), cu_seqlens=torch.tensor([500, 7, 7, 7], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(none[5].cpu(), dS)
+
+
+def test_a_gate_that_is_no_number_is_not_hidden():
+    p, dout, dS = draw(H=2, D=64, B=1, T=80, io="f32", seed=21)
+    p.g[0, 30, 1, 5] = float("nan")
+    got = gpu(p, dout, dS)
+    assert got["dg"][0, :, 1].isnan().any() and got["dq"][0, 31:, 1].isnan().any() and got["dS0"][0, 1].isnan().any()
+    assert all(torch.isfinite(got[n][:, :, 0]).all() for n in ("dq", "dk", "dv", "dg", "dbeta"))
