@@ -612,12 +612,17 @@ def kda_output_gate_backward(o, gate, dout, weight=None, *, eps: float = 1e-6, d
     return do, dgate, dweight
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 def _norm_rows(x):
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be a tensor [..., W]")
     if x.dtype not in _FLOAT_IO:
         raise ValueError(f"x must be one of {[str(d) for d in _FLOAT_IO]}, got {x.dtype}")
     W = x.shape[-1]
+    if x.numel() // W > _INT_MAX or W > _INT_MAX:
+        raise ValueError(f"x has {x.numel() // W} rows of {W}, more than the library counts")
     return x.numel() // W, W
 
 

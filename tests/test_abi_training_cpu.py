@@ -178,3 +178,13 @@ def test_binding_refuses():
         lib_py.kda_layer_norm_backward(t, t, torch.zeros(3, 2), torch.zeros(3))
     with pytest.raises(ValueError, match="must be a GPU tensor"):
         lib_py.kda_layer_norm(t)
+
+
+def test_binding_refuses_counts_beyond_an_int():
+    """Row counts that a C int would cut short (no memory behind these tensors)."""
+    for shape in ((2 ** 31, 1), (2 ** 16, 2 ** 16, 1), (1, 2 ** 32 + 8)):
+        x = torch.empty(*shape, dtype=torch.bfloat16, device="meta")
+        with pytest.raises(ValueError, match="more than the library counts"):
+            lib_py.kda_layer_norm(x)
+        with pytest.raises(ValueError, match="more than the library counts"):
+            lib_py.kda_layer_norm_backward(x, x, None, None, rms=True)
