@@ -20,18 +20,27 @@
 //     dg_i = sum_{t >= i} row_t + sum_{t < i} out_t + gam sum_j M dM'
 // where the s = t terms of P, which no decay touches, stay out of row.
 //
-// Three kernels (times: 8192 tokens x 32 heads x 128 channels, bf16, in a call of 1.25 ms):
-//   prep    every (chunk, head): P, A, both inverses, Qd, Kd, Kr to a record. 229 us;
-//           it writes 0.8 GB (3.4 TB/s), matrix units busy 20% of the time, between
-//           barriers that two workgroups a CU cover for each other
+// With TE and TY the inverses of I + A Diag(b) and I + Diag(b) A, the recurrences are
+//     E = TE V - (TE Kd) M,   Y = (P TY)^T dO + (TY^T Kr) dM',
+// every matrix but the state known beforehand: the state passes through one product
+// before U (dV) and one after it. That took the scans from 572 to 510 us for 45 us more
+// in prep (a second product through TE or TY costs the scan a barrier and 24 matrix
+// instructions a chunk).
+//
+// Three kernels (times: 8192 tokens x 32 heads x 128 channels, bf16, in a call of 1.2 ms):
+//   prep    every (chunk, head): P, A, both inverses and the matrices above to a
+//           record. 270 us; 0.27 GB in, 0.76 GB out (3.7 TB/s), matrix units busy 34%,
+//           vector units 42% of the time, between barriers that two workgroups a CU
+//           cover for each other
 //   scan    every (sequence, head, 16 or 32 value channels), once forwards for M
 //           and E and once backwards for dM' and Y. Value channels never meet in
 //           either recurrence, and neither needs the other, so both run in one
-//           launch. 572 us; bound by operand loads (without them 501 of then 759 us)
-//           and the 0.8 GB of M, E, dM' and Y that it writes; matrix units 21%
+//           launch. 510 us; 0.92 GB in, 0.81 GB out (3.3 TB/s), matrix units 23%, vector
+//           units 30%, one wavefront a SIMD: a chain's chunks wait for one another
 //   finish  every (chunk, head, 64 key channels): all gradients but dS0 from M,
-//           dM', E and Y. 460 us; bound by instruction issue: vector instructions
-//           45% and matrix instructions 41% of the cycles at two wavefronts a SIMD
+//           dM', E and Y. 485 us; bound by instruction issue: vector instructions
+//           43% and matrix instructions 40% of the cycles at two wavefronts a SIMD;
+//           1.15 GB in, 0.34 GB out
 //
 // The call's floor is 145 us for inputs and outputs (739 MB at 5.1 TB/s); chunks of 64
 // tokens leave 0.8 GB of states beside them, each written and read once.
@@ -104,20 +113,32 @@ template <int M> __device__ __forceinline__ float lane_across(float x) {
 // MFMA 16x16x32: a lane holds row (column) l % 16 and eight inner indices of its
 // lane group l / 16; two float4 of neighbouring 16-wide tiles make one operand.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ void split3(f32x4 a, f32x4 b, u32v4 (&p)[3]) {
-    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u0 = __float_as_uint(x[2 * i]), u1 = __float_as_uint(x[2 * i + 1]);
-        p[0][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-        const float r0 = x[2 * i] - __uint_as_float(u0 & 0xffff0000u), r1 = x[2 * i + 1] - __uint_as_float(u1 & 0xffff0000u);
-        u0 = __float_as_uint(r0);
-        u1 = __float_as_uint(r1);
-        p[1][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-        u0 = __float_as_uint(r0 - __uint_as_float(u0 & 0xffff0000u));
-        u1 = __float_as_uint(r1 - __uint_as_float(u1 & 0xffff0000u));
-        p[2][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+// The high halves of a and b, which keep what these leave. With DOT, x - h is one
+// instruction, h still packed: a dot product of the pair with (-1, 0) or (0, -1) onto
+// x, exact like the subtraction. It is used where operands of many products are cut
+// at once (8k gradient 1284 -> 1259 us); where few values are cut and used at once,
+// in the scan of 16 channels, its latency costs more (packed gradient 266 -> 272 us).
+template <bool DOT> __device__ __forceinline__ uint32_t cut_pair(float &a, float &b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t h = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    if constexpr (DOT) {
+        uint32_t first = 0xbf80u, second = 0xbf800000u;
+        asm("" : "+s"(first), "+s"(second));           // as an immediate the first would reach the wrong half
+        const bf16x2 hv = __builtin_bit_cast(bf16x2, h);
+        a = __builtin_amdgcn_fdot2_f32_bf16(hv, __builtin_bit_cast(bf16x2, first), a, false);
+        b = __builtin_amdgcn_fdot2_f32_bf16(hv, __builtin_bit_cast(bf16x2, second), b, false);
+    } else {
+        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
     }
+    return h;
+}
+template <bool DOT> __device__ __forceinline__ void split3(f32x4 a, f32x4 b, u32v4 (&p)[3]) {
+    float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[z][i] = cut_pair<DOT>(x[2 * i], x[2 * i + 1]);
 }
 __device__ __forceinline__ f32x4 mfma32(u32v4 a, u32v4 b, f32x4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
@@ -165,10 +186,10 @@ __device__ __forceinline__ f32x4 ld4s(const float *p, int stride) {
 //   lower triangular C x C matrices: the ten tiles on and below the diagonal,
 //   float4 l: row l % 16, columns 4 (l / 16) + 0..3, or transposed the reverse
 template <int D> struct Rec {
-    static constexpr size_t KDR = 0, KRT = KDR + C * D, TE = KRT + C * D,   // the forward scan's; TE (I + A Diag(b))^-1
-        KRR = TE + TILES * 256, KDT = KRR + C * D, QDT = KDT + C * D,        // the backward scan's
-        TYT = QDT + C * D, PT = TYT + TILES * 256,                           // (I + Diag(b) A)^-1 and P, transposed
-        GAM = PT + TILES * 256,                                         // [D]
+    static constexpr size_t WR = 0, KRT = WR + C * D, TE = KRT + C * D,      // the forward scan's: -TE Kd, Kr, TE
+        XR = TE + TILES * 256, KDT = XR + C * D, QDT = KDT + C * D,          // the backward scan's: TY^T Kr, Kd, Qd
+        ZT = QDT + C * D,                                                    // and (P TY)^T
+        GAM = ZT + TILES * 256,                                         // [D]
         RQ = GAM + D, RK = RQ + C,                                      // 1 / norms of q and k [C]
         SIZE = RK + C;
 };
@@ -285,25 +306,35 @@ struct Decay {
 // leaves there can lead a kernel outside its buffers.
 __global__ __launch_bounds__(256) void plan_kernel(const int32_t *__restrict__ cu, int N, int T, int32_t *cut,
                                                    int32_t *chunk_off) {
-    __shared__ int32_t part[256];
+    __shared__ int32_t part[4];
     const int t = threadIdx.x, per = N / 256 + 1;
     const int lo = min(N + 1, t * per), hi = min(N + 1, lo + per);
+    // what `op` makes of the threads' x before this one (0 for none)
+    auto before = [&](int32_t x, auto op) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int32_t y = __shfl_up(x, o, 64);
+            if ((t & 63) >= o) x = op(x, y);
+        }
+        __syncthreads();
+        if ((t & 63) == 63) part[t >> 6] = x;
+        __syncthreads();
+        x = __shfl_up(x, 1, 64);
+        if ((t & 63) == 0) x = 0;
+        for (int i = 0; i < t >> 6; ++i) x = op(x, part[i]);
+        return x;
+    };
+    auto larger = [](int32_t a, int32_t b) { return max(a, b); };
     int32_t top = 0;
     for (int n = lo; n < hi; ++n) top = max(top, min(cu[n], T));
-    part[t] = top;
-    __syncthreads();
-    top = 0;
-    for (int i = 0; i < t; ++i) top = max(top, part[i]);
+    top = before(top, larger);
     for (int n = lo; n < hi; ++n) cut[n] = top = max(top, min(cu[n], T));
     __syncthreads();
     // chunks of sequence n, which ends at offset n + 1
     auto chunks = [&](int n) { return n < N ? (cut[n + 1] - cut[n] + C - 1) / C : 0; };
     int32_t sum = 0;
     for (int n = lo; n < hi; ++n) sum += chunks(n);
-    part[t] = sum;
-    __syncthreads();
-    sum = 0;
-    for (int i = 0; i < t; ++i) sum += part[i];
+    sum = before(sum, [](int32_t a, int32_t b) { return a + b; });
     for (int n = lo; n < hi; ++n) {
         chunk_off[n] = sum;
         sum += chunks(n);
@@ -456,32 +487,14 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
                 }
             }
         }
-        // the scans' operands, from the staging tiles: whole blocks before (k, q with
-        // their decay from the start) or behind (k with its decay to the end) come in
+        // Qd from its staging tile, the decay of whole blocks before comes in
         const int tt = w % NB;                          // this wavefront's token block
-        auto blocks = [&](auto d, auto &f0, auto &f1) {  // products of the blocks' decays before and behind it
-            const auto d0 = d(0), d1 = d(1), d2 = d(2), d3 = d(3);
-            typedef std::decay_t<decltype(f0)> F;
-            f0 = tt == 0 ? (F)1.f : tt == 1 ? d0 : tt == 2 ? d0 * d1 : d0 * d1 * d2;
-            f1 = tt == 3 ? (F)1.f : tt == 2 ? d3 : tt == 1 ? d2 * d3 : d1 * d2 * d3;
-        };
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            if (NW == 8 && (kk & 1) != w / NB) continue;
-            const int x = 16 * kk + 4 * lg, at = ((tt * (D / 16) + 4 * hf + kk) * 64 + l) * 4;
-            f32x4 f0, f1;
-            blocks([&](int b) { return ld4(&s.dec[b][64 * hf + x]); }, f0, f1);
-            store4_far(rec + R::KDR + at, ld4(&s.X[0][16 * tt + lr][x]) * f0);
-            store4_far(rec + R::KRR + at, ld4(&s.X[1][16 * tt + lr][x]) * f1);
-        }
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
             if (NW == 8 && (ct & 1) != w / NB) continue;
             const int x = 16 * ct + lr, at = (((4 * hf + ct) * NB + tt) * 64 + l) * 4;
-            float f0, f1;
-            blocks([&](int b) { return s.dec[b][64 * hf + x]; }, f0, f1);
-            store4_far(rec + R::KDT + at, ld4s(&s.X[0][16 * tt + 4 * lg][x], 64 + 4) * f0);
-            store4_far(rec + R::KRT + at, ld4s(&s.X[1][16 * tt + 4 * lg][x], 64 + 4) * f1);
+            const float d0 = s.dec[0][64 * hf + x], d1 = s.dec[1][64 * hf + x], d2 = s.dec[2][64 * hf + x];
+            const float f0 = tt == 0 ? 1.f : tt == 1 ? d0 : tt == 2 ? d0 * d1 : d0 * d1 * d2;
             store4_far(rec + R::QDT + at, ld4s(&s.X[2][16 * tt + 4 * lg][x], 64 + 4) * f0);
         }
     }
@@ -589,19 +602,80 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         }
         __syncthreads();
     }
-    // out: X, and transposed (I + Diag(b) A)^-1 = I - Diag(b) X A and P
-    for (int i = w; i < TILES; i += NW) {
-        const int bi = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, bj = i - bi * (bi + 1) / 2;
+    // TY = (I + Diag(b) A)^-1 = I - Diag(b) X A, in A's place, its tiles transposed
+    constexpr int OWN = (TILES + NW - 1) / NW;
+    f32x4 ty[OWN];
+#pragma unroll
+    for (int n = 0; n < OWN; ++n) {
+        int bi, bj;
+        tile_at(w + n * NW, bi, bj);
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
         for (int bk = bj; bk <= bi; ++bk)
             sum = mfma16(ld4(&X[tile_of(bi, bk)][lr][4 * lg]), ld4s(&s.A[tile_of(bk, bj)][4 * lg][lr], TP), sum);
         const int row = 16 * bi + 4 * lg, col = 16 * bj + lr;
-        f32x4 ty;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) ty[r] = (row + r == col ? 1.f : 0.f) - s.b[row + r] * sum[r];
-        store4_far(rec + R::TYT + (i * 64 + l) * 4, ty);
-        store4_far(rec + R::PT + (i * 64 + l) * 4, ld4s(&s.P[i][4 * lg][lr], TP));
-        store4_far(rec + R::TE + (i * 64 + l) * 4, ld4(&X[i][lr][4 * lg]));
+        for (int r = 0; r < 4; ++r) ty[n][r] = (row + r == col ? 1.f : 0.f) - s.b[row + r] * sum[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < OWN; ++n)
+        if (w + n * NW < TILES) store4(&s.A[w + n * NW][lr][4 * lg], ty[n]);
+    // Kd and Kr again, 64 channels at a time: out by columns, and times X and TY
+#pragma unroll 1
+    for (int hf = 0; hf < HALVES; ++hf) {
+        if (hf) __syncthreads();
+        if (c / 64 == hf) {
+            const float d0 = s.dec[0][c], d1 = s.dec[1][c], d2 = s.dec[2][c], d3 = s.dec[3][c];
+            const float f0 = blk == 0 ? 1.f : blk == 1 ? d0 : blk == 2 ? d0 * d1 : d0 * d1 * d2;
+            const float f1 = blk == 3 ? 1.f : blk == 2 ? d3 : blk == 1 ? d2 * d3 : d1 * d2 * d3;
+            float run = 0.f;
+            settle(run);
+#pragma unroll
+            for (int i = 0; i < BT; ++i) {
+                run += gv[i];
+                s.X[1][blk * BT + i][ch] = kv[i] * (__expf(run) * f0);
+            }
+            run = 0.f;
+#pragma unroll
+            for (int i = BT - 1; i >= 0; --i) {
+                s.X[2][blk * BT + i][ch] = kv[i] * (__expf(run) * f1);
+                run += gv[i];
+            }
+        }
+        __syncthreads();
+        if (hf == 0) {
+            for (int i = w; i < TILES; i += NW) {
+                int bi, bj;
+                tile_at(i, bi, bj);
+                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                for (int bk = bj; bk <= bi; ++bk)
+                    z = mfma16(ld4(&s.P[tile_of(bi, bk)][lr][4 * lg]), ld4(&s.A[tile_of(bk, bj)][lr][4 * lg]), z);
+                store4_far(rec + R::ZT + (i * 64 + l) * 4, z);
+                store4_far(rec + R::TE + (i * 64 + l) * 4, ld4(&X[i][lr][4 * lg]));
+            }
+        }
+        // a wavefront has 16 channels, and with eight of them two token blocks of four:
+        // the first and last or the middle ones, which are the same work
+        const int x = 16 * (w % 4) + lr, at = 4 * hf + w % 4;
+        f32x4 kd[NB], kr[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            kd[b] = ld4s(&s.X[1][16 * b + 4 * lg][x], 64 + 4);
+            kr[b] = ld4s(&s.X[2][16 * b + 4 * lg][x], 64 + 4);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (NW == 8 && (b == 0 || b == NB - 1) != (w < 4)) continue;
+            store4_far(rec + R::KDT + ((at * NB + b) * 64 + l) * 4, kd[b]);
+            store4_far(rec + R::KRT + ((at * NB + b) * 64 + l) * 4, kr[b]);
+            f32x4 y = {0.f, 0.f, 0.f, 0.f}, z = y;
+#pragma unroll
+            for (int i = 0; i <= b; ++i) y = mfma16(kd[i], -ld4(&X[tile_of(b, i)][lr][4 * lg]), y);
+#pragma unroll
+            for (int i = b; i < NB; ++i) z = mfma16(kr[i], ld4(&s.A[tile_of(i, b)][lr][4 * lg]), z);
+            store4_far(rec + R::WR + ((b * (D / 16) + at) * 64 + l) * 4, y);
+            store4_far(rec + R::XR + ((b * (D / 16) + at) * 64 + l) * 4, z);
+        }
     }
     if (t < D) rec[R::GAM + t] = (s.dec[0][t] * s.dec[1][t]) * (s.dec[2][t] * s.dec[3][t]);
 }
@@ -616,9 +690,8 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
 template <int D, int TV, int PO>
 struct ScanLds {
     uint16_t S[3][TV][D + 8];         // the state
-    uint16_t R[3][TV][C + 8];         // V - Kd M or dU
     uint16_t U[3][TV][C + 8];         // U or -dV
-    uint16_t O[2][PO][TV][C + 8];     // dO^T, two chunks in turn
+    uint16_t O[PO][TV][C + 8];        // V^T or dO^T
 };
 // Column of inner index k in those: the eight that a lane multiplies (of two
 // neighbouring 16-wide tiles, four each) lie together.
@@ -715,7 +788,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
             u32v4 b[3];
-            split3(x[2 * m], x[2 * m + 1], b);
+            split3<TV == 32>(x[2 * m], x[2 * m + 1], b);
 #pragma unroll
             for (int y = 0; y < JT; ++y) {
                 u32v4 a[3];
@@ -731,7 +804,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         for (int m = 0; m < 2; ++m)
             if (back ? 2 * m + 1 >= w : 2 * m <= w) {
                 u32v4 b[3];
-                split3(x[2 * m], x[2 * m + 1], b);
+                split3<TV == 32>(x[2 * m], x[2 * m + 1], b);
 #pragma unroll
                 for (int y = 0; y < JT; ++y) {
                     u32v4 a[decltype(parts)::value];
@@ -750,7 +823,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 u32v4 b[3];
-                split3(x[i][2 * m], x[i][2 * m + 1], b);
+                split3<TV == 32>(x[i][2 * m], x[i][2 * m + 1], b);
 #pragma unroll
                 for (int y = 0; y < JT; ++y) st[y][i] = product(a[y], b, st[y][i]);
             }
@@ -759,159 +832,100 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
     // The chain's workgroups together touch every 128-byte line of the record two
     // chunks ahead, so that it is in L2 when their operand loads are issued (8k
     // gradient 1297 -> 1278 us).
-    const size_t region = back ? R::KRR : 0, lines = ((back ? R::GAM : R::KRR) - region) / 32;
+    const size_t region = back ? R::XR : 0, lines = ((back ? R::GAM : R::XR) - region) / 32;
     const size_t line = region + 32 * min((size_t)(((slot % (D / TV)) * 4 + w) * 64 + l), lines - 1);
     float touched = 0.f;
     auto touch = [&](int step) {
         settle(touched);
         touched = p.ws.rec[item_of(min(step, chunks - 1)) * R::SIZE + line];
     };
+    auto tri_of = [&](f32x4(&x)[NB], const float *rec) {     // the other blocks stay zero
+#pragma unroll
+        for (int kk = 0; kk < NB; ++kk)
+            if (back ? kk >= w : kk <= w)
+                x[kk] = ld4(rec + (back ? R::ZT + (tile_of(kk, w) * 64 + l) * 4 : R::TE + (tile_of(w, kk) * 64 + l) * 4));
+    };
     typedef std::integral_constant<int, 3> Three;
-    if (chunks == 0) {
-    } else if (!back) {
-        f32x4 kd[D / 16], te[NB] = {zero, zero, zero, zero}, kr[CT][NB];
+    // `in`: V or dO, T its type
+    auto run = [&](auto direction, const auto *in) {
+        constexpr bool BACK = decltype(direction)::value;
+        typedef std::decay_t<decltype(*in)> T;
+        typedef std::integral_constant<int, sizeof(T) == 2 ? 1 : 3> Parts;
+        f32x4 rows[D / 16], tri[NB] = {zero, zero, zero, zero}, qd[CT][NB], kt[CT][NB];
         float gam[CT];
-        typename Rows<TI>::Raw4 vt[JT];
+        typename Rows<T>::Raw4 ov[JT];
         typename Rows<TB>::Raw b;
-        auto v_of = [&](const Item &it) {
-            const Rows<TI> r(v, it, p.H, D);
-#pragma unroll
-            for (int y = 0; y < JT; ++y) vt[y] = r.raw4(tau, jr + 16 * y);
-        };
-        auto te_of = [&](const float *rec) {               // blocks behind w stay zero
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk)
-                if (kk <= w) te[kk] = ld4(rec + R::TE + (tile_of(w, kk) * 64 + l) * 4);
-        };
-        {
-            const float *rec = p.ws.rec + item_of(0) * R::SIZE;
-            const Item it = chunk_of(0);
-            rows_of(kd, rec + R::KDR);
-            v_of(it);
-            te_of(rec);
-            b = beta_of(it);
-            cols_of(kr, rec + R::KRT);
-            gam_of(gam, rec);
-        }
-        for (int step = 0; step < chunks; ++step) {
-            const int next = min(step + 1, chunks - 1);
-            const Item it = chunk_of(next);
-            const size_t item = item_of(step);
-            const float *rec = p.ws.rec + item_of(next) * R::SIZE;
-            put_state(item);
-            touch(step + 2);
-            __syncthreads();
-            f32x4 acc[JT], e[JT];
-#pragma unroll
-            for (int y = 0; y < JT; ++y) acc[y] = e[y] = zero;
-            times_rows(kd, acc);
-            rows_of(kd, rec + R::KDR);
-#pragma unroll
-            for (int y = 0; y < JT; ++y) put(s.R, y, tau_col, Rows<TI>::value4(vt[y]) - acc[y]);
-            v_of(it);
-            __syncthreads();
-            times_tri(s.R, te, e, Three{});
-            te_of(rec);
-#pragma unroll
-            for (int y = 0; y < JT; ++y) {
-                put(s.U, y, tau_col, e[y] * Rows<TB>::value(b));
-                store4_far(p.ws.E + item * C * D + ((w * NT + jt + y) * 64 + l) * 4, e[y]);
-            }
-            b = beta_of(it);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < CT; ++i)
-#pragma unroll
-                for (int y = 0; y < JT; ++y) st[y][i] *= gam[i];
-            onto_state(s.U, kr, Three{});
-            cols_of(kr, rec + R::KRT);
-            gam_of(gam, rec);
-        }
-    } else {
-        f32x4 kr[D / 16], pt[NB] = {zero, zero, zero, zero}, ty[NB] = {zero, zero, zero, zero}, qd[CT][NB], kd[CT][NB];
-        float gam[CT];
-        typename Rows<TG>::Raw4 ov[JT];
-        typename Rows<TB>::Raw b;
-        typedef std::integral_constant<int, PO> Parts;
         const int ot = t / 4, oj = t % 4 * 4;
-        auto o_of = [&](const Item &it) {
-            const Rows<TG> r(dout, it, p.H, D);
+        auto in_of = [&](const Item &it) {
+            const Rows<T> r(in, it, p.H, D);
 #pragma unroll
             for (int y = 0; y < JT; ++y) ov[y] = r.raw4(ot, j0 + 16 * y + oj);
         };
-        auto upper_of = [&](f32x4(&x)[NB], const float *m) {   // blocks before w stay zero
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk)
-                if (kk >= w) x[kk] = ld4(m + (tile_of(kk, w) * 64 + l) * 4);
-        };
         {
             const float *rec = p.ws.rec + item_of(0) * R::SIZE;
             const Item it = chunk_of(0);
-            o_of(it);
-            rows_of(kr, rec + R::KRR);
-            upper_of(pt, rec + R::PT);
-            cols_of(qd, rec + R::QDT);
+            in_of(it);
+            tri_of(tri, rec);
+            rows_of(rows, rec + (BACK ? R::XR : R::WR));
+            if constexpr (BACK) cols_of(qd, rec + R::QDT);
             gam_of(gam, rec);
-            upper_of(ty, rec + R::TYT);
             b = beta_of(it);
-            cols_of(kd, rec + R::KDT);
+            cols_of(kt, rec + (BACK ? R::KDT : R::KRT));
         }
         for (int step = 0; step < chunks; ++step) {
             const int next = min(step + 1, chunks - 1);
             const Item it = chunk_of(next);
             const size_t item = item_of(step);
             const float *rec = p.ws.rec + item_of(next) * R::SIZE;
-            auto &O = s.O[step & 1];
             put_state(item);
             touch(step + 2);
 #pragma unroll
             for (int y = 0; y < JT; ++y)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (PO == 1) {
-                        O[0][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(ov[y][r / 2] >> 16 * (r % 2));
-                    } else {
-                        float f = Rows<TG>::value4(ov[y])[r];
+                for (int r = 0; r < 4; r += 2) {
+                    float f0 = 0.f, f1 = 0.f;
+                    if constexpr (Parts::value == 3) f0 = Rows<T>::value4(ov[y])[r], f1 = Rows<T>::value4(ov[y])[r + 1];
 #pragma unroll
-                        for (int z = 0; z < 3; ++z) {
-                            const uint32_t u = __float_as_uint(f);
-                            O[z][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(u >> 16);
-                            f -= __uint_as_float(u & 0xffff0000u);
-                        }
+                    for (int z = 0; z < Parts::value; ++z) {
+                        uint32_t u = ov[y][r / 2];
+                        if constexpr (Parts::value == 3) u = cut_pair<false>(f0, f1);
+                        s.O[z][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(u);
+                        s.O[z][16 * y + oj + r + 1][inner(ot)] = static_cast<uint16_t>(u >> 16);
                     }
                 }
-            o_of(it);
+            in_of(it);
             __syncthreads();
-            f32x4 acc[JT], e[JT];
+            f32x4 e[JT];
 #pragma unroll
-            for (int y = 0; y < JT; ++y) acc[y] = e[y] = zero;
-            times_rows(kr, acc);
-            rows_of(kr, rec + R::KRR);
-            times_tri(O, pt, acc, Parts{});
-            upper_of(pt, rec + R::PT);
+            for (int y = 0; y < JT; ++y) e[y] = zero;
+            times_tri(s.O, tri, e, Parts{});
+            tri_of(tri, rec);
+            times_rows(rows, e);
+            rows_of(rows, rec + (BACK ? R::XR : R::WR));
+            const float be = BACK ? -Rows<TB>::value(b) : Rows<TB>::value(b);
+            b = beta_of(it);
 #pragma unroll
-            for (int y = 0; y < JT; ++y) put(s.R, y, tau_col, acc[y]);
-            // dO's share of the new state waits for nothing
+            for (int y = 0; y < JT; ++y) {
+                put(s.U, y, tau_col, e[y] * be);
+                store4_far((BACK ? p.ws.Y : p.ws.E) + item * C * D + ((w * NT + jt + y) * 64 + l) * 4, e[y]);
+            }
 #pragma unroll
             for (int i = 0; i < CT; ++i)
 #pragma unroll
                 for (int y = 0; y < JT; ++y) st[y][i] *= gam[i];
-            onto_state(O, qd, Parts{});
-            cols_of(qd, rec + R::QDT);
             gam_of(gam, rec);
-            __syncthreads();
-            times_tri(s.R, ty, e, Three{});
-            upper_of(ty, rec + R::TYT);
-#pragma unroll
-            for (int y = 0; y < JT; ++y) {
-                put(s.U, y, tau_col, e[y] * -Rows<TB>::value(b));
-                store4_far(p.ws.Y + item * C * D + ((w * NT + jt + y) * 64 + l) * 4, e[y]);
+            if constexpr (BACK) {                          // dO's share of the new state waits for nothing
+                onto_state(s.O, qd, Parts{});
+                cols_of(qd, rec + R::QDT);
             }
-            b = beta_of(it);
             __syncthreads();
-            onto_state(s.U, kd, Three{});
-            cols_of(kd, rec + R::KDT);
+            onto_state(s.U, kt, Three{});
+            cols_of(kt, rec + (BACK ? R::KDT : R::KRT));
         }
+    };
+    if (chunks > 0) {
+        if (back) run(std::true_type{}, dout);
+        else run(std::false_type{}, v);
     }
     if (back && dS0)
 #pragma unroll
@@ -1017,9 +1031,9 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
             const int j = 32 * (stage * SM + sm) + 4 * lg;
             u32v4 o[PO], u[3], v[3];
             if constexpr (PO == 1) o[0] = u32v4{o0[0], o0[1], o1[0], o1[1]};
-            else split3(Rows<TG>::value4(o0), Rows<TG>::value4(o1), o);
-            split3(e0 * be, e1 * be, u);
-            split3(y0 * be, y1 * be, v);
+            else split3<true>(Rows<TG>::value4(o0), Rows<TG>::value4(o1), o);
+            split3<true>(e0 * be, e1 * be, u);
+            split3<true>(y0 * be, y1 * be, v);
             if (first) {
                 dvr.put4(stau, j, y0 * be);
                 dvr.put4(stau, j + 16, y1 * be);
@@ -1044,8 +1058,8 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
             u32v4 ms[3], ds[3];
             const f32x4 x = m0[m] * d0[m] + m1[m] * d1[m];
             mdm += (x[0] + x[1]) + (x[2] + x[3]);
-            split3(m0[m], m1[m], ms);
-            split3(d0[m], d1[m], ds);
+            split3<true>(m0[m], m1[m], ms);
+            split3<true>(d0[m], d1[m], ds);
             load_states(next, m);
             // operands of the next block are read while this one's products run
             u32v4 o[2][PO], u[2][3], v[2][3];

@@ -381,8 +381,8 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
  * KDA_BF16 with either; (T_total / 64 + N + 1) * H below 2^23. opt->snapshots
  * must be NULL; opt may be NULL. All tensors but beta, dbeta and a per-head g, dg
  * must be 16-byte aligned. No gradient may be any other buffer of the call.
- * workspace: kda_prefill_backward_workspace_size bytes (about 390 KB per
- * 64 tokens and head at Dk = 128, 180 KB at 64), 256-byte aligned, its contents
+ * workspace: kda_prefill_backward_workspace_size bytes (about 380 KB per
+ * 64 tokens and head at Dk = 128, 170 KB at 64), 256-byte aligned, its contents
  * ignored, not used by anything else until the call's work has finished.
  * The size function returns 0 for sizes that the call rejects.
  */
