@@ -22,7 +22,7 @@
 // a fixed order, so results repeat bit for bit. No atomics.
 //
 // 8192 rows x 4096 channels, bf16: forward 134 MB in 27 us (4.9 TB/s), backward 201 MB in
-// 38 us (5.3 TB/s) and 5 us for the sums. Loading the next row ahead and one barrier
+// 36 us (5.6 TB/s) and 5 us for the sums. Loading the next row ahead and one barrier
 // a row instead of four took the backward kernel from 60 to 36 us.
 #include "kda_device.h"
 #include "kda_launch.h"
@@ -45,10 +45,13 @@ __device__ __forceinline__ f32x8 load8(const T *row, int c, int step, int W) {
         return x;
     }
 }
-template <bool VEC, typename T>
+template <bool VEC, bool PUT = false, typename T>
 __device__ __forceinline__ void store8(T *row, int c, int step, int W, f32x8 x) {
     if constexpr (VEC) {
-        if (c < W) vec8<T>::store(row + c, x);
+        if (c < W) {
+            if constexpr (PUT) vec8<T>::put(row + c, x);
+            else vec8<T>::store(row + c, x);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -185,7 +188,7 @@ __global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_backward_kernel(
     float *__restrict__ db_part, int rows, int W) {
     using S = Shape<NW, K>;
     __shared__ float part[2][2][NW];
-    __shared__ float fold[S::ROWS > 1 ? (S::ROWS - 1) * S::MAX_W : 1];
+    __shared__ __align__(32) float fold[S::ROWS > 1 ? (S::ROWS - 1) * S::MAX_W : 1];
     const int t = threadIdx.x % S::SPAN, wave = t / 64, rg = threadIdx.x / S::SPAN;
     constexpr int STEP = VEC ? 1 : S::SPAN;
     f32x8 dw[K] = {}, db[K] = {}, wv[K];
@@ -252,7 +255,7 @@ __global__ __launch_bounds__((Shape<NW, K>::THREADS)) void norm_backward_kernel(
         sh = mean_in ? sh * inv : 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            store8<VEC>(dx + (size_t)r * W, first_channel<VEC, S::SPAN>(t, k), STEP, W,
+            store8<VEC, true>(dx + (size_t)r * W, first_channel<VEC, S::SPAN>(t, k), STEP, W,
                         (h[k] - n[k] * shn - sh) * rstd);
     }
     auto put = [&](f32x8 (&a)[K], float *out) {
