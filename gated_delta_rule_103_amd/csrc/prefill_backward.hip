@@ -1473,10 +1473,10 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
     const unsigned groups = (static_cast<unsigned>(a.N * a.H) + 7) / 8;
     // 32 value channels per workgroup load each operand half as often, but on half
     // the workgroups. Whole calls at 32 / 16 channels, D = 128: one workgroup a CU (one
-    // sequence of 8192 tokens, 32 heads) 1248 / 1278 us, two (2 x 4096) 1141 / 1279 us,
-    // a quarter (8192 tokens, 8 heads) 733 / 585 us. The longest of packed sequences
-    // decides when a call ends: 64 chains of 1 to 2048 tokens (two a CU) 303 / 261 us, 96
-    // (three) 394 / 398 us, 384 1196 / 1307 us.
+    // sequence of 8192 tokens, 32 heads) 1190 / 1282 us, two (2 x 4096) 1160 / 1272 us,
+    // half a one (8192 tokens, 16 heads) 814 / 714 us. The longest of packed sequences
+    // decides when a call ends: 64 chains of 1 to 2048 tokens (two a CU) 300 / 252 us, 96
+    // (three) 651 / 697 us, 384 1815 / 1986 us.
     int dev = 0, cus = 0;
     if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
     if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
