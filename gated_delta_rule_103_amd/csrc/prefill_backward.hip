@@ -165,6 +165,18 @@ template <int M> __device__ __forceinline__ void halve(float *v, int lane) {
     }
 }
 
+// The sums of v[0..15] over the 16 lanes of a row: lane l of them gets that of v[l]. Fifteen
+// exchanges instead of 64 (and in prep no second reading of q and k for their norms): the
+// gradient of 4 x 1000 tokens x 16 heads x 64 with normalised q and k 184 -> 159 us,
+// 8192 tokens x 32 heads x 128 1573 -> 1468 us.
+__device__ __forceinline__ float sums16(float (&v)[16], int lane) {
+    halve<8>(v, lane);
+    halve<4>(v, lane);
+    halve<2>(v, lane);
+    halve<1>(v, lane);
+    return v[0];
+}
+
 // Keeps the computation of x before what follows: without it the compiler sinks
 // whole chains of products towards their uses and holds all their operands.
 __device__ __forceinline__ void settle(f32x4 &x) { asm volatile("" : "+v"(x)); }
@@ -384,18 +396,27 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
     if (t < C) s.b[t] = Rows<TB>(beta, it, p.H, 1).at(t, 0);
     for (int i = t; i < TILES * BT * TP; i += THREADS) (&s.A[0][0][0])[i] = (&s.P[0][0][0])[i] = 0.f;
     if (p.qk_norm) {
-        for (int tau = w; tau < C; tau += NW) {
-            float sq = 0.f, sk = 0.f;
-            for (int i = l; i < D; i += 64) {
-                const float x = qr.at(tau, i), y = kr.at(tau, i);
-                sq += x * x;
-                sk += y * y;
-            }
-            const float rq = 1.f / sqrtf(warp_sum(sq) + p.norm_eps), rk = 1.f / sqrtf(warp_sum(sk) + p.norm_eps);
-            if (l == 0) {
-                rec[R::RQ + tau] = s.rq[tau] = rq;
-                rec[R::RK + tau] = s.rk[tau] = rk;
-            }
+        // squares summed over the wavefront's 64 channels, then over the wavefronts of the block
+        float(*sums)[2][BT] = reinterpret_cast<float(*)[2][BT]>(&s.X[0][0][0]);
+        auto squares = [&](const float(&x)[BT], int which) {
+            float y[BT];
+#pragma unroll
+            for (int i = 0; i < BT; ++i) y[i] = x[i] * x[i];
+            float z = sums16(y, l);
+            z += __shfl_xor(z, 16, 64);
+            z += __shfl_xor(z, 32, 64);
+            if (l < BT) sums[w][which][l] = z;
+        };
+        squares(qv, 0);
+        squares(kv, 1);
+        __syncthreads();
+        if (t < 2 * C) {
+            const int which = t / C, tau = t % C, b = tau / BT;
+            float x = sums[b * HALVES][which][tau % BT];
+            if (HALVES == 2) x += sums[b * HALVES + HALVES - 1][which][tau % BT];
+            x = 1.f / sqrtf(x + p.norm_eps);
+            (which ? s.rk : s.rq)[tau] = x;
+            rec[(which ? R::RK : R::RQ) + tau] = x;
         }
         __syncthreads();
 #pragma unroll
@@ -423,11 +444,7 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
         float v[16] = {qv[o] * k0,      q1 * (e10 * k0), q1 * k1,         q2 * (e20 * k0), q2 * (e21 * k1), q2 * k2,
                        q3 * (e30 * k0), q3 * (e31 * k1), q3 * (e32 * k2), q3 * k3,         k1 * (e10 * k0), k2 * (e20 * k0),
                        k2 * (e21 * k1), k3 * (e30 * k0), k3 * (e31 * k1), k3 * (e32 * k2)};
-        halve<8>(v, l);
-        halve<4>(v, l);
-        halve<2>(v, l);
-        halve<1>(v, l);
-        float x = v[0];
+        float x = sums16(v, l);
         x += __shfl_xor(x, 16, 64);
         x += __shfl_xor(x, 32, 64);
         settle(x);
@@ -1306,21 +1323,15 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     }
 
     if (p.qk_norm) {                                   // dx = (dx^ - x^ (x^ . dx^)) / |x|
+        float v[16];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int which = 0; which < 2; ++which) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float x = qv[b][r] * pq[b][r], y = kv[b][r] * pk[b][r];
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int m = 1; m < 16; m <<= 1) {
-                    x += __shfl_xor(x, m, 64);
-                    y += __shfl_xor(y, m, 64);
-                }
-                if (lr == 0) {
-                    s.rows[0][w][16 * b + 4 * lg + r] = x;
-                    s.rows[1][w][16 * b + 4 * lg + r] = y;
-                }
-            }
+                for (int r = 0; r < 4; ++r) v[4 * b + r] = which ? kv[b][r] * pk[b][r] : qv[b][r] * pq[b][r];
+            s.rows[which][w][16 * (lr / 4) + 4 * lg + lr % 4] = sums16(v, lr);
+        }
         __syncthreads();
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -1380,15 +1391,16 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
                 sq[tau * SI + x] = round_bf16(pq[b][r]);
                 sk[tau * SI + x] = round_bf16(pk[b][r]);
             }
-            if (!p.g_head) {
-                sg[tau * SG + x] = pc[b][r];
-            } else {
-                float y = pc[b][r];
-#pragma unroll
-                for (int m = 1; m < 16; m <<= 1) y += __shfl_xor(y, m, 64);
-                if (lr == 0) s.rows[0][w][tau] = y;
-            }
+            if (!p.g_head) sg[tau * SG + x] = pc[b][r];
         }
+    if (p.g_head) {
+        float v[16];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * b + r] = pc[b][r];
+        s.rows[0][w][16 * (lr / 4) + 4 * lg + lr % 4] = sums16(v, lr);
+    }
     __syncthreads();
     constexpr int PER = 16 / sizeof(TI), CHUNKS = CH / PER;         // elements of a store, stores of a row
 #pragma unroll
