@@ -263,3 +263,11 @@ def test_a_gate_that_is_no_number_is_not_hidden():
     got = gpu(p, dout, dS)
     assert got["dg"][0, :, 1].isnan().any() and got["dq"][0, 31:, 1].isnan().any() and got["dS0"][0, 1].isnan().any()
     assert all(torch.isfinite(got[n][:, :, 0]).all() for n in ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.parametrize("scale", [1e-28, 1e25])
+@pytest.mark.parametrize("D,io", [(64, "bf16"), (128, "f32")])
+def test_gradient_magnitudes_far_from_one(D, io, scale):
+    """The gradients are linear in dout and dS_out: far magnitudes lose nothing while the smallest
+    part of a value cut in three (2^-16 of it) stays a normal fp32 number."""
+    run(H=2, D=D, B=1, T=130, io=io, l2=D == 64, scale=scale, seed=22)
