@@ -313,7 +313,19 @@ int kda_prefill_backward(const void *q, const void *k, const void *v, const floa
                          float *dg, void *dbeta, float *dS0, const int32_t *cu_seqlens, int N, int B, int T, int H,
                          int Dk, int Dv, kda_dtype io_dtype, kda_dtype beta_dtype, kda_dtype dout_dtype,
                          const kda_options *opt, void *workspace, size_t workspace_bytes, void *stream) {
+    return kda_prefill_backward_padded(q, k, v, g, beta, dout, S0, dS_out, dq, dk, dv, dg, dbeta, dS0, cu_seqlens, N, B,
+                                       T, H, Dk, Dv, io_dtype, beta_dtype, dout_dtype, 0, opt, workspace,
+                                       workspace_bytes, stream);
+}
+
+int kda_prefill_backward_padded(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                                const void *dout, const float *S0, const float *dS_out, void *dq, void *dk, void *dv,
+                                float *dg, void *dbeta, float *dS0, const int32_t *cu_seqlens, int N, int B, int T,
+                                int H, int Dk, int Dv, kda_dtype io_dtype, kda_dtype beta_dtype, kda_dtype dout_dtype,
+                                int zero_rows, const kda_options *opt, void *workspace, size_t workspace_bytes,
+                                void *stream) {
     if (!options_ok(opt)) return KDA_ERR_INVALID_ARG;
+    if (zero_rows & ~KDA_ZERO_ALL) return KDA_ERR_INVALID_ARG;
     const kda_options o = opt ? *opt : kda_options{};
     if (o.snapshots) return KDA_ERR_INVALID_ARG;
     const bool g_head = o.gate == KDA_GATE_HEAD;
@@ -356,6 +368,7 @@ int kda_prefill_backward(const void *q, const void *k, const void *v, const floa
     a.g_head = g_head;
     a.qk_norm = o.qk_l2norm != 0;
     a.norm_eps = o.l2norm_eps;
+    a.zero_rows = zero_rows;
     return kda::launch_prefill_backward(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

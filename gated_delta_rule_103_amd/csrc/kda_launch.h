@@ -98,6 +98,7 @@ struct PrefillBackwardArgs {
     bool g_head = false;        // as in PrefillArgs
     bool qk_norm = false;
     float norm_eps = 0.f;
+    int zero_rows = 0;          // KDA_ZERO_*: gradients whose rows of no sequence become zero
 };
 
 struct OutputGateBackwardArgs {

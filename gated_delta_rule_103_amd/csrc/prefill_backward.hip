@@ -66,6 +66,8 @@
 // the next product along its rows, which finish and prep use, and the states
 // and E, Y go to memory as whole accumulators (1 KB per wavefront store) in the
 // order in which finish reads them as operands.
+#include "../../include/kda.h"
+
 #include "kda_chunks.h"
 #include "kda_device.h"
 #include "kda_launch.h"
@@ -225,6 +227,7 @@ struct Common {
     int H, slots;             // heads; workspace slots of a head, one per chunk
     bool g_head, qk_norm;
     float norm_eps;
+    int zero_rows;            // KDA_ZERO_*: gradients whose rows of no sequence are set to zero
 };
 
 // A (chunk, head) and its tokens: the first one's row of [T_total][H] tensors,
@@ -955,6 +958,36 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 
 // ---- finish ---------------------------------------------------------------
 
+// Zeros into rows of tokens in no sequence, all of which lie before the first sequence or
+// behind the last one: of those, in order, the 64 that start with 64 `behind`, channels
+// c0 .. c0 + CH of one head. `behind` counts the workgroups behind the last chunk: the grid
+// is for ceil(T / 64) + N chunks and a sequence of n tokens takes at most (n + 63) / 64, so
+// 64 tokens each reach every row that the sequences leave.
+template <int D, int CH, typename TI, typename TB>
+__device__ void clear_rows(const Common &p, size_t item, int part, TI *dq, TI *dk, TI *dv, float *dg, TB *dbeta) {
+    const int h = (int)(item % p.H), before = p.sv.cu[0], end = p.sv.cu[p.sv.N];
+    const long long first = 64ll * ((long long)(item / p.H) - p.sv.total_chunks());
+    const u32v4 zero = {0, 0, 0, 0};
+    for (int i = threadIdx.x / (CH / 4); i < C; i += 4 * CH / (CH / 4)) {
+        const long long n = first + i, token = n < before ? n : n - before + end;
+        if (token >= p.sv.T) return;
+        const size_t row = (size_t)token * p.H + h, x = row * D + part * CH + threadIdx.x % (CH / 4) * 4;
+        auto clear4 = [&](auto *to) {
+            if constexpr (sizeof(*to) == 4) *reinterpret_cast<u32v4 *>(to) = zero;
+            else *reinterpret_cast<u32v2 *>(to) = u32v2{0, 0};
+        };
+        if (p.zero_rows & KDA_ZERO_DQ) clear4(dq + x);
+        if (p.zero_rows & KDA_ZERO_DK) clear4(dk + x);
+        if (p.zero_rows & KDA_ZERO_DV) clear4(dv + x);
+        const bool gate = dg && (p.zero_rows & KDA_ZERO_DG);
+        if (gate && !p.g_head) clear4(dg + x);
+        if (part == 0 && threadIdx.x % (CH / 4) == 0) {
+            if (gate && p.g_head) dg[row] = 0.f;
+            if (p.zero_rows & KDA_ZERO_DBETA) dbeta[row] = TB(0);
+        }
+    }
+}
+
 // A workgroup takes CH key channels of a (chunk, head), one wavefront for each 16.
 // CH = 64 leaves room for two workgroups on a CU, which cover each other's loads
 // and barriers (dP and dA are then formed twice at D = 128); where rows are summed
@@ -991,7 +1024,11 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
     // to the eight XCDs in turn)
     constexpr unsigned PARTS = D / CH;
     const int part = blockIdx.x / 8 % PARTS;
-    if (!it.find(p, blockIdx.x / (8 * PARTS) * 8 + blockIdx.x % 8)) return;
+    const size_t nth = blockIdx.x / (8 * PARTS) * 8 + blockIdx.x % 8;
+    if (!it.find(p, nth)) {
+        if (p.sv.cu && p.zero_rows) clear_rows<D, CH>(p, nth, part, dq, dk, dv, dg, dbeta);
+        return;
+    }
     const size_t item = it.slot;
     const float *rec = p.ws.rec + item * R::SIZE, *M = p.ws.M + item * D * D, *dM = p.ws.dM + item * D * D;
     const float *E = p.ws.E + item * C * D, *Y = p.ws.Y + item * C * D;
@@ -1460,7 +1497,7 @@ hipError_t launch_t(const PrefillBackwardArgs &a) {
     }
     const SeqView sv{a.cu_seqlens ? ws.cut : nullptr, ws.chunk_off, a.N, a.T, C};
     const long long chunks = a.cu_seqlens ? max_chunks(a.N, a.T, C) : (long long)a.N * ((a.T + C - 1) / C);
-    const Common p{sv, ws, a.g, a.H, (int)chunks, a.g_head, a.qk_norm, a.norm_eps};
+    const Common p{sv, ws, a.g, a.H, (int)chunks, a.g_head, a.qk_norm, a.norm_eps, a.zero_rows};
     const unsigned items = static_cast<unsigned>(chunks * a.H);
     const TI *q = static_cast<const TI *>(a.q), *k = static_cast<const TI *>(a.k), *v = static_cast<const TI *>(a.v);
     const TB *beta = static_cast<const TB *>(a.beta);

@@ -88,6 +88,8 @@ def load_library() -> ctypes.CDLL:
     lib.kda_prefill_backward_workspace_size.argtypes = [i] * 5
     lib.kda_prefill_backward.restype = i
     lib.kda_prefill_backward.argtypes = [vp] * 15 + [i] * 9 + [op, vp, sz, vp]
+    lib.kda_prefill_backward_padded.restype = i
+    lib.kda_prefill_backward_padded.argtypes = [vp] * 15 + [i] * 10 + [op, vp, sz, vp]
     lib.kda_output_gate_backward_workspace_size.restype = sz
     lib.kda_output_gate_backward_workspace_size.argtypes = [i] * 3
     lib.kda_output_gate_backward.restype = i
@@ -541,6 +543,8 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
     _expect(dS0, "dS0", (N, H, Dv, Dk), (torch.float32,), optional=True)
     _check_prefill(q, k, v, g, beta, S0, None, None, cu_seqlens, workspace, g_head)
     dev = _same_gpu(q=q, dout=dout, dS_out=dS_out, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta, dS0=dS0)
+    # rows of no sequence: left alone in the caller's buffers, zero in those allocated here
+    zero_rows = sum(bit for bit, x in zip((1, 2, 4, 8, 16), (dq, dk, dv, dg, dbeta)) if x is None)
     with _running(dev, stream):
         dq, dk, dv, dbeta = (torch.empty_like(like) if x is None else x
                              for x, like in ((dq, q), (dk, k), (dv, v), (dbeta, beta)))
@@ -549,10 +553,11 @@ def _prefill_backward(entry, q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq,
         if dS0 is None and S0 is not None:
             dS0 = torch.empty_like(S0)
         workspace, ws_bytes = _workspace(kda_prefill_backward_workspace_size(N, B * T, H, Dk, Dv), workspace, dev)
-        st = lib.kda_prefill_backward(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(dout), _at(S0),
-                                      _at(dS_out), _at(dq), _at(dk), _at(dv), _at(dg), _at(dbeta), _at(dS0),
-                                      _at(cu_seqlens), N, B, T, H, Dk, Dv, _dt(q), _dt(beta), _dt(dout),
-                                      _options(g_head, qk_l2norm, l2norm_eps), _at(workspace), ws_bytes, _stream(stream, dev))
+        st = lib.kda_prefill_backward_padded(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(dout), _at(S0),
+                                             _at(dS_out), _at(dq), _at(dk), _at(dv), _at(dg), _at(dbeta), _at(dS0),
+                                             _at(cu_seqlens), N, B, T, H, Dk, Dv, _dt(q), _dt(beta), _dt(dout),
+                                             zero_rows, _options(g_head, qk_l2norm, l2norm_eps), _at(workspace),
+                                             ws_bytes, _stream(stream, dev))
     if st != 0:
         raise KDAError(st, entry)
     return dq, dk, dv, dg, dbeta, dS0
@@ -564,7 +569,9 @@ def kda_prefill_backward(q, k, v, g, beta, dout, S0=None, dS_out=None, *, cu_seq
     """The gradient of kda_prefill: q, k, v, g, beta, S0 and cu_seqlens as given to it, dout
     [B, T, H, Dv] the gradient of out and dS_out [N, H, Dv, Dk] that of S_out (None: zero).
     Returns (dq, dk, dv, dg, dbeta, dS0), each of its input's dtype and shape; dS0 is None
-    when neither S0 nor a buffer for it is given."""
+    when neither S0 nor a buffer for it is given. Rows of tokens in no sequence (packed
+    offsets that start behind 0 or end before T) are zero, but left as they were in buffers
+    that the caller gives."""
     return _prefill_backward("kda_prefill_backward", q, k, v, g, beta, dout, S0, dS_out, cu_seqlens, dq, dk, dv, dg,
                              dbeta, dS0, workspace, stream, qk_l2norm, l2norm_eps)
 

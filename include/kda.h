@@ -395,6 +395,27 @@ int kda_prefill_backward(const void *q, const void *k, const void *v, const floa
                          const kda_options *opt, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * kda_prefill_backward_padded -- kda_prefill_backward for buffers whose contents on
+ * entry mean nothing: rows of tokens in no sequence of a packed batch, whose gradient is
+ * zero, become zero in the gradients that zero_rows names (KDA_ZERO_* added up; other
+ * bits: KDA_ERR_INVALID_ARG), and are left as they were in the others. All else as there.
+ */
+typedef enum {
+    KDA_ZERO_DQ = 1,
+    KDA_ZERO_DK = 2,
+    KDA_ZERO_DV = 4,
+    KDA_ZERO_DG = 8,
+    KDA_ZERO_DBETA = 16,
+    KDA_ZERO_ALL = 31
+} kda_zero_rows;
+int kda_prefill_backward_padded(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                                const void *dout, const float *S0, const float *dS_out, void *dq, void *dk, void *dv,
+                                float *dg, void *dbeta, float *dS0, const int32_t *cu_seqlens, int N, int B, int T,
+                                int H, int Dk, int Dv, kda_dtype io_dtype, kda_dtype beta_dtype, kda_dtype dout_dtype,
+                                int zero_rows, const kda_options *opt, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
  * kda_output_gate_backward -- the gradient of kda_output_gate. With
  * r = 1 / sqrt(mean_j o_j^2 + eps), n = o r, s = sigmoid(z) and x = dout s w:
  *     d_o = r (x - n mean_j(x n)),  dgate = dout n w s (1 - s),
