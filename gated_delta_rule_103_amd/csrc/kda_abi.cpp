@@ -273,7 +273,16 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
                   void *out, const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N,
                   int T_total, int H, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype,
                   kda_dtype out_dtype, const kda_options *opt, void *stream) {
+    return kda_recurrent_padded(q, k, v, g, beta, S, out, cu_seqlens, slot_in, slot_out, N, T_total, H, Dk, Dv, slots,
+                                io_dtype, beta_dtype, out_dtype, 0, opt, stream);
+}
+
+int kda_recurrent_padded(const void *q, const void *k, const void *v, const float *g, const void *beta, float *S,
+                         void *out, const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N,
+                         int T_total, int H, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype,
+                         kda_dtype out_dtype, int zero_rows, const kda_options *opt, void *stream) {
     if (!options_ok(opt)) return KDA_ERR_INVALID_ARG;
+    if (zero_rows != 0 && zero_rows != 1) return KDA_ERR_INVALID_ARG;
     const kda_options o = opt ? *opt : kda_options{};
     if (o.snapshots) return KDA_ERR_INVALID_ARG;                  // prefill only
     const bool g_head = o.gate == KDA_GATE_HEAD;
@@ -299,6 +308,7 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
     a.g_head = g_head;
     a.qk_norm = o.qk_l2norm != 0;
     a.norm_eps = o.l2norm_eps;
+    a.zero_rows = zero_rows != 0;
     return kda::launch_recurrent(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

@@ -78,6 +78,7 @@ struct RecurrentArgs {
     bool g_head = false;        // as in PrefillArgs
     bool qk_norm = false;
     float norm_eps = 0.f;
+    bool zero_rows = false;     // out rows of no sequence become zero
 };
 
 struct PrefillBackwardArgs {

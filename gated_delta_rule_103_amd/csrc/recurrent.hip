@@ -53,8 +53,8 @@ __global__ __launch_bounds__(NT) void recurrent_kernel(const TI *__restrict__ q,
                                                        const TB *__restrict__ beta, float *__restrict__ S,
                                                        TO *__restrict__ out, const int32_t *__restrict__ cu,
                                                        const int32_t *__restrict__ slot_in,
-                                                       const int32_t *__restrict__ slot_out, int T, int H, int slots,
-                                                       bool g_head, bool qk_norm, float norm_eps) {
+                                                       const int32_t *__restrict__ slot_out, int N, int T, int H, int slots,
+                                                       bool g_head, bool qk_norm, float norm_eps, bool zero_rows) {
     constexpr int LPR = D / 4, SLOTS = NT / LPR, ROWS = R * SLOTS, SPLIT = D / ROWS;
     static_assert(NT % LPR == 0 && D % ROWS == 0, "recurrent tiling");
     const int chain = blockIdx.x / SPLIT, n = chain / H, h = chain % H;
@@ -62,6 +62,17 @@ __global__ __launch_bounds__(NT) void recurrent_kernel(const TI *__restrict__ q,
     const int row0 = (blockIdx.x % SPLIT) * ROWS + t / LPR;
     // offsets outside the packed rows are cut to them
     const int begin = min(max(cu[n], 0), T), end = min(max(cu[n + 1], begin), T);
+    if (zero_rows) {                                     // uniform
+        // rows of no sequence lie before the first one and behind the last one, whose
+        // workgroups clear them, each its head's value channels
+        constexpr int TOKENS = NT / ROWS;
+        const int col = (blockIdx.x % SPLIT) * ROWS + t % ROWS;
+        auto clear = [&](int from, int to) {
+            for (int tok = from + t / ROWS; tok < to; tok += TOKENS) out[((size_t)tok * H + h) * D + col] = TO(0);
+        };
+        if (n == 0) clear(0, begin);
+        if (n == N - 1) clear(end, T);
+    }
     if (begin == end) return;
 
     const size_t DD = (size_t)D * D;
@@ -127,8 +138,8 @@ hipError_t launch_t(const RecurrentArgs &a) {
     hipLaunchKernelGGL((recurrent_kernel<D, NT, R, TI, TB, TO>), dim3((unsigned)(a.N * a.H * SPLIT)), dim3(NT), 0,
                        a.stream, static_cast<const TI *>(a.q), static_cast<const TI *>(a.k),
                        static_cast<const TI *>(a.v), a.g, static_cast<const TB *>(a.beta), a.S,
-                       static_cast<TO *>(a.out), a.cu, a.slot_in, a.slot_out, a.T, a.H, a.slots, a.g_head, a.qk_norm,
-                       a.norm_eps);
+                       static_cast<TO *>(a.out), a.cu, a.slot_in, a.slot_out, a.N, a.T, a.H, a.slots, a.g_head,
+                       a.qk_norm, a.norm_eps, a.zero_rows);
     return hipGetLastError();
 }
 

@@ -84,6 +84,8 @@ def load_library() -> ctypes.CDLL:
     f = ctypes.c_float
     lib.kda_recurrent.restype = i
     lib.kda_recurrent.argtypes = [vp] * 10 + [i] * 9 + [op, vp]
+    lib.kda_recurrent_padded.restype = i
+    lib.kda_recurrent_padded.argtypes = [vp] * 10 + [i] * 10 + [op, vp]
     lib.kda_prefill_backward_workspace_size.restype = sz
     lib.kda_prefill_backward_workspace_size.argtypes = [i] * 5
     lib.kda_prefill_backward.restype = i
@@ -484,12 +486,14 @@ def _recurrent(entry, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, o
     _expect(out, "out", (T, H, Dv), _FLOAT_IO, optional=True)
     dev = _same_gpu(q=q, k=k, v=v, g=g, beta=beta, S=S, cu_seqlens=cu_seqlens, slot_in=slot_in, slot_out=slot_out,
                     out=out)
+    zero_rows = int(out is None)        # rows of no sequence: left alone in the caller's out
     with _running(dev, stream):
         if out is None:
             out = torch.empty(T, H, Dv, dtype=out_dtype or q.dtype, device=q.device)
-        st = lib.kda_recurrent(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(S), _at(out), _at(cu_seqlens),
-                               _at(slot_in), _at(slot_out), N, T, H, Dk, Dv, S.shape[0], _dt(q), _dt(beta),
-                               _dt(out), _options(g_head, qk_l2norm, l2norm_eps), _stream(stream, dev))
+        st = lib.kda_recurrent_padded(_at(q), _at(k), _at(v), _at(g), _at(beta), _at(S), _at(out), _at(cu_seqlens),
+                                      _at(slot_in), _at(slot_out), N, T, H, Dk, Dv, S.shape[0], _dt(q), _dt(beta),
+                                      _dt(out), zero_rows, _options(g_head, qk_l2norm, l2norm_eps),
+                                      _stream(stream, dev))
     if st != 0:
         raise KDAError(st, entry)
     return out
@@ -503,7 +507,7 @@ def kda_recurrent(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, *, out=Non
     S: [slots, H, Dv, Dk] fp32. slot_in (int32 [N], or None): the slot a sequence starts from,
     negative = the zero state; slot_out (int32 [T], or None): the slot that receives the state
     after a token, negative = none. All index tensors on the device. Returns out [T, H, Dv];
-    rows of tokens in no sequence are not written."""
+    rows of tokens in no sequence are zero, but left as they were in an ``out`` that is given."""
     return _recurrent("kda_recurrent", q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream,
                       qk_l2norm, l2norm_eps)
 

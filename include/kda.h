@@ -331,7 +331,8 @@ int kda_output_gate(const void *o, const void *gate, const float *weight, void *
  *   cu_seqlens  int32 [N+1]: sequence n is tokens cu_seqlens[n] up to
  *          cu_seqlens[n+1]. It may be empty; out rows (and states) of tokens
  *          that belong to no sequence are left as they were. Offsets outside
- *          [0, T_total] are cut to it.
+ *          [0, T_total] are cut to it. Offsets that fall make sequences share
+ *          tokens: their out rows are then undefined (no fault).
  *   slot_in   int32 [N]: the slot a sequence starts from; a value outside
  *          [0, slots), or slot_in NULL: the zero state
  *   slot_out  int32 [T_total]: the slot that receives the state after a token;
@@ -352,6 +353,16 @@ int kda_recurrent(const void *q, const void *k, const void *v, const float *g, c
                   void *out, const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N,
                   int T_total, int H, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype,
                   kda_dtype out_dtype, const kda_options *opt, void *stream);
+
+/*
+ * kda_recurrent_padded -- kda_recurrent for an out whose contents on entry mean nothing:
+ * with zero_rows 1, rows before cu_seqlens[0] and from cu_seqlens[N] on become zero (0: they
+ * are left as they were; else KDA_ERR_INVALID_ARG). All else as there.
+ */
+int kda_recurrent_padded(const void *q, const void *k, const void *v, const float *g, const void *beta, float *S,
+                         void *out, const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N,
+                         int T_total, int H, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype,
+                         kda_dtype out_dtype, int zero_rows, const kda_options *opt, void *stream);
 
 /*
  * kda_prefill_backward -- the gradient of kda_prefill (and, with

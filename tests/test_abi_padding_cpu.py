@@ -33,3 +33,19 @@ def _backward(lib, **kw):
 ])
 def test_prefill_backward_padded(lib, kw, status):
     assert _backward(lib, **kw) == status
+
+
+def _recurrent(lib, **kw):
+    a = dict(q=P[0], k=P[1], v=P[2], g=P[3], beta=P[4], S=P[5], out=P[6], cu=P[7], si=P[8], so=P[9], N=2, T=5, H=2, Dk=64,
+             Dv=64, slots=3, io=1, bd=1, od=1, zero=1, opt=None)
+    a.update(kw)
+    return lib.kda_recurrent_padded(*(a[n] for n in ("q", "k", "v", "g", "beta", "S", "out", "cu", "si", "so", "N", "T", "H",
+                                                     "Dk", "Dv", "slots", "io", "bd", "od", "zero", "opt")), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(zero=2), INVALID), (dict(zero=-1), INVALID), (dict(q=None), INVALID), (dict(out=P[2]), INVALID),
+    (dict(slots=0), INVALID), (dict(cu=None), INVALID), (dict(Dk=32, Dv=32), UNSUPPORTED), (dict(N=2 ** 20, H=4096), UNSUPPORTED),
+])
+def test_recurrent_padded(lib, kw, status):
+    assert _recurrent(lib, **kw) == status

@@ -1,5 +1,6 @@
-"""Packed batches whose offsets leave rows out, with results that the binding allocates: the
-gradient of a row that belongs to no sequence is zero, whatever the memory held before.
+"""Packed batches whose offsets leave rows out, with results that the binding allocates: a row
+that belongs to no sequence has gradient zero, and output zero of the recurrent form, whatever
+the memory held before.
 
 Every call runs on memory that held NaN: buffers of the results' sizes are filled and freed
 just before it, so the allocator hands the same blocks out again. Values of rows that belong
@@ -8,7 +9,7 @@ to a sequence are those of the same sequences packed without any rows around the
 import pytest
 import torch
 
-from gated_delta_rule_103_amd import gdn_prefill_backward, inputs, kda_prefill_backward
+from gated_delta_rule_103_amd import gdn_prefill_backward, gdn_recurrent, inputs, kda_prefill_backward, kda_recurrent
 
 pytestmark = pytest.mark.gpu
 NAMES = ("dq", "dk", "dv", "dg", "dbeta")
@@ -120,3 +121,41 @@ def test_captured_with_offsets_that_change():
         for n, a, b in zip(NAMES, got, want):
             assert torch.equal(a, b), (new, n)
             assert (a[:, :new[0]] == 0).all() and (a[:, new[-1]:] == 0).all(), (new, n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gate", ["channel", "head", "none"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_recurrent_rows_in_no_sequence_are_zero(D, gate, out_dtype):
+    x, cu = problem([3, 0, 1, 5], 3, D, "bf16", gate, D)
+    x = [None if t is None else t[0] for t in x[:5]]
+    f = kda_recurrent if gate == "channel" else gdn_recurrent
+    pool = torch.randn(13, 3, D, D, generator=torch.Generator().manual_seed(1)).cuda() * 0.1
+    idx = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    start = idx([0, 1, 2, 3])
+    first, kept = pool.clone(), idx(range(4, 13))
+    want = f(*x, first, start, kept, cu.cuda(), out_dtype=out_dtype)
+    for before, behind in ((0, 1), (1, 0), (7, 9), (70, 33)):
+        ins = [None if t is None else surround(t[None], before, behind)[0] for t in x]
+        none = lambda n: torch.full((n,), -1, dtype=torch.int32, device="cuda")
+        S, T = pool.clone(), before + 9 + behind
+        spoil([torch.empty(T, 3, D, dtype=out_dtype, device="cuda")])
+        got = f(*ins, S, start, torch.cat([none(before), kept, none(behind)]), (cu + before).cuda(), out_dtype=out_dtype)
+        torch.cuda.synchronize()
+        assert torch.equal(got[before:before + 9], want) and torch.equal(S, first), (before, behind)
+        assert (got[:before] == 0).all() and (got[before + 9:] == 0).all(), (before, behind)
+        mine = torch.full_like(got, 3.0)
+        f(*ins, pool.clone(), start, None, (cu + before).cuda(), out=mine)
+        torch.cuda.synchronize()
+        assert (mine[:before] == 3).all() and (mine[before + 9:] == 3).all() and torch.equal(mine[before:before + 9], want)
+
+
+def test_recurrent_without_any_sequence():
+    x, _ = problem([20], 2, 64, "f32", "channel", 5)
+    x = [t[0] for t in x[:5]]
+    pool = torch.ones(2, 2, 64, 64, device="cuda")
+    for cu in ([0, 0], [20, 20, 20], [6, 6, 6], [50, 50]):
+        spoil([x[2]])
+        got = kda_recurrent(*x, pool, None, None, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        assert (got == 0).all() and (pool == 1).all(), cu
