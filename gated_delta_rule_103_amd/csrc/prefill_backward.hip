@@ -108,39 +108,55 @@ template <int M> __device__ __forceinline__ float lane_across(float x) {
     constexpr int ctrl = M == 8 ? 0x140 : M == 4 ? 0x141 : M == 2 ? 0x4e : 0xb1;
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), ctrl, 0xf, 0xf, true));
 }
-// fp32 products on the bf16 matrix cores. A value is cut into three bf16 parts of
-// eight significand bits each, h + m + l, exactly; of the nine products the three
-// below 2^-24 of the whole are left out, so the result is as good as an fp32
-// product's, at 6 / 16 of fp32 MFMA's time (3 / 16 where one side is bf16 already).
+// fp32 products on the bf16 matrix cores. A value x is cut into three bf16 parts of
+// eight significand bits each, x = h + m + l, exactly. Of the nine products of two values
+// the three smallest (m l, l m, l l) are left out. On one side of every product h and m are
+// rounded to nearest, so |m| <= 2^-8 |x| and |l| <= 2^-17 |x| and both have either sign; on
+// the other they may be truncated, |m| < 2^-7 |x| and |l| < 2^-15 |x|, which takes less. What
+// is left out is then at most 2^-23 + 2^-24 of the whole and 0 on average, an fp32
+// product's own rounding twice or so; six of nine products take 6 / 16 of fp32 MFMA's time
+// (3 / 16 where one side is bf16 already). With both sides truncated it would be up to
+// 8 x 2^-24, always downwards; with both rounded 2^-24, for 4% of the packed gradient's
+// time (265 -> 274 us). (A value that rounds beyond bf16's largest, 3.39e38, is not cut.)
 // MFMA 16x16x32: a lane holds row (column) l % 16 and eight inner indices of its
 // lane group l / 16; two float4 of neighbouring 16-wide tiles make one operand.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-// The high halves of a and b, which keep what these leave. With DOT, x - h is one
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float high_value(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// The first bf16 part of a and of b, rounded with NEAR and truncated without; a and b keep
+// what it leaves. With DOT, x - h is one
 // instruction, h still packed: a dot product of the pair with (-1, 0) or (0, -1) onto
 // x, exact like the subtraction. It is used where operands of many products are cut
 // at once (8k gradient 1284 -> 1259 us); where few values are cut and used at once,
 // in the scan of 16 channels, its latency costs more (packed gradient 266 -> 272 us).
-template <bool DOT> __device__ __forceinline__ uint32_t cut_pair(float &a, float &b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const uint32_t h = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+template <bool NEAR, bool DOT> __device__ __forceinline__ uint32_t cut_pair(float &a, float &b) {
+#pragma clang fp contract(off)                         // x is the product's rounded value in every variant
+    const uint32_t h = NEAR ? pack_bf16(a, b) : high_halves(a, b);
     if constexpr (DOT) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
         uint32_t first = 0xbf80u, second = 0xbf800000u;
         asm("" : "+s"(first), "+s"(second));           // as an immediate the first would reach the wrong half
         const bf16x2 hv = __builtin_bit_cast(bf16x2, h);
         a = __builtin_amdgcn_fdot2_f32_bf16(hv, __builtin_bit_cast(bf16x2, first), a, false);
         b = __builtin_amdgcn_fdot2_f32_bf16(hv, __builtin_bit_cast(bf16x2, second), b, false);
     } else {
-        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+        a -= NEAR ? __uint_as_float(h << 16) : high_value(__float_as_uint(a));
+        b -= high_value(NEAR ? h : __float_as_uint(b));
     }
     return h;
 }
-template <bool DOT> __device__ __forceinline__ void split3(f32x4 a, f32x4 b, u32v4 (&p)[3]) {
+// Part z of a pair, taken in turn: what two parts leave has eight bits.
+template <bool NEAR, bool DOT> __device__ __forceinline__ uint32_t part_of(int z, float &a, float &b) {
+    return z < 2 ? cut_pair<NEAR, DOT>(a, b) : high_halves(a, b);
+}
+template <bool NEAR, bool DOT> __device__ __forceinline__ void split3(f32x4 a, f32x4 b, u32v4 (&p)[3]) {
     float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
     for (int z = 0; z < 3; ++z)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[z][i] = cut_pair<DOT>(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) p[z][i] = part_of<NEAR, DOT>(z, x[2 * i], x[2 * i + 1]);
 }
 __device__ __forceinline__ f32x4 mfma32(u32v4 a, u32v4 b, f32x4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
@@ -705,8 +721,8 @@ __global__ __launch_bounds__(4 * D, D == 128 ? 4 : 2) void prep_kernel(Common p,
 // A workgroup of four wavefronts carries TV = 16 JT value channels (rows j of S,
 // the accumulators' rows) of one chain; wavefront w owns D / 4 key channels of S
 // and the w-th 16 tokens of a chunk. Left operands pass through LDS cut in three
-// bf16 parts; right operands come from the record and are cut in registers, once
-// for the JT tiles.
+// rounded bf16 parts; right operands come from the record and are cut in registers by
+// truncation, once for the JT tiles.
 template <int D, int TV, int PO>
 struct ScanLds {
     uint16_t S[3][TV][D + 8];         // the state
@@ -755,16 +771,33 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
     // chunk cover the latency.
     const int tau = 16 * w + lr, tau_col = inner(tau);   // this lane's token where tokens are columns
     auto item_of = [&](int step) { return item0 + (back ? chunks - 1 - step : step); };
-    // an accumulator (rows 4 lg + r of tile y) into column `col` of an LDS matrix
+    // an accumulator (rows 4 lg + r of tile y) into column `col` of an LDS matrix, cut in
+    // three rounded parts: in pairs where two tiles' work covers the latency, one by one
+    // with the same rounding by an addition else (packed gradient 267 us against 270)
     auto put = [&](auto &m, int y, int col, f32x4 x) {
+#pragma clang fp contract(off)
+        if constexpr (TV == 32) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            float f = x[r];
+            for (int r = 0; r < 4; r += 2) {
+                float f0 = x[r], f1 = x[r + 1];
 #pragma unroll
-            for (int z = 0; z < 3; ++z) {
-                const uint32_t u = __float_as_uint(f);
-                m[z][16 * y + 4 * lg + r][col] = static_cast<uint16_t>(u >> 16);
-                f -= __uint_as_float(u & 0xffff0000u);
+                for (int z = 0; z < 3; ++z) {
+                    const uint32_t u = part_of<true, true>(z, f0, f1);
+                    m[z][16 * y + 4 * lg + r][col] = static_cast<uint16_t>(u);
+                    m[z][16 * y + 4 * lg + r + 1][col] = static_cast<uint16_t>(u >> 16);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float f = x[r];
+#pragma unroll
+                for (int z = 0; z < 3; ++z) {
+                    uint32_t u = __float_as_uint(f);
+                    if (z < 2) u += 0x7fffu + __builtin_amdgcn_ubfe(u, 16, 1);     // to nearest, ties to even
+                    m[z][16 * y + 4 * lg + r][col] = static_cast<uint16_t>(u >> 16);
+                    f -= high_value(u);
+                }
             }
         }
     };
@@ -808,7 +841,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
             u32v4 b[3];
-            split3<TV == 32>(x[2 * m], x[2 * m + 1], b);
+            split3<false, TV == 32>(x[2 * m], x[2 * m + 1], b);
 #pragma unroll
             for (int y = 0; y < JT; ++y) {
                 u32v4 a[3];
@@ -824,7 +857,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
         for (int m = 0; m < 2; ++m)
             if (back ? 2 * m + 1 >= w : 2 * m <= w) {
                 u32v4 b[3];
-                split3<TV == 32>(x[2 * m], x[2 * m + 1], b);
+                split3<false, TV == 32>(x[2 * m], x[2 * m + 1], b);
 #pragma unroll
                 for (int y = 0; y < JT; ++y) {
                     u32v4 a[decltype(parts)::value];
@@ -843,7 +876,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 u32v4 b[3];
-                split3<TV == 32>(x[i][2 * m], x[i][2 * m + 1], b);
+                split3<false, TV == 32>(x[i][2 * m], x[i][2 * m + 1], b);
 #pragma unroll
                 for (int y = 0; y < JT; ++y) st[y][i] = product(a[y], b, st[y][i]);
             }
@@ -908,7 +941,7 @@ __global__ __launch_bounds__(256, 2) void scan_kernel(Common p, const TI *__rest
 #pragma unroll
                     for (int z = 0; z < Parts::value; ++z) {
                         uint32_t u = ov[y][r / 2];
-                        if constexpr (Parts::value == 3) u = cut_pair<false>(f0, f1);
+                        if constexpr (Parts::value == 3) u = part_of<true, false>(z, f0, f1);
                         s.O[z][16 * y + oj + r][inner(ot)] = static_cast<uint16_t>(u);
                         s.O[z][16 * y + oj + r + 1][inner(ot)] = static_cast<uint16_t>(u >> 16);
                     }
@@ -1083,11 +1116,11 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
         if (stage) __syncthreads();
         {
             const int j = 32 * (stage * SM + sm) + 4 * lg;
-            u32v4 o[PO], u[3], v[3];
+            u32v4 o[PO], u[3], v[3];                   // u and the states M are the rounded sides
             if constexpr (PO == 1) o[0] = u32v4{o0[0], o0[1], o1[0], o1[1]};
-            else split3<true>(Rows<TG>::value4(o0), Rows<TG>::value4(o1), o);
-            split3<true>(e0 * be, e1 * be, u);
-            split3<true>(y0 * be, y1 * be, v);
+            else split3<false, true>(Rows<TG>::value4(o0), Rows<TG>::value4(o1), o);
+            split3<true, true>(e0 * be, e1 * be, u);
+            split3<false, true>(y0 * be, y1 * be, v);
             if (first) {
                 dvr.put4(stau, j, y0 * be);
                 dvr.put4(stau, j + 16, y1 * be);
@@ -1112,8 +1145,8 @@ __global__ __launch_bounds__(4 * CH, 2) void finish_kernel(Common p, const TI *_
             u32v4 ms[3], ds[3];
             const f32x4 x = m0[m] * d0[m] + m1[m] * d1[m];
             mdm += (x[0] + x[1]) + (x[2] + x[3]);
-            split3<true>(m0[m], m1[m], ms);
-            split3<true>(d0[m], d1[m], ds);
+            split3<true, true>(m0[m], m1[m], ms);
+            split3<false, true>(d0[m], d1[m], ds);
             load_states(next, m);
             // operands of the next block are read while this one's products run
             u32v4 o[2][PO], u[2][3], v[2][3];

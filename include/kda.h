@@ -385,7 +385,7 @@ int kda_recurrent_padded(const void *q, const void *k, const void *v, const floa
  *
  * Arithmetic, states and their gradients in fp32 (matrix products on fp32
  * instructions, or on bf16 ones with every operand cut in three), for any magnitude
- * of dout whose products stay between about 1e-33 and fp32's largest; a bf16 gradient
+ * of dout whose products stay between about 1e-33 and 3.3e38; a bf16 gradient
  * is the rounded fp32 value. A log-decay of -104 or less
  * (exp is 0 in fp32; -inf wipes a channel) has gradient 0. Results repeat bit for
  * bit.
