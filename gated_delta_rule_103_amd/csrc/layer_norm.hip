@@ -91,13 +91,13 @@ __device__ __forceinline__ float row_sum(float x, float *part, int wave_in_row) 
 }
 
 // One group of eight channels as it lies in memory, so that a row can be loaded
-// ahead in half the registers.
+// ahead in half the registers. Rows start on 16-byte boundaries, which is all that an
+// fp32 group may be loaded by.
 template <bool VEC, typename T> struct Group {
-    typedef std::conditional_t<sizeof(T) == 4, f32x8, u32x4> Packed;
-    std::conditional_t<VEC, Packed, f32x8> u;
+    std::conditional_t<VEC && sizeof(T) == 2, u32x4, f32x8> u;
     __device__ void load(const T *row, int c, int step, int W) {
-        if constexpr (VEC) u = c < W ? *reinterpret_cast<const Packed *>(row + c) : Packed{};
-        else u = load8<false>(row, c, step, W);
+        if constexpr (VEC && sizeof(T) == 2) u = c < W ? *reinterpret_cast<const u32x4 *>(row + c) : u32x4{};
+        else u = load8<VEC>(row, c, step, W);
     }
     __device__ f32x8 value() const {
         if constexpr (!VEC || sizeof(T) == 4) {
