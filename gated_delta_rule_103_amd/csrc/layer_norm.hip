@@ -303,9 +303,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
     }
 }
 
-// rows of the partial sums: as many workgroups as keep the card busy, never
-// more than there are rows for
-// and one for a few rows, whose sums then are the gradients themselves
+// Rows of the partial sums, one for each workgroup: as many as keep the card busy, never
+// more than there are rows for, and one for a few rows, whose sums then are the gradients
+// themselves.
 int partial_rows(long long rows, int rows_per_wg) {
     if (rows > 0 && rows <= 4 * rows_per_wg) return 1;
     const long long wgs = (rows + rows_per_wg - 1) / rows_per_wg;

@@ -301,7 +301,6 @@ template <typename T> struct Rows {
         }
     }
     __device__ float at(int tau, int c) const { return value(raw(tau, c)); }
-    __device__ f32x4 at4(int tau, int c) const { return value4(raw4(tau, c)); }
     __device__ void put(int tau, int c, float x) const {
         const int off = (tau * row + c) * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);

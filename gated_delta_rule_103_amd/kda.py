@@ -507,7 +507,10 @@ def kda_recurrent(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, *, out=Non
     S: [slots, H, Dv, Dk] fp32. slot_in (int32 [N], or None): the slot a sequence starts from,
     negative = the zero state; slot_out (int32 [T], or None): the slot that receives the state
     after a token, negative = none. All index tensors on the device. Returns out [T, H, Dv];
-    rows of tokens in no sequence are zero, but left as they were in an ``out`` that is given."""
+    rows of tokens in no sequence are zero, but left as they were in an ``out`` that is given.
+    A slot that one sequence keeps a state in must not be the start of another sequence of the
+    call, nor be kept by one: the states in it are then undefined, and nothing can check it.
+    """
     return _recurrent("kda_recurrent", q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream,
                       qk_l2norm, l2norm_eps)
 
@@ -516,7 +519,7 @@ def gdn_recurrent(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, *, out=Non
                   out_dtype: Optional[torch.dtype] = None, stream=None, qk_l2norm: bool = False,
                   l2norm_eps: float = 1e-6):
     """kda_recurrent with the scalar gate of Gated DeltaNet: g [T, H] fp32, or None
-    for DeltaNet (no decay)."""
+    for DeltaNet (no decay); its rule for slots that sequences share holds too."""
     return _recurrent("gdn_recurrent", q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens, out, out_dtype, stream,
                       qk_l2norm, l2norm_eps)
 

@@ -393,9 +393,10 @@ int kda_recurrent_padded(const void *q, const void *k, const void *v, const floa
  * KDA_BF16 with either; (T_total / 64 + N + 1) * H below 2^23. opt->snapshots
  * must be NULL; opt may be NULL. All tensors but beta, dbeta and a per-head g, dg
  * must be 16-byte aligned. No gradient may be any other buffer of the call.
- * workspace: kda_prefill_backward_workspace_size bytes (about 380 KB per
- * 64 tokens and head at Dk = 128, 170 KB at 64), 256-byte aligned, its contents
- * ignored, not used by anything else until the call's work has finished.
+ * workspace: kda_prefill_backward_workspace_size bytes, 256-byte aligned, its contents
+ * ignored, not used by anything else until the call's work has finished. That is about
+ * (ceil(T_total / 64) + N) * H times 381 KB at Dk = 128, 169 KB at 64: every sequence,
+ * an empty one too, adds a chunk's share for each head.
  * The size function returns 0 for sizes that the call rejects.
  */
 size_t kda_prefill_backward_workspace_size(int N, int T_total, int H, int Dk, int Dv);
@@ -434,7 +435,8 @@ int kda_prefill_backward_padded(const void *q, const void *k, const void *v, con
  *   o, gate, weight, rows, H, Dv, eps  as for kda_output_gate
  *   dout [rows][H][Dv] dout_dtype;  d_o o_dtype;  dgate gate_dtype
  *   dweight [Dv] fp32, or NULL to skip it (weight may be NULL, ones)
- * fp32 arithmetic; dweight's sum has a fixed order. rows == 0 gives dweight = 0.
+ * fp32 arithmetic (o of at most 1e18 in magnitude: its squares are summed); dweight's sum has a
+ * fixed order. rows == 0 gives dweight = 0.
  * No gradient may be any other buffer of the call. Alignment, support and errors
  * as for kda_output_gate. workspace: kda_output_gate_backward_workspace_size bytes
  * (at most 1 MiB), 256-byte aligned; may be NULL when that is 0 or dweight is NULL.
@@ -456,7 +458,8 @@ int kda_output_gate_backward(const void *o, const void *gate, const void *dout, 
  *   mean, rstd    [rows] fp32, kept for the backward pass; NULL to skip (mean
  *        must be NULL for RMS)
  *   eps  > 0
- * fp32 arithmetic; the variance is the mean square of centred values. Any W from 1
+ * fp32 arithmetic (x of at most 1e17 in magnitude: its squares are summed); the variance
+ * is the mean square of centred values. Any W from 1
  * to 16384 (above: KDA_ERR_UNSUPPORTED) and any alignment of the element type;
  * fastest with W a multiple of 8 and 16-byte aligned x, out, weight and bias.
  * rows == 0 launches nothing.
