@@ -27,20 +27,22 @@
 // in prep (a second product through TE or TY costs the scan a barrier and 24 matrix
 // instructions a chunk).
 //
-// Three kernels (times: 8192 tokens x 32 heads x 128 channels, bf16, in a call of 1.2 ms):
+// Three kernels (times: 8192 tokens x 32 heads x 128 channels, bf16; average and range of
+// 60 launches under the profiler, where they take a little longer than in a call of
+// 1.17-1.23 ms among others):
 //   prep    every (chunk, head): P, A, both inverses and the matrices above to a
-//           record. 270 us; 0.27 GB in, 0.76 GB out (3.7 TB/s), matrix units busy 34%,
-//           vector units 42% of the time, between barriers that two workgroups a CU
+//           record. 274 us (261-358); 0.27 GB in, 0.76 GB out (3.8 TB/s), matrix units busy
+//           34%, vector units 43% of the time, between barriers that two workgroups a CU
 //           cover for each other
 //   scan    every (sequence, head, 16 or 32 value channels), once forwards for M
 //           and E and once backwards for dM' and Y. Value channels never meet in
 //           either recurrence, and neither needs the other, so both run in one
-//           launch. 510 us; 0.92 GB in, 0.81 GB out (3.3 TB/s), matrix units 23%, vector
-//           units 30%, one wavefront a SIMD: a chain's chunks wait for one another
+//           launch. 500 us (468-653); 0.92 GB in, 0.81 GB out (3.5 TB/s), matrix units 23%,
+//           vector units 30%, one wavefront a SIMD: a chain's chunks wait for one another
 //   finish  every (chunk, head, 64 key channels): all gradients but dS0 from M,
-//           dM', E and Y. 485 us; bound by instruction issue: vector instructions
+//           dM', E and Y. 494 us (468-641); bound by instruction issue: vector instructions
 //           43% and matrix instructions 40% of the cycles at two wavefronts a SIMD;
-//           1.15 GB in, 0.34 GB out
+//           1.15 GB in, 0.34 GB out (3.0 TB/s)
 //
 // The call's floor is 145 us for inputs and outputs (739 MB at 5.1 TB/s); chunks of 64
 // tokens leave 0.8 GB of states beside them, each written and read once.

@@ -16,8 +16,9 @@
 // each), as in the single-token kernel, so both dot products of a row are
 // sums inside those lanes. The next token's vectors are loaded while the
 // current one is computed. 128 sequences x 4 tokens x 32 heads x 128 channels with every
-// state kept: 1.37 GB in 254 us, 5.4 TB/s (a large copy: 5.1). One sequence x 3 tokens:
-// 8 us, the latency of three dependent tokens behind that of loading a state.
+// state kept: 1.38 GB in 276 us (255-303 over 60 launches under the profiler), 5.0 TB/s, the
+// rate of a large copy, 5.1. One sequence x 3 tokens: 8 us, the latency of three dependent
+// tokens behind that of loading a state.
 #include "kda_device.h"
 #include "kda_launch.h"
 
