@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_abi.cpp", "decode.hip", "prefill_f32.hip", "prefill_mfma.hip", "output_gate.hip",
-           "noalloc.hip", "recurrent.hip", "prefill_backward.hip", "output_gate_backward.hip", "layer_norm.hip"]
+           "noalloc.hip", "recurrent.hip", "prefill_backward.hip", "output_gate_backward.hip", "layer_norm.hip",
+           "lin_abi.cpp", "serving_abi.cpp", "lin_chunk.hip", "lin_recurrent.hip", "tree.hip", "slots.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",

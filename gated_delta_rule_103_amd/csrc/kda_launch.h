@@ -138,6 +138,88 @@ struct LayerNormBackwardArgs {
     hipStream_t stream;
 };
 
+struct LinPrefillArgs {
+    const void *q, *k, *v;      // q, k of Hk heads, v of H
+    const float *g;             // [T_total][H], fixed: [H]; nullptr: no decay
+    const float *S0;            // or nullptr (zero)
+    void *out;
+    float *S_out;               // or nullptr (not wanted)
+    const int32_t *cu_seqlens;  // device, or nullptr (dense)
+    int N, B, T, H, Hk, Dk, Dv;
+    Dt io, out_dt;
+    bool fixed, zero_rows;
+    void *ws;
+    hipStream_t stream;
+};
+
+struct LinBackwardArgs {
+    const void *q, *k, *v;
+    const float *g;
+    const void *dout;
+    const float *S0, *dS_out;   // or nullptr (zero)
+    void *dq, *dk, *dv;
+    float *dg, *dS0;            // dg nullptr when g is; dS0 or nullptr (not wanted)
+    const int32_t *cu_seqlens;
+    int N, B, T, H, Hk, Dk, Dv;
+    Dt io;
+    bool fixed;
+    int zero_rows;              // KDA_ZERO_*
+    void *ws;
+    hipStream_t stream;
+};
+
+struct LinRecurrentArgs {
+    const void *q, *k, *v;
+    const float *g;
+    float *S;                   // [slots][H][Dv][Dk]
+    void *out;
+    const int32_t *cu;          // [N + 1], device; nullptr: one token per sequence, sequence n in slot n
+    const int32_t *slot_in;     // [N], device, or nullptr (zero states)
+    const int32_t *slot_out;    // [T], device, or nullptr (no state is kept)
+    int N, T, H, Hk, Dk, Dv, slots;
+    Dt io, out_dt;
+    bool fixed, zero_rows;
+    hipStream_t stream;
+};
+
+struct TreeArgs {
+    const void *q, *k, *v;      // [N][T][Hk or H][D]
+    const float *g;
+    const void *beta;           // or nullptr: no delta rule
+    float *S;                   // [slots][H][Dv][Dk]
+    void *out;                  // [N][T][H][Dv]
+    const int32_t *slot_in;     // [N] or nullptr (zero states)
+    const int32_t *slot_out;    // [N], accept only
+    const int32_t *parent;      // [N][T]
+    const int32_t *node;        // [N], accept only
+    int N, T, H, Hk, Dk, Dv, slots;
+    Dt io, beta_dt, out_dt;
+    int gate;                   // kda_gate
+    bool qk_norm;
+    float norm_eps;
+    bool zero_rows;
+    hipStream_t stream;
+};
+
+struct SlotsCopyArgs {
+    const char *from;
+    char *to;
+    const int32_t *src, *dst;
+    int n, layers, from_slots, to_slots;
+    size_t slot_bytes;
+    hipStream_t stream;
+};
+
+struct SlotsCompactArgs {
+    char *pool;
+    int32_t *uses, *count;
+    int32_t *table;             // entries naming slots, or nullptr
+    int slots, layers, table_n;
+    size_t slot_bytes;
+    int32_t *moved;             // workspace: [slots] new place of each slot, then the moves
+    hipStream_t stream;
+};
+
 // Upper bound on the number of chunks of all sequences (each sequence adds at
 // most one partial chunk).
 inline long long max_chunks(int N, long long T_total, int C) {
@@ -179,6 +261,28 @@ hipError_t launch_prefill_backward(const PrefillBackwardArgs &a);
 // the output gate's gradient.
 size_t output_gate_backward_workspace(long long rowheads, int Dv);
 hipError_t launch_output_gate_backward(const OutputGateBackwardArgs &a);
+
+// linear attention with a decay per head: chunked, its gradient, and the recurrent form.
+size_t lin_prefill_workspace(int N, long long T_total, int H, int Dk, int Dv);
+size_t lin_backward_workspace(int N, long long T_total, int H, int Hk, int Dk, int Dv);
+bool lin_chunk_fits(int N, long long T_total, int H);
+hipError_t launch_lin_prefill(const LinPrefillArgs &a);
+hipError_t launch_lin_backward(const LinBackwardArgs &a);
+bool lin_recurrent_fits(int N, int H, int Dk, int Dv);
+hipError_t launch_lin_recurrent(const LinRecurrentArgs &a);
+
+// trees of drafted tokens over a state each, and the state behind an accepted node.
+constexpr int kMaxTreeNodes = 64;
+bool tree_fits(int N, int H);
+hipError_t launch_tree(const TreeArgs &a);
+hipError_t launch_tree_accept(const TreeArgs &a);
+
+// the slots of a state pool. fits: the launch stays within the runtime's limits.
+bool slots_copy_fits(long long n, int layers, size_t slot_bytes);
+hipError_t launch_slots_copy(const SlotsCopyArgs &a);
+hipError_t launch_slots_count(int32_t *uses, const int32_t *which, int n, int slots, int add, hipStream_t stream);
+hipError_t launch_slots_acquire(int32_t *uses, int slots, int32_t *taken, int n, hipStream_t stream);
+hipError_t launch_slots_compact(const SlotsCompactArgs &a);
 
 // layer norm and RMS norm of rows of at most kMaxNormWidth channels, and the gradient.
 constexpr int kMaxNormWidth = 16384;

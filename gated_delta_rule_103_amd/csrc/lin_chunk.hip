@@ -1,0 +1,951 @@
+// lin_chunk.hip -- linear attention with a decay per head, chunked: the forward pass over
+// whole sequences and the gradient.
+//
+//     S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = S_t q_t
+//
+// With a = the cumulative sum of g inside a chunk and S the state before it:
+//     o_t = e^{a_t} S q_t + sum_{s <= t} e^{a_t - a_s} (q_t . k_s) v_s
+//     S  <- e^{a_C} S + sum_s e^{a_C - a_s} v_s k_s^T
+// The gradients of q, k and v are this form again, over other tensors and, for k and v,
+// backwards in time: dq = F(dout, v, k), dk = F(v, dout, q) and dv = F(k, q, dout), F(x, y, z)
+// being the outputs for queries x, keys y and values z. So one kernel serves all four.
+//
+// Split: the tokens of a sequence are cut into segments. Without states at the segments'
+// borders a chain is one workgroup's serial walk; with them every (segment, head) is a
+// workgroup of its own. state_kernel sums each segment's own contribution, border_kernel
+// carries the states across segments, output_kernel walks a segment's chunks from its border
+// state. Costs a second read of two of the tensors and 8 D^2 bytes a segment and pass.
+//
+// Arithmetic: bf16 matrix instructions with fp32 accumulators. An operand that is no bf16
+// value (decayed, a state, fp32 input) is cut into bf16 parts whose sum it is to 2^-17 (two)
+// or 2^-25 (three); of parts i and j the products i + j < the number of parts are taken.
+// States take three always; outputs in bf16 two, outputs in fp32 and those that a decay's
+// gradient is summed from three. The exponents of decays are differences of cumulative sums
+// that are taken in 64 bits and held as whole and fractional part in base 2, so that no
+// difference loses bits and no factor exceeds the decay that it stands for.
+//
+// A wavefront owns 32 value channels: its part of the state, transposed, stays in accumulator
+// layout (32 x 32 tiles: column = value channel, rows = key channels), whose registers are,
+// up to the order of the summed index, the A operand of the product with q^T; the score tile
+// q k^T is formed transposed for the same reason. Only scores go through LDS, because the
+// wavefronts share them.
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kMinLog = -104.f;       // e^-104 rounds to zero: a smaller decay is no other
+
+constexpr int kMaxSegment = 1024;
+
+struct Segments {
+    const int32_t *cu;      // packed offsets, or nullptr: N sequences of T tokens
+    int N, T, T_total, L;   // L tokens a segment
+};
+struct Gate {
+    const float *g;         // [tokens][H], fixed: [H]; nullptr: none
+    bool fixed;
+};
+// One sum over segments: keys y, values z (a shared tensor has a head per group of heads).
+struct StateJob {
+    const void *y, *z;
+    float *out;             // [ids][H][value channels][key channels]
+    bool y_shared, z_shared, tail, skip_last;
+};
+struct StateJobs { StateJob job[2]; };
+struct BorderArgs {
+    const float *S0, *dS_out;
+    float *states, *grads, *dS0, *dots;
+    const float *whole;     // each segment's decay
+    bool all;               // the gradients' states too
+};
+struct OutputJob {
+    const void *x, *y, *z, *with;
+    void *out;
+    float *dot, *past;      // [H][T_total], and a chunk's part from the state [ids][H][chunks of a segment]
+    const float *S;         // the state before each segment (border) or sequence, or nullptr
+    float *S_out;           // the state behind each sequence, or nullptr
+    bool x_shared, y_shared, z_shared, out_shared, border, key_rows, back, zero_rows;
+};
+struct OutputJobs { OutputJob job[3]; };
+
+// ---- sequences and segments -------------------------------------------------
+// Segment ids need no table: sequence n starts at id begin_n / L + n, which leaves room for
+// ceil(length / L) ids (one for an empty sequence) and grows with n, so an id's sequence is
+// found by bisection. Ids between two sequences' are holes.
+struct Segment {
+    int n, begin, end;      // the sequence and its tokens
+    int b, blocks;          // this segment's index in it, and how many it has
+};
+
+__device__ __forceinline__ void sequence_bounds(const Segments &s, int n, int &begin, int &end) {
+    if (!s.cu) {
+        begin = n * s.T;
+        end = begin + s.T;
+        return;
+    }
+    begin = min(max(s.cu[n], 0), s.T_total);        // offsets outside the packed rows are cut to them
+    end = min(max(s.cu[n + 1], begin), s.T_total);
+}
+__device__ __forceinline__ int block_count(const Segments &s, int len) { return max(1, (len + s.L - 1) / s.L); }
+__device__ __forceinline__ int first_id(const Segments &s, int n, int begin) { return begin / s.L + n; }
+
+// false: a hole
+__device__ __forceinline__ bool find_segment(const Segments &s, int id, Segment &x) {
+    int lo = 0, hi = s.N - 1;
+    while (lo < hi) {                               // the last sequence that starts at or before id
+        const int mid = (lo + hi + 1) / 2;
+        const int at = s.cu ? min(max(s.cu[mid], 0), s.T_total) : mid * s.T;
+        if (first_id(s, mid, at) <= id) lo = mid; else hi = mid - 1;
+    }
+    x.n = lo;
+    sequence_bounds(s, lo, x.begin, x.end);
+    x.blocks = block_count(s, x.end - x.begin);
+    x.b = id - first_id(s, lo, x.begin);
+    return x.b >= 0 && x.b < x.blocks;
+}
+
+// ---- cutting ----------------------------------------------------------------
+template <int P> __device__ __forceinline__ void cut(f32x8 x, bf16x8 (&p)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        p[i] = __builtin_convertvector(x, bf16x8);
+        if (i + 1 < P) x -= __builtin_convertvector(p[i], f32x8);
+    }
+}
+
+// acc += x y, x in PX parts and y in PY, products of parts whose indices add up to less than the larger count
+template <int PX, int PY>
+__device__ __forceinline__ f32x16 product(const bf16x8 (&x)[PX], const bf16x8 (&y)[PY], f32x16 acc) {
+    constexpr int P = PX > PY ? PX : PY;
+#pragma unroll
+    for (int i = PX - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = PY - 1; j >= 0; --j)
+            if (i + j < P) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc, 0, 0, 0);
+    return acc;
+}
+
+// ---- tiles in LDS -----------------------------------------------------------
+// Rows of D bf16 values in blocks of four, a row's blocks permuted by an exclusive or with
+// swz(row): 32 rows at one block, and four rows at eight neighbouring blocks (the transposing
+// read), both touch every bank once.
+template <int D> __device__ __forceinline__ int swz(int row) {
+    return D == 128 ? ((row & 3) << 3) | ((row >> 2) & 7) : (((row >> 1) & 1) << 3) | ((row >> 2) & 7);
+}
+template <int D> __device__ __forceinline__ int at(int row, int block) { return row * D + ((block ^ swz<D>(row)) << 2); }
+
+// The 16 values of a k-step m (of 16 channels) that a lane holds of a row, in the order of an
+// accumulator's rows: 16m + 4h .. + 3 and 16m + 8 + 4h .. + 3, h = lane / 32.
+template <int D> __device__ __forceinline__ bf16x8 row_frag(const bf16_t *tile, int row, int m, int h) {
+    const bf16x4 x = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 4 * m + h));
+    const bf16x4 y = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 4 * m + 2 + h));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// The transpose: channel 32c + lane % 32 of tokens 16m + 4h .. + 3 and 16m + 8 + 4h .. + 3.
+__device__ __forceinline__ bf16x4 read_tr(const bf16_t *p) {
+    const i16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)p);
+    return __builtin_bit_cast(bf16x4, r);
+}
+template <int D> __device__ __forceinline__ bf16x8 col_frag(const bf16_t *tile, int c, int m, int lane) {
+    const int h = lane >> 5, j = lane & 15, block = 8 * c + ((lane >> 4) & 1) * 4 + (j & 3);
+    const bf16x4 x = read_tr(tile + at<D>(16 * m + 4 * h + (j >> 2), block));
+    const bf16x4 y = read_tr(tile + at<D>(16 * m + 8 + 4 * h + (j >> 2), block));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A chunk's rows of one tensor on their way from memory to LDS: C rows of D values by NT threads.
+template <typename T, int D, int C, int NT, int NI> struct Rows {
+    static constexpr int PER = 16 / sizeof(T);              // values of a 16-byte load
+    static constexpr int N = C * D / PER / NT;              // loads of a thread
+    static_assert(C * D % (PER * NT) == 0, "chunk rows per thread");
+    u32x4 x[N];
+
+    // rows i0 .. i0 + C - 1 of a segment; row i is token first + i * step where lo <= i < hi, zeros elsewhere
+    __device__ __forceinline__ void load(const T *p, size_t stride, long long first, int step, int i0, int lo, int hi, int t) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int u = t + n * NT, row = i0 + u / (D / PER);
+            x[n] = u32x4{0u, 0u, 0u, 0u};
+            if (row >= lo && row < hi)
+                x[n] = *reinterpret_cast<const u32x4 *>(p + (size_t)(first + (long long)row * step) * stride +
+                                                        (u % (D / PER)) * PER);
+        }
+    }
+    __device__ __forceinline__ void store(bf16_t *tile, int t) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int u = t + n * NT, row = u / (D / PER), e = u % (D / PER);
+            if constexpr (NI == 1) {
+                *reinterpret_cast<u32x2 *>(tile + at<D>(row, 2 * e)) = u32x2{x[n][0], x[n][1]};
+                *reinterpret_cast<u32x2 *>(tile + at<D>(row, 2 * e + 1)) = u32x2{x[n][2], x[n][3]};
+            } else {
+                f32x4 y = __builtin_bit_cast(f32x4, x[n]);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const bf16x4 p = __builtin_convertvector(y, bf16x4);
+                    *reinterpret_cast<bf16x4 *>(tile + i * C * D + at<D>(row, e)) = p;
+                    y -= __builtin_convertvector(p, f32x4);
+                }
+            }
+        }
+    }
+};
+
+// ---- decays -----------------------------------------------------------------
+__device__ __forceinline__ double wave_prefix(double x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+__device__ __forceinline__ float gate_at(const Gate &g, long long token, int h, int H) {
+    if (!g.g) return 0.f;
+    const float x = g.fixed ? g.g[h] : g.g[token * H + h];
+    return x < kMinLog ? kMinLog : x;
+}
+
+// Cumulative log2-decays of a segment's rows lo .. hi - 1: whole part in A[i].x, fraction in A[i].y (rows
+// before lo: none). Row i is token first + i * step. Backwards (step -1) the decay of row i is that of
+// the token before it in walking order, and row lo has none. Returns the sum over the segment's tokens.
+template <int NT>
+__device__ __forceinline__ double segment_decays(const Gate &g, int h, int H, long long first, int step, int lo, int hi,
+                                                 float2 *A, double *waves, int t) {
+    constexpr int NW = NT / 64;
+    const int per = (hi + NT - 1) / NT, i0 = t * per, i1 = min(i0 + per, hi);
+    auto at = [&](int i) {
+        if (i < lo || (step < 0 && i == lo)) return 0.;
+        return (double)gate_at(g, first + (long long)(step > 0 ? i : 1 - i), h, H) * 1.4426950408889634;
+    };
+    double sum = 0.;
+    for (int i = i0; i < i1; ++i) sum += at(i);
+    const double incl = wave_prefix(sum, t & 63);
+    if ((t & 63) == 63) waves[t >> 6] = incl;
+    __syncthreads();
+    double run = incl - sum, total = 0.;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < (t >> 6)) run += waves[w];
+        total += waves[w];
+    }
+    for (int i = i0; i < i1; ++i) {
+        run += at(i);
+        const double whole = floor(run);
+        A[i] = float2{(float)whole, (float)(run - whole)};
+    }
+    if (step < 0 && hi > lo) total += (double)gate_at(g, first - (hi - 1), h, H) * 1.4426950408889634;
+    __syncthreads();
+    return total;
+}
+__device__ __forceinline__ float decay(float2 to, float2 from) {
+    return __builtin_amdgcn_exp2f((to.x - from.x) + (to.y - from.y));
+}
+
+// ---- a segment's own contribution to the state -------------------------------
+// S^T = sum_i w_i y_i z_i^T over the segment, y [DA] keys and z [DC] values; w_i is the decay
+// from row i to the segment's end (`tail`), or from its start through row i.
+template <typename T, int DA, int DC, int NI, int C>
+__global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate gate, StateJobs jobs, float *whole, int H,
+                                                          int group) {
+    constexpr int NT = DC * 2, ND = DA / 32;
+    __shared__ bf16_t Y[NI * C * DA], Z[NI * C * DC];
+    __shared__ float2 A[kMaxSegment];
+    __shared__ double waves[NT / 64];
+    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5;
+    Segment x;
+    if (!find_segment(segs, id, x)) return;
+    const StateJob &job = jobs.job[blockIdx.y];
+    if (job.skip_last && x.b == x.blocks - 1) return;
+    const long long first = x.begin + (long long)x.b * segs.L;
+    const int len = min(segs.L, x.end - (int)first);
+    const double total = segment_decays<NT>(gate, h, H, first, 1, 0, len, A, waves, t);
+    if (t == 0 && blockIdx.y == 0) whole[(size_t)id * H + h] = (float)exp2(total);
+
+    const T *y = static_cast<const T *>(job.y) + (job.y_shared ? h / group : h) * DA;
+    const T *z = static_cast<const T *>(job.z) + (job.z_shared ? h / group : h) * DC;
+    const size_t ys = (size_t)(job.y_shared ? H / group : H) * DA, zs = (size_t)(job.z_shared ? H / group : H) * DC;
+    const double tw = floor(total);
+    const float2 end = float2{(float)tw, (float)(total - tw)};
+
+    f32x16 S[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) S[d] = f32x16{};
+    Rows<T, DA, C, NT, NI> ry;
+    Rows<T, DC, C, NT, NI> rz;
+    ry.load(y, ys, first, 1, 0, 0, len, t);
+    rz.load(z, zs, first, 1, 0, 0, len, t);
+    for (int c0 = 0; c0 < len; c0 += C) {
+        __syncthreads();
+        ry.store(Y, t);
+        rz.store(Z, t);
+        __syncthreads();
+        if (c0 + C < len) {
+            ry.load(y, ys, first, 1, c0 + C, 0, len, t);
+            rz.load(z, zs, first, 1, c0 + C, 0, len, t);
+        }
+#pragma unroll
+        for (int m = 0; m < C / 16; ++m) {
+            f32x8 zw = {};
+#pragma unroll
+            for (int i = NI - 1; i >= 0; --i)
+                zw += __builtin_convertvector(col_frag<DC>(Z + i * C * DC, w, m, lane), f32x8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = min(c0 + 16 * m + 8 * (e >> 2) + 4 * half + (e & 3), len - 1);
+                zw[e] *= job.tail ? decay(end, A[i]) : __builtin_amdgcn_exp2f(A[i].x + A[i].y);
+            }
+            bf16x8 zp[3];
+            cut<3>(zw, zp);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                bf16x8 yp[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) yp[i] = col_frag<DA>(Y + i * C * DA, d, m, lane);
+                S[d] = product<NI, 3>(yp, zp, S[d]);
+            }
+        }
+    }
+    float *out = job.out + ((size_t)id * H + h) * DA * DC + (size_t)(32 * w + (lane & 31)) * DA + 4 * half;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * i) =
+                f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]};
+}
+
+// ---- states at the segments' borders ------------------------------------------
+// Forward: each segment's own sum is replaced by the state before it. Backward (dS): the same
+// from the last segment on, for the gradient of the state behind a segment; with both, their
+// inner products at every border, which the decays' gradients end on.
+__global__ __launch_bounds__(256) void border_kernel(Segments segs, BorderArgs a, int H, int DD) {
+    __shared__ float sums[4];
+    const int n = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x;
+    const size_t e = ((size_t)blockIdx.y * 256 + t) * 4;
+    int begin, end;
+    sequence_bounds(segs, n, begin, end);
+    const int blocks = block_count(segs, end - begin), id0 = first_id(segs, n, begin);
+    const size_t own = ((size_t)n * H + h) * DD + e, step = (size_t)H * DD;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    auto load = [&](const float *p) { return *reinterpret_cast<const f32x4 *>(p); };
+    f32x4 cur = a.S0 ? load(a.S0 + own) : zero;
+    float *p = a.states + ((size_t)id0 * H + h) * DD + e;
+    const float *g = a.whole + (size_t)id0 * H + h;
+    const int sums_wanted = a.all ? blocks : blocks - 1;     // the last segment's own sum: only its state's gradient needs it
+#pragma unroll 4
+    for (int b = 0; b < sums_wanted; ++b) {
+        const f32x4 add = load(p + b * step);
+        *reinterpret_cast<f32x4 *>(p + b * step) = cur;
+        cur = cur * g[(size_t)b * H] + add;
+    }
+    if (!a.all) {
+        *reinterpret_cast<f32x4 *>(p + (blocks - 1) * step) = cur;
+        return;
+    }
+    f32x4 after = cur;                                       // the state behind segment b
+    cur = a.dS_out ? load(a.dS_out + own) : zero;
+    float *d = a.grads + ((size_t)id0 * H + h) * DD + e;
+    float *dots = a.dots + (((size_t)id0 * H + h) * gridDim.y + blockIdx.y);
+    for (int b = blocks - 1; b >= 0; --b) {
+        const f32x4 add = load(d + b * step), before = load(p + b * step);
+        *reinterpret_cast<f32x4 *>(d + b * step) = cur;
+        float x = cur.x * after.x + cur.y * after.y + cur.z * after.z + cur.w * after.w;
+        x = warp_sum(x);
+        if ((t & 63) == 0) sums[t >> 6] = x;
+        __syncthreads();
+        if (t == 0) dots[(size_t)b * H * gridDim.y] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        __syncthreads();
+        after = before;
+        cur = cur * g[(size_t)b * H] + add;
+    }
+    if (a.dS0) *reinterpret_cast<f32x4 *>(a.dS0 + own) = cur;
+}
+
+// ---- the outputs of a segment ---------------------------------------------------
+template <typename TO> __device__ __forceinline__ void store4(TO *p, f32x4 x);
+template <> __device__ __forceinline__ void store4<float>(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
+template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
+    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(x, bf16x4);
+}
+template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
+template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
+    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
+}
+
+// F(x, y, z): queries x and keys y of DA channels, values z of DC. T: the tensors' type, in NI
+// bf16 parts; TO the outputs'; NX parts of states and scores; chunks of 32 NC tokens; DOT: the
+// sum over channels of each output row (its own token's share left out) times a row of `with`.
+template <typename T, typename TO, int DA, int DC, int NI, int NX, int NC, bool DOT>
+__global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate gate, OutputJobs jobs, int H, int group) {
+    constexpr int NT = DC * 2, NW = DC / 32, C = 32 * NC, ND = DA / 32, TILES = NC * (NC + 1) / 2;
+    __shared__ bf16_t X[NI * C * DA], Y[NI * C * DA], Z[NI * C * DC];
+    __shared__ bf16x8 P[TILES][2][NX][64];
+    __shared__ float2 A[kMaxSegment];
+    __shared__ double waves[NW];
+    __shared__ float own[DOT ? C : 1], dots[DOT ? NW : 1][DOT ? C : 1], past[DOT ? NW : 1];
+    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5,
+              col = lane & 31;
+    Segment s;
+    if (!find_segment(segs, id, s)) return;
+    const OutputJob &job = jobs.job[blockIdx.y];
+    const int hs = h / group, HS = H / group;
+    TO *out = static_cast<TO *>(job.out) + (job.out_shared ? hs : h) * DC;
+    const size_t os = (size_t)(job.out_shared ? HS : H) * DC;
+    if (job.zero_rows) {
+        // rows of no sequence lie before the first one and behind the last one
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        if (s.n == 0 && s.b == 0)
+            for (size_t u = t; u < (size_t)s.begin * (DC / 4); u += NT) store4(out + u / (DC / 4) * os + u % (DC / 4) * 4, zero);
+        if (s.n == segs.N - 1 && s.b == s.blocks - 1)
+            for (size_t u = t; u < (size_t)(segs.T_total - s.end) * (DC / 4); u += NT)
+                store4(out + (s.end + u / (DC / 4)) * os + u % (DC / 4) * 4, zero);
+    }
+    // rows lo .. hi - 1; backwards the empty rows come first, so that chunks have the same borders both ways
+    const int start = s.begin + s.b * segs.L, len = min(segs.L, s.end - start), step = job.back ? -1 : 1;
+    const int hi = job.back ? (len + C - 1) / C * C : len, lo = hi - len;
+    const long long first = job.back ? start + hi - 1 : start;
+    segment_decays<NT>(gate, h, H, first, step, lo, hi, A, waves, t);
+
+    const T *x = static_cast<const T *>(job.x) + (job.x_shared ? hs : h) * DA;
+    const T *y = static_cast<const T *>(job.y) + (job.y_shared ? hs : h) * DA;
+    const T *z = static_cast<const T *>(job.z) + (job.z_shared ? hs : h) * DC;
+    const size_t xs = (size_t)(job.x_shared ? HS : H) * DA, ys = (size_t)(job.y_shared ? HS : H) * DA,
+                 zs = (size_t)(job.z_shared ? HS : H) * DC;
+    Rows<T, DA, C, NT, NI> rx, ry;
+    Rows<T, DC, C, NT, NI> rz;
+    rx.load(x, xs, first, step, 0, lo, hi, t);
+    ry.load(y, ys, first, step, 0, lo, hi, t);
+    rz.load(z, zs, first, step, 0, lo, hi, t);
+
+    // the state before the segment, transposed: column = value channel, rows = key channels
+    f32x16 S[ND];
+    const size_t cell = ((size_t)(job.border ? id : s.n) * H + h) * DA * DC;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            const int r = 32 * d + 8 * i + 4 * half, c = 32 * w + col;
+            if (job.S) {
+                if (job.key_rows) {                        // as it lies: a row per key channel
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = job.S[cell + (size_t)(r + e) * DC + c];
+                } else {
+                    v = *reinterpret_cast<const f32x4 *>(job.S + cell + (size_t)c * DA + r);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[d][4 * i + e] = v[e];
+        }
+    const bool last = job.back ? s.b == 0 : s.b == s.blocks - 1;
+    const bool keep = last && job.S_out;
+
+    for (int c0 = 0; c0 < hi; c0 += C) {
+        __syncthreads();
+        rx.store(X, t);
+        ry.store(Y, t);
+        rz.store(Z, t);
+        __syncthreads();
+        if (c0 + C < hi) {
+            rx.load(x, xs, first, step, c0 + C, lo, hi, t);
+            ry.load(y, ys, first, step, c0 + C, lo, hi, t);
+            rz.load(z, zs, first, step, c0 + C, lo, hi, t);
+        }
+        const float2 base = c0 ? A[c0 - 1] : float2{0.f, 0.f};
+        const float2 end = A[min(c0 + C, hi) - 1];
+
+        // scores, transposed (rows = key tokens s, column = query token i), a tile or two of 32 x 32 a wavefront
+        for (int tile = w; tile < TILES; tile += NW) {
+            const int ti = NC == 1 ? 0 : (tile + 1) / 2, ts = tile / 2;     // (ts, ti): 00, 01, 11
+            f32x16 acc = {};
+#pragma unroll
+            for (int m = 0; m < DA / 16; ++m) {
+                bf16x8 ky[NI], qx[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    ky[i] = row_frag<DA>(Y + i * C * DA, 32 * ts + col, m, half);
+                    qx[i] = row_frag<DA>(X + i * C * DA, 32 * ti + col, m, half);
+                }
+                acc = product<NI, NI>(ky, qx, acc);
+            }
+            const int i = 32 * ti + col;
+            const float2 ai = A[min(c0 + i, hi - 1)];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int sr = 32 * ts + 8 * (r >> 2) + 4 * half + (r & 3);
+                const float dec = decay(ai, A[min(c0 + sr, hi - 1)]);
+                if (DOT && sr == i) own[i] = acc[r];
+                acc[r] = (DOT ? sr < i : sr <= i) ? acc[r] * dec : 0.f;
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                f32x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = acc[8 * m + e];
+                bf16x8 p[NX];
+                cut<NX>(v, p);
+#pragma unroll
+                for (int j = 0; j < NX; ++j) P[tile][m][j][lane] = p[j];
+            }
+        }
+        // e^{a_i} S x_i
+        f32x16 O[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) O[i] = f32x16{};
+#pragma unroll
+        for (int m = 0; m < DA / 16; ++m) {
+            f32x8 v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = S[m >> 1][8 * (m & 1) + e];
+            bf16x8 sp[NX];
+            cut<NX>(v, sp);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                bf16x8 qx[NI];
+#pragma unroll
+                for (int j = 0; j < NI; ++j) qx[j] = row_frag<DA>(X + j * C * DA, 32 * i + col, m, half);
+                O[i] = product<NX, NI>(sp, qx, O[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) O[i] *= decay(A[min(c0 + 32 * i + col, hi - 1)], base);
+        if constexpr (DOT) {
+            // what the chunk's rows have from the state, against `with`
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int row = c0 + 32 * i + col;
+                if (row < lo || row >= hi) continue;
+                const T *with = static_cast<const T *>(job.with) + hs * DC + 32 * w + 4 * half +
+                                (size_t)(first + (long long)row * step) * ((size_t)HS * DC);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 y4 = load4(with + 8 * j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum += O[i][4 * j + e] * y4[e];
+                }
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) past[w] = sum;
+        }
+        __syncthreads();
+        // the values: scores times them, and their share of the state
+        const float over = decay(end, base);
+        const bool carry = c0 + C < hi || keep;
+        if (carry) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[d] *= over;
+        }
+#pragma unroll
+        for (int m = 0; m < C / 16; ++m) {
+            bf16x8 zv[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane);
+#pragma unroll
+            for (int i = m / 2; i < NC; ++i) {
+                bf16x8 p[NX];
+#pragma unroll
+                for (int j = 0; j < NX; ++j) p[j] = P[m / 2 + i][m & 1][j][lane];
+                O[i] = product<NI, NX>(zv, p, O[i]);
+            }
+            if (carry) {
+                f32x8 zw = {};
+#pragma unroll
+                for (int i = NI - 1; i >= 0; --i) zw += __builtin_convertvector(zv[i], f32x8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    zw[e] *= decay(end, A[min(c0 + 16 * m + 8 * (e >> 2) + 4 * half + (e & 3), hi - 1)]);
+                bf16x8 zp[3];
+                cut<3>(zw, zp);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    bf16x8 ky[NI];
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) ky[i] = col_frag<DA>(Y + i * C * DA, d, m, lane);
+                    S[d] = product<NI, 3>(ky, zp, S[d]);
+                }
+            }
+        }
+        // out: a lane has token i's channels in groups of four
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int row = c0 + 32 * i + col;
+            const bool live = row >= lo && row < hi;
+            const size_t token = (size_t)(first + (long long)row * step);
+            if constexpr (DOT) {
+                const T *with = static_cast<const T *>(job.with) + hs * DC + 32 * w + 4 * half;
+                float dot = 0.f;
+                const float mine = own[32 * i + col];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f32x4 y4 = {0.f, 0.f, 0.f, 0.f};
+                    if (live) y4 = load4(with + token * ((size_t)HS * DC) + 8 * j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dot += O[i][4 * j + e] * y4[e];
+                    f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int p = NI - 1; p >= 0; --p)
+                        z4 += __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(
+                                  Z + p * C * DC + at<DC>(32 * i + col, 8 * w + 2 * j + half)), f32x4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[i][4 * j + e] += mine * z4[e];
+                }
+                dot += __shfl_xor(dot, 32, 64);
+                if (half == 0) dots[w][32 * i + col] = dot;
+            }
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    store4(out + token * os + 32 * w + 8 * j + 4 * half,
+                           f32x4{O[i][4 * j], O[i][4 * j + 1], O[i][4 * j + 2], O[i][4 * j + 3]});
+            }
+        }
+        if constexpr (DOT) {
+            __syncthreads();
+            if (t < C && c0 + t >= lo && c0 + t < hi) {
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) d += dots[i][t];
+                job.dot[(size_t)h * segs.T_total + (size_t)(first + (long long)(c0 + t) * step)] = d;
+            }
+            if (t == 0) {
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) d += past[i];
+                const int chunk = job.back ? hi / C - 1 - c0 / C : c0 / C;
+                job.past[((size_t)id * H + h) * (segs.L / C) + chunk] = d;
+            }
+        }
+    }
+    if (keep) {
+        // backwards, the decay of the segment's first token is still to be applied
+        const float more = job.back && len > 0 ? expf(gate_at(gate, start, h, H)) : 1.f;
+        float *so = job.S_out + ((size_t)s.n * H + h) * DA * DC;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 32 * d + 8 * i + 4 * half, c = 32 * w + col;
+                *reinterpret_cast<f32x4 *>(so + (size_t)c * DA + r) =
+                    f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]} * more;
+            }
+    }
+}
+
+// ---- the decays' gradients --------------------------------------------------------
+// What passes the decay of token t: with G(p) = <gradient of the state behind token p, that state>,
+//     dg_t = G(t - 1) = G(p) + sum_{t <= i <= p} (q_i . dq_i - k_i . dk_i)
+// (a token's own share left out of both). The terms of a long sum cancel, and their rounding would
+// not, so it never runs further than a chunk: G at the chunks' borders follows from G at the segment's
+// end by what the chunks' tokens have from the state (read, q . dq) and from its gradient (past,
+// k . dk) alone, and inside a chunk the sums from both of its borders are weighted by their
+// nearness. C tokens a chunk; a wavefront a (segment, head), sums in 64 bits.
+__global__ __launch_bounds__(64) void decay_grad_kernel(Segments segs, Gate gate, const float *__restrict__ rows,
+                                                        const float *__restrict__ cols, const float *__restrict__ read,
+                                                        const float *__restrict__ past, const float *__restrict__ dots,
+                                                        int parts, int C, float *__restrict__ dg, double *__restrict__ sums,
+                                                        int H, int zero_rows) {
+    const int id = blockIdx.x / H, h = blockIdx.x % H, lane = threadIdx.x;
+    Segment s;
+    if (!find_segment(segs, id, s)) {
+        if (gate.fixed && lane == 0) sums[(size_t)id * H + h] = 0.;
+        return;
+    }
+    if (zero_rows && !gate.fixed) {
+        if (s.n == 0 && s.b == 0)
+            for (int i = lane; i < s.begin; i += 64) dg[(size_t)i * H + h] = 0.f;
+        if (s.n == segs.N - 1 && s.b == s.blocks - 1)
+            for (int i = s.end + lane; i < segs.T_total; i += 64) dg[(size_t)i * H + h] = 0.f;
+    }
+    const int start = s.begin + s.b * segs.L, len = min(segs.L, s.end - start);
+    const size_t at = (size_t)h * segs.T_total + start, cell = (size_t)id * H + h;
+    double G = 0., sum = 0.;
+    for (int i = 0; i < parts; ++i) G += dots[cell * parts + i];
+    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {       // C <= 64 tokens, one a lane
+        const int i = c * C + lane, n = min(C, len - c * C);
+        const double before = G + (double)read[cell * (segs.L / C) + c] - (double)past[cell * (segs.L / C) + c];
+        const double x = lane < n ? (double)rows[at + i] - (double)cols[at + i] : 0.;
+        const double upto = wave_prefix(x, lane), all = __shfl(upto, 63, 64);
+        const double near = (double)lane / n;
+        const double d = near * (G + (all - upto) + x) + (1. - near) * (before - (upto - x));
+        if (lane < n) {
+            // at -104 the decay is zero, and its gradient too
+            const bool none = gate.g[gate.fixed ? h : (size_t)(start + i) * H + h] <= kMinLog;
+            if (gate.fixed) sum += none ? 0. : d; else dg[(size_t)(start + i) * H + h] = none ? 0.f : (float)d;
+        }
+        G = before;
+    }
+    if (gate.fixed) {
+        sum = wave_prefix(sum, lane);
+        if (lane == 63) sums[(size_t)id * H + h] = sum;
+    }
+}
+
+// A fixed decay's gradient: the sum over all segments, in a fixed order.
+__global__ __launch_bounds__(64) void fixed_grad_kernel(const double *__restrict__ sums, float *__restrict__ dg, int ids, int H) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double x = 0.;
+    for (int i = lane; i < ids; i += 64) x += sums[(size_t)i * H + h];
+    x = wave_prefix(x, lane);
+    if (lane == 63) dg[h] = (float)x;
+}
+
+// The gradient of a shared query or key head: the sum over its group's heads.
+template <typename TO>
+__global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *__restrict__ part, TO *__restrict__ out, int H,
+                                                    int group, int D, int zero_rows) {
+    const size_t u = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const int HS = H / group, q = D / 4;
+    const size_t token = u / ((size_t)HS * q);
+    if (token >= (size_t)segs.T_total) return;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    bool live = true;
+    if (segs.cu) {
+        int b0, b1, e0, e1;
+        sequence_bounds(segs, 0, b0, e0);
+        sequence_bounds(segs, segs.N - 1, b1, e1);
+        live = token >= (size_t)b0 && token < (size_t)e1;
+        if (!live && !zero_rows) return;
+    }
+    const int hs = (int)(u / q % HS), c = (int)(u % q) * 4;
+    if (live)
+        for (int i = 0; i < group; ++i) sum += *reinterpret_cast<const f32x4 *>(part + (token * H + hs * group + i) * D + c);
+    store4(out + (token * HS + hs) * D + c, sum);
+}
+
+// ---- host -----------------------------------------------------------------------
+// Tokens a segment: enough segments for a few workgroups on every CU, while the states between
+// them (8 D^2 bytes a segment and pass, 0.5 KB a token at 256) stay below the tokens' own bytes.
+int segment_length(long long T_total, int H) {
+    long long L = T_total * H / 1024;
+    int p = 128;
+    while (p < kMaxSegment && 2 * p <= L) p *= 2;
+    return p;
+}
+long long id_count(long long T_total, int N, int L) { return T_total / L + N; }
+size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// The workspace of a call, piece after piece.
+struct Carver {
+    char *p;
+    size_t used = 0;
+    template <typename T> T *take(size_t n) {
+        T *r = reinterpret_cast<T *>(p + used);
+        used += round_up(n * sizeof(T));
+        return r;
+    }
+};
+struct ForwardSpace { float *states, *whole; };
+struct BackwardSpace {
+    float *states, *grads, *whole, *dots, *rows, *cols, *read, *past, *dq, *dk;
+    double *sums;
+};
+ForwardSpace carve_forward(Carver &c, int N, long long T_total, int H, int Dk, int Dv, int L) {
+    ForwardSpace s{};
+    if (T_total <= L) return s;                             // every sequence is one segment
+    const size_t cells = (size_t)id_count(T_total, N, L) * H;
+    s.states = c.take<float>(cells * Dk * Dv);
+    s.whole = c.take<float>(cells);
+    return s;
+}
+BackwardSpace carve_backward(Carver &c, int N, long long T_total, int H, int group, int Dk, int Dv, int L) {
+    BackwardSpace s{};
+    const size_t cells = (size_t)id_count(T_total, N, L) * H;
+    s.states = c.take<float>(cells * Dk * Dv);
+    s.grads = c.take<float>(cells * Dk * Dv);
+    s.whole = c.take<float>(cells);
+    s.dots = c.take<float>(cells * (Dk * Dv / 1024));
+    s.sums = c.take<double>(cells);
+    s.rows = c.take<float>((size_t)T_total * H);
+    s.cols = c.take<float>((size_t)T_total * H);
+    s.read = c.take<float>(cells * (L / 32));              // chunks of 32 tokens at least
+    s.past = c.take<float>(cells * (L / 32));
+    if (group > 1) {
+        s.dq = c.take<float>((size_t)T_total * H * Dk);
+        s.dk = c.take<float>((size_t)T_total * H * Dk);
+    }
+    return s;
+}
+
+template <typename T> struct Parts { static constexpr int N = 1, C = 64; };
+template <> struct Parts<float> { static constexpr int N = 3, C = 32; };
+
+template <typename T, int DA, int DC>
+hipError_t run_states(const Segments &segs, const Gate &gate, const StateJobs &jobs, int n, float *whole, int H, int group,
+                      hipStream_t stream) {
+    const unsigned ids = (unsigned)id_count(segs.T_total, segs.N, segs.L);
+    hipLaunchKernelGGL((state_kernel<T, DA, DC, Parts<T>::N, Parts<T>::C>), dim3(ids * H, n), dim3(DC * 2), 0, stream, segs,
+                       gate, jobs, whole, H, group);
+    return hipGetLastError();
+}
+hipError_t run_borders(const Segments &segs, const BorderArgs &a, int H, int DD, hipStream_t stream) {
+    hipLaunchKernelGGL(border_kernel, dim3((unsigned)(segs.N * H), DD / 1024), dim3(256), 0, stream, segs, a, H, DD);
+    return hipGetLastError();
+}
+template <typename T, typename TO, int DA, int DC, int NX, bool DOT>
+hipError_t run_outputs(const Segments &segs, const Gate &gate, const OutputJobs &jobs, int n, int H, int group,
+                       hipStream_t stream) {
+    const unsigned ids = (unsigned)id_count(segs.T_total, segs.N, segs.L);
+    hipLaunchKernelGGL((output_kernel<T, TO, DA, DC, Parts<T>::N, NX, Parts<T>::C / 32, DOT>), dim3(ids * H, n), dim3(DC * 2),
+                       0, stream, segs, gate, jobs, H, group);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV> hipError_t prefill(const LinPrefillArgs &a) {
+    const long long T_total = (long long)a.B * a.T;
+    const int L = segment_length(T_total, a.H), group = a.H / a.Hk;
+    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L};
+    const Gate gate{a.g, a.fixed};
+    Carver c{static_cast<char *>(a.ws)};
+    const ForwardSpace ws = carve_forward(c, a.N, T_total, a.H, DK, DV, L);
+    OutputJobs out{};
+    OutputJob &o = out.job[0];
+    o.x = a.q; o.y = a.k; o.z = a.v; o.out = a.out; o.S = a.S0; o.S_out = a.S_out;
+    o.x_shared = o.y_shared = true;
+    o.zero_rows = a.zero_rows;
+    if (ws.states) {
+        StateJobs st{};
+        st.job[0] = StateJob{a.k, a.v, ws.states, true, false, true, true};
+        hipError_t e = run_states<T, DK, DV>(segs, gate, st, 1, ws.whole, a.H, group, a.stream);
+        if (e != hipSuccess) return e;
+        BorderArgs b{};
+        b.S0 = a.S0; b.states = ws.states; b.whole = ws.whole;
+        e = run_borders(segs, b, a.H, DK * DV, a.stream);
+        if (e != hipSuccess) return e;
+        o.S = ws.states;
+        o.border = true;
+    }
+    if constexpr (sizeof(T) == 2)
+        if (a.out_dt == Dt::BF16) return run_outputs<T, bf16_t, DK, DV, 2, false>(segs, gate, out, 1, a.H, group, a.stream);
+    return run_outputs<T, float, DK, DV, 3, false>(segs, gate, out, 1, a.H, group, a.stream);
+}
+
+template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs &a) {
+    const long long T_total = (long long)a.B * a.T;
+    const int L = segment_length(T_total, a.H), group = a.H / a.Hk, ids = (int)id_count(T_total, a.N, L);
+    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L};
+    const Gate gate{a.g, a.fixed};
+    Carver c{static_cast<char *>(a.ws)};
+    const BackwardSpace ws = carve_backward(c, a.N, T_total, a.H, group, DK, DV, L);
+    StateJobs st{};
+    st.job[0] = StateJob{a.k, a.v, ws.states, true, false, true, false};
+    st.job[1] = StateJob{a.q, a.dout, ws.grads, true, false, false, false};
+    hipError_t e = run_states<T, DK, DV>(segs, gate, st, 2, ws.whole, a.H, group, a.stream);
+    if (e != hipSuccess) return e;
+    BorderArgs b{};
+    b.S0 = a.S0; b.dS_out = a.dS_out; b.states = ws.states; b.grads = ws.grads; b.dS0 = a.dS0; b.dots = ws.dots;
+    b.whole = ws.whole; b.all = true;
+    e = run_borders(segs, b, a.H, DK * DV, a.stream);
+    if (e != hipSuccess) return e;
+
+    // dq = F(dout, v, k) from the states, dk = F(v, dout, q) and dv = F(k, q, dout) from their gradients
+    OutputJobs qk{}, vj{};
+    OutputJob &q = qk.job[0], &k = qk.job[1], &v = vj.job[0];
+    q.x = a.dout; q.y = a.v; q.z = a.k; q.with = a.q; q.dot = ws.rows; q.past = ws.read; q.S = ws.states;
+    k.x = a.v; k.y = a.dout; k.z = a.q; k.with = a.k; k.dot = ws.cols; k.past = ws.past; k.S = ws.grads;
+    v.x = a.k; v.y = a.q; v.z = a.dout; v.S = ws.grads; v.out = a.dv;
+    q.z_shared = k.z_shared = v.x_shared = v.y_shared = true;
+    q.border = k.border = v.border = q.key_rows = k.key_rows = k.back = v.back = true;
+    v.zero_rows = a.zero_rows & 4;
+    if (group == 1) {
+        q.out = a.dq; k.out = a.dk;
+        q.out_shared = k.out_shared = true;
+        q.zero_rows = a.zero_rows & 1;
+        k.zero_rows = a.zero_rows & 2;
+    } else {
+        q.out = ws.dq; k.out = ws.dk;
+    }
+    if (group == 1 && sizeof(T) == 2) {
+        if constexpr (sizeof(T) == 2)
+            e = a.g ? run_outputs<T, bf16_t, DV, DK, 3, true>(segs, gate, qk, 2, a.H, group, a.stream)
+                    : run_outputs<T, bf16_t, DV, DK, 2, false>(segs, gate, qk, 2, a.H, group, a.stream);
+    } else {
+        e = a.g ? run_outputs<T, float, DV, DK, 3, true>(segs, gate, qk, 2, a.H, group, a.stream)
+                : run_outputs<T, float, DV, DK, 3, false>(segs, gate, qk, 2, a.H, group, a.stream);
+    }
+    if (e != hipSuccess) return e;
+    if constexpr (sizeof(T) == 2) e = run_outputs<T, bf16_t, DK, DV, 2, false>(segs, gate, vj, 1, a.H, group, a.stream);
+    else e = run_outputs<T, float, DK, DV, 3, false>(segs, gate, vj, 1, a.H, group, a.stream);
+    if (e != hipSuccess) return e;
+    if (group > 1) {
+        const unsigned blocks = (unsigned)(((size_t)T_total * a.Hk * (DK / 4) + 255) / 256);
+        const float *part[2] = {ws.dq, ws.dk};
+        void *to[2] = {a.dq, a.dk};
+        for (int i = 0; i < 2; ++i) {
+            hipLaunchKernelGGL((share_kernel<T>), dim3(blocks), dim3(256), 0, a.stream, segs, part[i], static_cast<T *>(to[i]),
+                               a.H, group, DK, a.zero_rows & (1 << i));
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    if (a.g) {
+        hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(ids * a.H)), dim3(64), 0, a.stream, segs, gate, ws.rows, ws.cols,
+                           ws.read, ws.past, ws.dots, DK * DV / 1024, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (a.fixed) {
+            hipLaunchKernelGGL(fixed_grad_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, ws.sums, a.dg, ids, a.H);
+            e = hipGetLastError();
+        }
+    }
+    return e;
+}
+
+// No tokens at all: the states pass through.
+__global__ __launch_bounds__(256) void pass_kernel(const float *from, float *to, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) to[i] = from ? from[i] : 0.f;
+}
+hipError_t pass(const float *from, float *to, size_t n, hipStream_t stream) {
+    if (!to || from == to) return hipSuccess;
+    hipLaunchKernelGGL(pass_kernel, dim3((unsigned)(n / 4096 + 1 < 4096 ? n / 4096 + 1 : 4096)), dim3(256), 0, stream, from, to, n);
+    return hipGetLastError();
+}
+
+template <typename T, typename A, typename F> hipError_t by_width(const A &a, F) {
+    if (a.Dk == 64) return a.Dv == 64 ? F::template run<T, 64, 64>(a) : F::template run<T, 64, 128>(a);
+    return a.Dv == 64 ? F::template run<T, 128, 64>(a) : F::template run<T, 128, 128>(a);
+}
+struct Prefill { template <typename T, int DK, int DV> static hipError_t run(const LinPrefillArgs &a) { return prefill<T, DK, DV>(a); } };
+struct Backward { template <typename T, int DK, int DV> static hipError_t run(const LinBackwardArgs &a) { return backward<T, DK, DV>(a); } };
+
+}  // namespace
+
+size_t lin_prefill_workspace(int N, long long T_total, int H, int Dk, int Dv) {
+    Carver c{nullptr};
+    carve_forward(c, N, T_total, H, Dk, Dv, segment_length(T_total, H));
+    return c.used;
+}
+size_t lin_backward_workspace(int N, long long T_total, int H, int Hk, int Dk, int Dv) {
+    if (T_total == 0) return 0;
+    Carver c{nullptr};
+    carve_backward(c, N, T_total, H, H / Hk, Dk, Dv, segment_length(T_total, H));
+    return c.used;
+}
+bool lin_chunk_fits(int N, long long T_total, int H) {
+    // workgroups of a launch times their threads stay below 2^32
+    return id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
+}
+hipError_t launch_lin_prefill(const LinPrefillArgs &a) {
+    if ((long long)a.B * a.T == 0) return pass(a.S0, a.S_out, (size_t)a.N * a.H * a.Dk * a.Dv, a.stream);
+    return a.io == Dt::F32 ? by_width<float>(a, Prefill{}) : by_width<bf16_t>(a, Prefill{});
+}
+hipError_t launch_lin_backward(const LinBackwardArgs &a) {
+    if ((long long)a.B * a.T == 0) {
+        const hipError_t e = pass(a.dS_out, a.dS0, (size_t)a.N * a.H * a.Dk * a.Dv, a.stream);
+        return e != hipSuccess || !a.dg || !a.fixed ? e : pass(nullptr, a.dg, (size_t)a.H, a.stream);
+    }
+    return a.io == Dt::F32 ? by_width<float>(a, Backward{}) : by_width<bf16_t>(a, Backward{});
+}
+
+}  // namespace kda

@@ -1,0 +1,133 @@
+// lin_recurrent.hip -- linear attention with a decay per head, token by token: one
+// token per sequence in place, or a few tokens of each over the slots of a pool.
+//
+//     S = e^g S' + v k^T,   o = S q = e^g (S' q) + (k . q) v
+//
+// The rows of S (value channels) do not meet, so a workgroup owns 64 rows of one (sequence,
+// head) for all of its tokens and holds them in registers: a state is read once, and written
+// once for each token that keeps it, which is what bounds the kernel (memory, 4 Dk Dv bytes
+// each). Dk / 4 consecutive lanes own a row, four key channels each; the read-out is taken
+// from the state before the update, so a row needs one sum over its lanes, besides k . q, that
+// all rows share. The next token's vectors are loaded while the current one is computed.
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+template <int W>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) x += __shfl_xor(x, o, W);
+    return x;
+}
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+
+template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
+template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xffff0000u)};
+}
+
+constexpr int R = 4, ROWS = 64;      // rows of a thread and of a workgroup
+
+// One token's vectors as a lane holds them.
+struct Token {
+    f32x4 q, k;
+    float v[R], g;
+    int slot;
+};
+
+template <int DK, int DV, typename T, typename TO>
+__global__ __launch_bounds__(DK * 4) void lin_recurrent_kernel(const T *__restrict__ q, const T *__restrict__ k,
+                                                               const T *__restrict__ v, const float *__restrict__ g,
+                                                               float *__restrict__ S, TO *__restrict__ out,
+                                                               const int32_t *__restrict__ cu,
+                                                               const int32_t *__restrict__ slot_in,
+                                                               const int32_t *__restrict__ slot_out, int N, int tokens, int H,
+                                                               int group, int slots, bool fixed, bool zero_rows) {
+    constexpr int LPR = DK / 4, PASS = ROWS / R, SPLIT = DV / ROWS, NT = DK * 4;
+    static_assert(NT / LPR == PASS, "rows of a workgroup");
+    const int chain = blockIdx.x / SPLIT, n = chain / H, h = chain % H, hs = h / group, HS = H / group;
+    const int t = threadIdx.x, kq = t % LPR, row0 = (blockIdx.x % SPLIT) * ROWS + t / LPR;
+    // offsets outside the packed rows are cut to them
+    const int begin = cu ? min(max(cu[n], 0), tokens) : n, end = cu ? min(max(cu[n + 1], begin), tokens) : n + 1;
+    if (zero_rows) {                                     // uniform
+        // rows of no sequence lie before the first one and behind the last one
+        const int col = (blockIdx.x % SPLIT) * ROWS + t % ROWS;
+        auto clear = [&](int from, int to) {
+            for (int tok = from + t / ROWS; tok < to; tok += NT / ROWS) out[((size_t)tok * H + h) * DV + col] = TO(0);
+        };
+        if (n == 0) clear(0, begin);
+        if (n == N - 1) clear(end, tokens);
+    }
+    if (begin == end) return;
+
+    const size_t DD = (size_t)DK * DV;
+    f32x4 s[R];
+    const int from = cu ? (slot_in ? slot_in[n] : -1) : n;
+    const bool live = from >= 0 && from < slots;
+    const f32x4 *Sp = reinterpret_cast<const f32x4 *>(S + ((size_t)(live ? from : 0) * H + h) * DD);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        s[i] = live ? __builtin_nontemporal_load(&Sp[(row0 + PASS * i) * LPR + kq]) : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto load = [&](int tok) {
+        Token x;
+        const size_t th = (size_t)tok * H + h, ts = (size_t)tok * HS + hs;
+        x.q = load4(q + ts * DK + 4 * kq);
+        x.k = load4(k + ts * DK + 4 * kq);
+        x.g = g ? (fixed ? g[h] : g[th]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) x.v[i] = io<T>::load(v, th * DV + row0 + PASS * i);
+        x.slot = cu ? (slot_out ? slot_out[tok] : -1) : n;
+        return x;
+    };
+
+    Token next = load(begin);
+    for (int tok = begin; tok < end; ++tok) {
+        const Token x = next;
+        if (tok + 1 < end) next = load(tok + 1);
+        const float a = expf(x.g), qk = group_sum<LPR>(dot4(x.q, x.k));
+        const bool keep = x.slot >= 0 && x.slot < slots;
+        f32x4 *Kp = reinterpret_cast<f32x4 *>(S + ((size_t)(keep ? x.slot : 0) * H + h) * DD);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const f32x4 d = s[i] * a;
+            const float o = group_sum<LPR>(dot4(d, x.q)) + qk * x.v[i];
+            s[i] = d + x.k * x.v[i];
+            const int row = row0 + PASS * i;
+            if (keep) __builtin_nontemporal_store(s[i], &Kp[row * LPR + kq]);
+            if (kq == 0) io<TO>::store(out, ((size_t)tok * H + h) * DV + row, o);
+        }
+    }
+}
+
+template <int DK, int DV, typename T, typename TO> hipError_t launch_t(const LinRecurrentArgs &a) {
+    hipLaunchKernelGGL((lin_recurrent_kernel<DK, DV, T, TO>), dim3((unsigned)(a.N * a.H * (DV / ROWS))), dim3(DK * 4), 0,
+                       a.stream, static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v), a.g,
+                       a.S, static_cast<TO *>(a.out), a.cu, a.slot_in, a.slot_out, a.N, a.T, a.H, a.H / a.Hk, a.slots,
+                       a.fixed, a.zero_rows);
+    return hipGetLastError();
+}
+template <int DK, int DV, typename T> hipError_t launch_o(const LinRecurrentArgs &a) {
+    return a.out_dt == Dt::F32 ? launch_t<DK, DV, T, float>(a) : launch_t<DK, DV, T, bf16_t>(a);
+}
+template <int DK, int DV> hipError_t launch_i(const LinRecurrentArgs &a) {
+    return a.io == Dt::F32 ? launch_o<DK, DV, float>(a) : launch_o<DK, DV, bf16_t>(a);
+}
+
+}  // namespace
+
+bool lin_recurrent_fits(int N, int H, int Dk, int Dv) {
+    return (unsigned long long)N * H * (Dk * Dv / 16) < (1ull << 32);    // sixteen values of a state per thread
+}
+
+hipError_t launch_lin_recurrent(const LinRecurrentArgs &a) {
+    if (a.Dk == 64) return a.Dv == 64 ? launch_i<64, 64>(a) : launch_i<64, 128>(a);
+    return a.Dv == 64 ? launch_i<128, 64>(a) : launch_i<128, 128>(a);
+}
+
+}  // namespace kda

@@ -39,7 +39,7 @@ class Options(ctypes.Structure):
                 ("snapshots", ctypes.c_void_p)]
 
 
-GATE_CHANNEL, GATE_HEAD = 0, 1
+GATE_CHANNEL, GATE_HEAD, GATE_FIXED = 0, 1, 2
 
 
 def load_library() -> ctypes.CDLL:
@@ -102,6 +102,34 @@ def load_library() -> ctypes.CDLL:
     lib.kda_layer_norm_backward_workspace_size.argtypes = [i] * 2
     lib.kda_layer_norm_backward.restype = i
     lib.kda_layer_norm_backward.argtypes = [vp] * 8 + [i] * 5 + [vp, sz, vp]
+    lib.lin_prefill_workspace_size.restype = sz
+    lib.lin_prefill_workspace_size.argtypes = [i] * 5
+    lib.lin_prefill.restype = i
+    lib.lin_prefill.argtypes = [vp] * 8 + [i] * 11 + [vp, sz, vp]
+    lib.lin_prefill_backward_workspace_size.restype = sz
+    lib.lin_prefill_backward_workspace_size.argtypes = [i] * 6
+    lib.lin_prefill_backward.restype = i
+    lib.lin_prefill_backward.argtypes = [vp] * 13 + [i] * 10 + [vp, sz, vp]
+    lib.lin_decode.restype = i
+    lib.lin_decode.argtypes = [vp] * 6 + [i] * 8 + [vp]
+    lib.lin_recurrent.restype = i
+    lib.lin_recurrent.argtypes = [vp] * 9 + [i] * 11 + [vp]
+    lib.kda_tree.restype = i
+    lib.kda_tree.argtypes = [vp] * 9 + [i] * 10 + [op, vp]
+    lib.kda_tree_accept.restype = i
+    lib.kda_tree_accept.argtypes = [vp] * 9 + [i] * 8 + [op, vp]
+    lib.lin_tree.restype = i
+    lib.lin_tree.argtypes = [vp] * 8 + [i] * 11 + [vp]
+    lib.lin_tree_accept.restype = i
+    lib.lin_tree_accept.argtypes = [vp] * 8 + [i] * 9 + [vp]
+    lib.kda_slots_copy.restype = i
+    lib.kda_slots_copy.argtypes = [vp] * 4 + [i] * 4 + [sz, vp]
+    lib.kda_slots_share.restype = lib.kda_slots_release.restype = lib.kda_slots_acquire.restype = i
+    lib.kda_slots_share.argtypes = lib.kda_slots_release.argtypes = lib.kda_slots_acquire.argtypes = [vp, vp, i, i, vp]
+    lib.kda_slots_compact_workspace_size.restype = sz
+    lib.kda_slots_compact_workspace_size.argtypes = [i]
+    lib.kda_slots_compact.restype = i
+    lib.kda_slots_compact.argtypes = [vp] * 4 + [i] * 3 + [sz, vp, sz, vp]
     _lib = lib
     return lib
 

@@ -62,8 +62,10 @@ typedef enum {
 /* Layout of the decay gate g (kda_options.gate). */
 typedef enum {
     KDA_GATE_CHANNEL = 0,   /* g [..][H][Dk]: one log-decay per key channel (KDA) */
-    KDA_GATE_HEAD = 1       /* g [..][H]: one per token and head (Gated DeltaNet);
+    KDA_GATE_HEAD = 1,      /* g [..][H]: one per token and head (Gated DeltaNet);
                                g NULL: no decay (DeltaNet) */
+    KDA_GATE_FIXED = 2      /* lin_* and trees without the delta rule: g [H], one per head for
+                               every token; g NULL: no decay */
 } kda_gate;
 
 /*
@@ -483,6 +485,152 @@ size_t kda_layer_norm_backward_workspace_size(int rows, int W);
 int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, const float *rstd, const float *weight,
                             void *dx, float *dweight, float *dbias, int rows, int W, int rms, kda_dtype x_dtype,
                             kda_dtype dy_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * lin_prefill -- linear attention with a decay for each head, without the delta rule:
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = S_t q_t
+ * (the explainer's linear attention with the forget gate of its GDN paragraph), chunked over
+ * whole sequences. Query and key heads may be shared: head h uses head h / (H / Hk) of q and k.
+ *
+ *   q, k   [T_total][Hk][Dk] io_dtype      v    [T_total][H][Dv] io_dtype
+ *   g      fp32, gate KDA_GATE_HEAD: [T_total][H], KDA_GATE_FIXED: [H]; NULL = no decay;
+ *          4-byte aligned. Natural log-decay, g <= 0 intended; -104 or less (exp is 0 in
+ *          fp32; -inf) forgets everything
+ *   S0     [N][H][Dv][Dk] fp32 or NULL (zero)   S_out  the final states, or NULL; may be S0
+ *   out    [T_total][H][Dv] out_dtype
+ *   cu_seqlens, N, B, T  as for kda_prefill. Packed offsets may start behind 0 and end before
+ *          T_total; offsets outside [0, T_total] or below the one before them are cut. Offsets
+ *          that fall make sequences share tokens: those rows are undefined (no fault)
+ *   zero_rows  1: out rows of tokens in no sequence become zero; 0: they stay as they were
+ *          (else KDA_ERR_INVALID_ARG)
+ * A zero-length sequence gives S_out = S0. q, k, v, out, S0 and S_out 16-byte aligned; out must
+ * be none of the inputs.
+ *
+ * Support (else KDA_ERR_UNSUPPORTED): Dk and Dv each 64 or 128; io_dtype KDA_F32 with fp32 out, or
+ * KDA_BF16 with either; (T_total / 128 + N) * H below 2^23, T_total * H below 2^27. Hk must divide H
+ * (else KDA_ERR_INVALID_ARG).
+ * Arithmetic: states in fp32 with products of operands cut in three bf16 parts (fp32 precision),
+ * for values whose products stay between about 1e-33 and 3.3e38; an fp32 out likewise; a bf16 out is
+ * rounded from sums whose operands are cut in two (2^-17). A NaN or an infinity in a token may reach
+ * earlier outputs of its sequence (up to 63 tokens before).
+ * workspace: lin_prefill_workspace_size bytes, 256-byte aligned, contents ignored, used by
+ * nothing else until the call's work has finished; may be NULL when that is 0 (it is where all
+ * tokens together are one segment, 128 to 1024 tokens). It holds a state per segment and head.
+ */
+size_t lin_prefill_workspace_size(int N, int T_total, int H, int Dk, int Dv);
+int lin_prefill(const void *q, const void *k, const void *v, const float *g, const float *S0, void *out, float *S_out,
+                const int32_t *cu_seqlens, int N, int B, int T, int H, int Hk, int Dk, int Dv, kda_dtype io_dtype,
+                kda_dtype out_dtype, int gate, int zero_rows, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * lin_prefill_backward -- its gradient, from dout [T_total][H][Dv] io_dtype and dS_out [N][H][Dv][Dk]
+ * fp32 (NULL: zero) to those of every input; nothing of the forward call is needed.
+ *   dq, dk [T_total][Hk][Dk], dv [T_total][H][Dv] io_dtype (a shared head's is the sum over its group)
+ *   dg     fp32, g's layout (fixed: the sum over all tokens); NULL exactly when g is
+ *   dS0    [N][H][Dv][Dk] fp32, or NULL to skip it
+ *   zero_rows  KDA_ZERO_DQ .. KDA_ZERO_DG added up: the gradients whose rows of tokens in no sequence
+ *          become zero; other bits: KDA_ERR_INVALID_ARG
+ * A log-decay of -104 or less has gradient 0. A zero-length sequence gives dS0 = dS_out. fp32 precision
+ * as above, for dq, dk and dv of bf16 tensors before they are rounded. Results repeat bit for bit. No gradient may
+ * be any other buffer of the call. Support, alignment and workspace as for lin_prefill.
+ */
+size_t lin_prefill_backward_workspace_size(int N, int T_total, int H, int Hk, int Dk, int Dv);
+int lin_prefill_backward(const void *q, const void *k, const void *v, const float *g, const void *dout, const float *S0,
+                         const float *dS_out, void *dq, void *dk, void *dv, float *dg, float *dS0,
+                         const int32_t *cu_seqlens, int N, int B, int T, int H, int Hk, int Dk, int Dv,
+                         kda_dtype io_dtype, int gate, int zero_rows, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * lin_decode -- one token per sequence, S [N][H][Dv][Dk] fp32 updated in place. q, k [N][Hk][Dk],
+ * v [N][H][Dv], g [N][H] (KDA_GATE_HEAD), [H] (KDA_GATE_FIXED) or NULL, out [N][H][Dv]. fp32 arithmetic;
+ * io_dtype and out_dtype either. q, k, v, S and out 16-byte aligned; out none of the other buffers.
+ *
+ * lin_recurrent -- a few tokens per sequence over a pool of slots: cu_seqlens, slot_in, slot_out, slots
+ * and rows of no sequence exactly as for kda_recurrent_padded; g [T_total][H], [H] or NULL.
+ * Both: Dk and Dv each 64 or 128; N * H * Dk * Dv / 16 below 2^32 (else KDA_ERR_UNSUPPORTED).
+ */
+int lin_decode(const void *q, const void *k, const void *v, const float *g, float *S, void *out, int N, int H, int Hk,
+               int Dk, int Dv, kda_dtype io_dtype, kda_dtype out_dtype, int gate, void *stream);
+int lin_recurrent(const void *q, const void *k, const void *v, const float *g, float *S, void *out,
+                  const int32_t *cu_seqlens, const int32_t *slot_in, const int32_t *slot_out, int N, int T_total, int H,
+                  int Hk, int Dk, int Dv, int slots, kda_dtype io_dtype, kda_dtype out_dtype, int gate, int zero_rows,
+                  void *stream);
+
+/*
+ * kda_tree -- the outputs of a tree of drafted tokens that continues each sequence's state, without
+ * writing one: node t continues the state behind its parent, which is an earlier node, or the
+ * sequence's own state. What a chain of kda_decode steps down from the root to a node gives at it.
+ *
+ *   q, k   [N][T][H][Dk] io_dtype     v    [N][T][H][Dv] io_dtype
+ *   g      [N][T][H][Dk] fp32, with opt->gate == KDA_GATE_HEAD [N][T][H], NULL = no decay
+ *   beta   [N][T][H] beta_dtype       out  [N][T][H][Dv] out_dtype
+ *   S      [slots][H][Dv][Dk] fp32, the pool, only read
+ *   slot_in int32 [N]: the sequence's slot; outside [0, slots), or slot_in NULL: the zero state
+ *   parent int32 [N][T]: an earlier node of the sequence, or -1: the sequence's state. Any other value:
+ *          the node is absent, and so are those that descend from it. Their inputs do not matter
+ *   zero_rows  1: out rows of absent nodes become zero; 0: they stay as they were (else
+ *          KDA_ERR_INVALID_ARG)
+ * slot_in and parent are device arrays. fp32 arithmetic. A NaN or an infinity in a node that is there
+ * may reach other nodes of its sequence. opt: gate and qk_l2norm as for kda_decode_ex, no snapshots; may be
+ * NULL. Support: 1 <= T <= KDA_TREE_NODES; Dk == Dv in {64, 128}; N * H below 2^22 (else
+ * KDA_ERR_UNSUPPORTED). q, k, v, a per-channel g, S and out 16-byte aligned; out none of the other buffers.
+ *
+ * kda_tree_accept -- the state behind one node of such a tree (or, with node -1, the sequence's own) into
+ * a slot: the path to it replayed in fp32.
+ *   k, v, g, beta, S, slot_in, parent  as for kda_tree
+ *   node   int32 [N]: the accepted node, or -1: the state itself. One that is absent, or outside
+ *          [-1, T): nothing is written for the sequence
+ *   slot_out int32 [N]: the slot that receives the state (it may be slot_in's); outside [0, slots): none.
+ *          A slot that one sequence writes must not be read nor written by another one of the call.
+ * opt->qk_l2norm normalises k.
+ *
+ * lin_tree, lin_tree_accept -- the same for linear attention without the delta rule: no beta, q and k
+ * [N][T][Hk][Dk], Dk and Dv each 64 or 128, g [N][T][H], [H] (KDA_GATE_FIXED) or NULL.
+ */
+#define KDA_TREE_NODES 64
+int kda_tree(const void *q, const void *k, const void *v, const float *g, const void *beta, const float *S, void *out,
+             const int32_t *slot_in, const int32_t *parent, int N, int T, int H, int Dk, int Dv, int slots,
+             kda_dtype io_dtype, kda_dtype beta_dtype, kda_dtype out_dtype, int zero_rows, const kda_options *opt,
+             void *stream);
+int kda_tree_accept(const void *k, const void *v, const float *g, const void *beta, float *S, const int32_t *slot_in,
+                    const int32_t *slot_out, const int32_t *parent, const int32_t *node, int N, int T, int H, int Dk,
+                    int Dv, int slots, kda_dtype io_dtype, kda_dtype beta_dtype, const kda_options *opt, void *stream);
+int lin_tree(const void *q, const void *k, const void *v, const float *g, const float *S, void *out,
+             const int32_t *slot_in, const int32_t *parent, int N, int T, int H, int Hk, int Dk, int Dv, int slots,
+             kda_dtype io_dtype, kda_dtype out_dtype, int gate, int zero_rows, void *stream);
+int lin_tree_accept(const void *k, const void *v, const float *g, float *S, const int32_t *slot_in,
+                    const int32_t *slot_out, const int32_t *parent, const int32_t *node, int N, int T, int H, int Hk,
+                    int Dk, int Dv, int slots, kda_dtype io_dtype, int gate, void *stream);
+
+/*
+ * The slots of a state pool [layers][slots][slot_bytes] and their uses, int32 [slots] on the device: how
+ * many sequences (or cached prefixes) hold a slot, 0 = free. All index arrays are device arrays, so a
+ * serving step can run and be captured without the host.
+ *
+ * kda_slots_copy -- for every i < n and layer, slot dst[i] of `to` becomes slot src[i] of `from` (which may be
+ * the same pool: a fork); src[i] outside [0, from_slots): zeros; dst[i] outside [0, to_slots): nothing. A
+ * slot written must not be read, nor written again, by another entry of the call (contents undefined, no
+ * fault). slot_bytes a multiple of 16; pools 16-byte aligned.
+ * kda_slots_share -- uses[which[i]] += 1 for every i < n (a slot named twice counts twice); entries outside
+ * [0, slots) are skipped. kda_slots_release -- the same with -1; a count below zero becomes zero.
+ * kda_slots_acquire -- the n lowest free slots, ascending, into taken [n], their uses 1; -1 where there are
+ * no more.
+ * kda_slots_compact -- moves live slots to the front: with c = the number of slots in use, the ones at or
+ * behind c go, in ascending order, to the free ones before c, in every layer and in uses; other slots
+ * stay where they are and what they hold. table int32 [table_n] (or NULL): entries in [0, slots) become
+ * the slot's new place, -1 for one that was free. count int32 [1] = c. workspace:
+ * kda_slots_compact_workspace_size bytes, 256-byte aligned.
+ * A negative count is free to acquire and compact alike.
+ */
+int kda_slots_copy(const void *from, void *to, const int32_t *src, const int32_t *dst, int n, int layers, int from_slots,
+                   int to_slots, size_t slot_bytes, void *stream);
+int kda_slots_share(int32_t *uses, const int32_t *which, int n, int slots, void *stream);
+int kda_slots_release(int32_t *uses, const int32_t *which, int n, int slots, void *stream);
+int kda_slots_acquire(int32_t *uses, int32_t *taken, int n, int slots, void *stream);
+size_t kda_slots_compact_workspace_size(int slots);
+int kda_slots_compact(void *pool, int32_t *uses, int32_t *table, int32_t *count, int table_n, int layers, int slots,
+                      size_t slot_bytes, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,360 @@
+"""lin_prefill, its gradient and the recurrent forms against the fp64 recurrence.
+
+Bars, as max |error| / RMS over a tensor. fp32 results: every product's operands are exact to 2^-25
+and sums of at most a few thousand terms are taken in fp32: 1e-4, the bar of the library's other
+fp32 paths. bf16 results are off by half a step, 2^-8 relative, besides; their operands, cut in two
+(2^-17, with terms no larger than a few times the sum's RMS), stay under the same 1e-4.
+"""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_103_amd as lib
+from kda_testlib import host64
+from oracle import linear
+
+pytestmark = pytest.mark.gpu
+BAR = 1e-4
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def close(name, got, ref, bar=BAR):
+    half = 2.0 ** -8 if got.dtype == torch.bfloat16 else 0.0
+    err = np.abs(host64(got).reshape(ref.shape) - ref) - half * np.abs(ref)
+    rms = np.sqrt(np.mean(ref * ref))
+    print(f"  {name}: {err.max():.2e} of rms {rms:.2e}", file=sys.stderr, flush=True)
+    assert err.max() <= bar * rms, name
+
+
+def draw(T, H, Hk, Dk, Dv, N=0, io="bf16", gate="head", shift=0.0, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen)
+    unit = lambda *s: torch.nn.functional.normalize(rn(*s), dim=-1)
+    x = dict(q=unit(T, Hk, Dk).to(DT[io]), k=unit(T, Hk, Dk).to(DT[io]), v=rn(T, H, Dv).to(DT[io]))
+    g = -torch.nn.functional.softplus(rn(T, H) + shift)
+    x["g"] = g if gate == "head" else g[0].clone() if gate == "fixed" else None
+    x["S0"] = rn(N, H, Dv, Dk) * 0.3 if N else None
+    return x, rn
+
+
+def gates(x):
+    """g per token and head for the reference."""
+    T, H = x["v"].shape[:2]
+    return np.zeros((T, H)) if x["g"] is None else np.broadcast_to(host64(x["g"]), (T, H))
+
+
+def on(x):
+    return None if x is None else x.cuda().contiguous()
+
+
+def offsets(lengths, before=0):
+    return np.cumsum([before, *lengths]).tolist()
+
+
+def forward(x, cu=None, B=1, **kw):
+    batch = lambda y: on(y).view(B, -1, *y.shape[1:])
+    g = x["g"]
+    g = None if g is None else on(g) if g.dim() == 1 else batch(g)
+    if cu is not None:
+        kw["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    return lib.lin_prefill(batch(x["q"]), batch(x["k"]), batch(x["v"]), g, on(x["S0"]), **kw)
+
+
+def reference(x, cu):
+    return linear.recurrent(*(host64(x[n]) for n in "qkv"), gates(x), None if x["S0"] is None else host64(x["S0"]), cu)
+
+
+LENGTHS = [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300, 0, 513]
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["head", "fixed", "none"])
+def test_packed(Dk, Dv, io, gate):
+    print(f"packed {Dk} {Dv} {io} {gate}", file=sys.stderr, flush=True)
+    cu = offsets(LENGTHS)
+    x, _ = draw(cu[-1], 4, 2, Dk, Dv, len(LENGTHS), io, gate, shift=-1.0, seed=Dk + Dv)
+    o, S = reference(x, cu)
+    out, S_out = forward(x, cu)
+    close("out", out, o)
+    close("S", S_out, S)
+    if io == "bf16":
+        out, _ = forward(x, cu, out_dtype=torch.float32)
+        close("fp32 out", out, o)
+
+
+@pytest.mark.parametrize("T", [1, 2, 64, 100, 128, 129, 700])
+@pytest.mark.parametrize("B", [1, 3])
+def test_dense(T, B):
+    x, _ = draw(B * T, 3, 1, 128, 128, seed=T)
+    o, S = reference(x, [n * T for n in range(B + 1)])
+    out, S_out = forward(x, B=B)
+    assert out.shape == (B, T, 3, 128)
+    close("out", out, o)
+    close("S", S_out, S)
+
+
+@pytest.mark.parametrize("shift", [-6.0, 4.0])
+def test_slow_and_fast_decays(shift):
+    """alpha from about 0.998 to about 0.02, over several segments."""
+    x, _ = draw(2500, 1, 1, 64, 64, 1, "f32", shift=shift, seed=3)
+    o, S = reference(x, [0, 2500])
+    out, S_out = forward(x)
+    close("out", out, o)
+    close("S", S_out, S)
+
+
+def test_decays_that_wipe_and_grow():
+    """-inf and -1000 forget everything; a few steps above zero grow."""
+    x, _ = draw(200, 2, 2, 64, 64, 1, "f32", seed=4)
+    x["g"][[5, 70, 131], 0] = -np.inf
+    x["g"][[64, 128, 150], 1] = -1000.0
+    x["g"][20:25] = 0.5
+    o, S = reference(x, [0, 200])
+    out, S_out = forward(x)
+    close("out", out, o)
+    close("S", S_out, S)
+
+
+@pytest.mark.parametrize("scale", [1e-9, 1e8])
+def test_magnitudes(scale):
+    x, _ = draw(300, 1, 1, 128, 128, 1, "bf16", seed=5)
+    x["v"], x["S0"] = (x["v"].float() * scale).to(torch.bfloat16), x["S0"] * scale
+    o, S = reference(x, [0, 300])
+    out, S_out = forward(x)
+    close("out", out, o)
+    close("S", S_out, S)
+
+
+def test_rows_of_no_sequence_and_in_place_state():
+    x, _ = draw(300, 2, 1, 64, 128, 3, "bf16", seed=6)
+    cu = [7, 150, 150, 280]
+    o, S = reference(x, cu)
+    state = on(x["S0"])
+    out = torch.full((1, 300, 2, 128), 3.0, dtype=torch.bfloat16).cuda()
+    batch = {n: on(x[n])[None] for n in "qkvg"}
+    tcu = torch.tensor(cu, dtype=torch.int32).cuda()
+    lib.lin_prefill(batch["q"], batch["k"], batch["v"], batch["g"], state, out=out, S_out=state, cu_seqlens=tcu)
+    assert (out[0, :7] == 3).all() and (out[0, 280:] == 3).all()
+    close("out", out[0, 7:280], o[7:280])
+    close("S", state, S)
+    fresh, _ = forward(x, cu)
+    assert (fresh[0, :7] == 0).all() and (fresh[0, 280:] == 0).all() and torch.equal(fresh[0, 7:280], out[0, 7:280])
+    # inputs of rows in no sequence do not matter, nor do offsets beyond the rows
+    for n in "qkvg":
+        batch[n][0, :7] = float("nan")
+        batch[n][0, 280:] = float("nan")
+    again, S2 = lib.lin_prefill(batch["q"], batch["k"], batch["v"], batch["g"], on(x["S0"]), cu_seqlens=tcu)
+    assert torch.equal(again, fresh) and torch.equal(S2, state)
+
+
+def test_no_tokens():
+    x, _ = draw(1, 2, 2, 64, 64, 2, seed=7)
+    empty = {n: on(x[n][:0])[None] for n in "qkvg"}
+    cu = torch.zeros(3, dtype=torch.int32).cuda()
+    out, S = lib.lin_prefill(empty["q"], empty["k"], empty["v"], empty["g"], on(x["S0"]), cu_seqlens=cu)
+    assert out.shape[1] == 0 and torch.equal(S, on(x["S0"]))
+    _, S = lib.lin_prefill(empty["q"], empty["k"], empty["v"], empty["g"], cu_seqlens=cu)
+    assert (S == 0).all()
+    d = lib.lin_prefill_backward(empty["q"], empty["k"], empty["v"], on(x["g"][0]), empty["v"], on(x["S0"]), on(x["S0"]),
+                                 cu_seqlens=cu)
+    assert torch.equal(d[4], on(x["S0"])) and (d[3] == 0).all()
+
+
+def backward(x, dout, dS, cu=None, B=1, **kw):
+    batch = lambda y: on(y).view(B, -1, *y.shape[1:])
+    g = x["g"]
+    g = None if g is None else on(g) if g.dim() == 1 else batch(g)
+    if cu is not None:
+        kw["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    return lib.lin_prefill_backward(batch(x["q"]), batch(x["k"]), batch(x["v"]), g, batch(dout),
+                                    on(x["S0"]), on(dS), **kw)
+
+
+def check_gradient(x, dout, dS, cu, got):
+    ref = linear.backward(*(host64(x[n]) for n in "qkv"), gates(x), host64(dout), None if x["S0"] is None else host64(x["S0"]),
+                          None if dS is None else host64(dS), cu)
+    if x["g"] is not None and x["g"].dim() == 1:
+        ref["dg"] = ref["dg"].sum(0)
+    for name, y in zip(("dq", "dk", "dv", "dg", "dS0"), got):
+        if y is not None:
+            close(name, y, ref[name])
+    assert (got[3] is None) == (x["g"] is None) and (got[4] is None) == (x["S0"] is None)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["head", "fixed", "none"])
+def test_gradient_packed(Dk, Dv, io, gate):
+    print(f"gradient {Dk} {Dv} {io} {gate}", file=sys.stderr, flush=True)
+    cu = offsets(LENGTHS)
+    for Hk in (4, 2):
+        x, rn = draw(cu[-1], 4, Hk, Dk, Dv, len(LENGTHS), io, gate, shift=-1.0, seed=Dk + Dv + Hk)
+        dout, dS = (rn(cu[-1], 4, Dv) * 0.1).to(DT[io]), rn(*x["S0"].shape) * 0.1
+        check_gradient(x, dout, dS, cu, backward(x, dout, dS, cu))
+
+
+@pytest.mark.parametrize("T,B", [(1, 1), (64, 2), (129, 3), (700, 1)])
+def test_gradient_dense_without_states(T, B):
+    x, rn = draw(B * T, 2, 2, 128, 128, seed=T)
+    dout = rn(B * T, 2, 128).to(torch.bfloat16)
+    check_gradient(x, dout, None, [n * T for n in range(B + 1)], backward(x, dout, None, B=B))
+
+
+@pytest.mark.parametrize("shift", [-6.0, 4.0])
+def test_gradient_slow_and_fast(shift):
+    x, rn = draw(1500, 1, 1, 64, 64, 1, "f32", shift=shift, seed=8)
+    dout, dS = rn(1500, 1, 64), rn(1, 1, 64, 64)
+    check_gradient(x, dout, dS, [0, 1500], backward(x, dout, dS))
+
+
+def test_gradient_of_wiped_states():
+    x, rn = draw(200, 2, 2, 64, 64, 1, "f32", seed=9)
+    x["g"][[5, 70, 131], 0] = -np.inf
+    x["g"][[64, 128, 150], 1] = -1000.0
+    dout, dS = rn(200, 2, 64), rn(1, 2, 64, 64)
+    got = backward(x, dout, dS)
+    check_gradient(x, dout, dS, [0, 200], got)
+    assert (got[3][0, [5, 70, 131], 0] == 0).all() and (got[3][0, [64, 128, 150], 1] == 0).all()
+
+
+def test_gradient_rows_of_no_sequence():
+    x, rn = draw(300, 4, 2, 64, 64, 2, "bf16", seed=10)
+    dout, dS, cu = rn(300, 4, 64).to(torch.bfloat16), rn(2, 4, 64, 64), [7, 150, 280]
+    fresh = backward(x, dout, dS, cu)
+    out = {n: torch.full(y.shape, 3.0, dtype=y.dtype).cuda() for n, y in zip(("dq", "dk", "dv", "dg"), fresh)}
+    kept = backward(x, dout, dS, cu, **out)
+    for a, b in zip(fresh[:4], kept[:4]):
+        assert (a[0, :7] == 0).all() and (a[0, 280:] == 0).all()
+        assert (b[0, :7] == 3).all() and (b[0, 280:] == 3).all() and torch.equal(a[0, 7:280], b[0, 7:280])
+    y = {n: x[n].clone() for n in "qkvg"}
+    bad = dout.clone()
+    for z in (*y.values(), bad):
+        z[:7] = float("nan")
+        z[280:] = float("nan")
+    for a, b in zip(fresh, backward(dict(y, S0=x["S0"]), bad, dS, cu)):
+        assert torch.equal(a, b)
+
+
+def test_gradient_against_differences_of_the_forward_pass():
+    """A directional derivative of the kernels' own forward pass, fp32: a step e along a direction of unit RMS leaves an error of
+    order e^2 in central differences and rounding of the loss (about 1e-6 of it) over e."""
+    x, rn = draw(150, 2, 1, 64, 64, 1, "f32", seed=11)
+    dout, dS = rn(150, 2, 64), rn(1, 2, 64, 64)
+    got = backward(x, dout, dS)
+
+    def loss(y):
+        o, S = forward(y)
+        return float((o[0].double().cpu() * dout).sum() + (S.double().cpu() * dS).sum())
+
+    for name, d in zip(("q", "k", "v", "g", "S0"), got):
+        way = rn(*x[name].shape)
+        e = 1e-2
+        up, down = (loss(dict(x, **{name: x[name] + s * e * way})) for s in (1, -1))
+        want, have = (up - down) / (2 * e), float((d.double().cpu().view(way.shape) * way).sum())
+        size = float(d.double().norm())
+        assert abs(want - have) <= 2e-2 * size + 1e-6 * abs(up) / e, (name, want, have)
+
+
+def test_repeats_and_graph_replays():
+    x, rn = draw(700, 4, 2, 128, 64, 2, "bf16", gate="head", seed=12)
+    y = {n: on(x[n])[None] for n in "qkvg"}
+    cu, S0 = torch.tensor([0, 600, 700], dtype=torch.int32).cuda(), on(x["S0"])
+    dout, dS = on(rn(1, 700, 4, 64).to(torch.bfloat16)), on(rn(2, 4, 64, 128))
+
+    def both():
+        return (*lib.lin_prefill(y["q"], y["k"], y["v"], y["g"], S0, cu_seqlens=cu),
+                *lib.lin_prefill_backward(y["q"], y["k"], y["v"], y["g"], dout, S0, dS, cu_seqlens=cu))
+
+    first = both()
+    assert all(torch.equal(a, b) for a, b in zip(first, both()))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for i in range(3):
+        y["v"].mul_(-0.7)
+        S0.add_(0.01)
+        graph.replay()
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        want = (*lib.lin_prefill(y["q"], y["k"], y["v"], y["g"], S0, cu_seqlens=cu, stream=st),
+                *lib.lin_prefill_backward(y["q"], y["k"], y["v"], y["g"], dout, S0, dS, cu_seqlens=cu, stream=st))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def recurrent_reference(x, cu, pool, slot_in, slot_out):
+    q, k, v = (host64(x[n]) for n in "qkv")
+    g, start, new = gates(x), host64(pool), host64(pool)
+    out = np.zeros(v.shape)
+    for n in range(len(cu) - 1):
+        s = -1 if slot_in is None else slot_in[n]
+        S = start[s][None] if 0 <= s < len(start) else np.zeros((1, *start.shape[1:]))
+        for t in range(cu[n], cu[n + 1]):
+            one = slice(t, t + 1)
+            out[one], S = linear.recurrent(q[one], k[one], v[one], g[one], S)
+            s = -1 if slot_out is None else slot_out[t]
+            if 0 <= s < len(start):
+                new[s] = S[0]
+    return out, new
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["head", "fixed", "none"])
+def test_recurrent(Dk, Dv, io, gate):
+    lengths = [3, 0, 1, 5, 0, 2]
+    cu = offsets(lengths)
+    x, rn = draw(cu[-1], 4, 2, Dk, Dv, io=io, gate=gate, seed=Dk)
+    pool = (rn(17, 4, Dv, Dk) * 0.2).cuda()
+    slot_in, slot_out = [16, 3, 2, -1, 5, 99], [1, 4, 6, 7, -1, 10, 11, 12, 13, 14, 77][:cu[-1]]
+    ref_o, ref_S = recurrent_reference(x, cu, pool, slot_in, slot_out)
+    idx = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
+    out = lib.lin_recurrent(*(on(x[n]) for n in "qkvg"), pool, idx(slot_in), idx(slot_out), idx(cu))
+    close("out", out, ref_o)
+    close("S", pool, ref_S)
+    # one token each, in place
+    N = 5
+    x, rn = draw(N, 4, 2, Dk, Dv, io=io, gate=gate, seed=Dk + 1)
+    S = (rn(N, 4, Dv, Dk) * 0.2).cuda()
+    ref_o, ref_S = recurrent_reference(x, list(range(N + 1)), S, list(range(N)), list(range(N)))
+    out = lib.lin_decode(*(on(x[n]) for n in "qkvg"), S, out_dtype=torch.float32)
+    close("decode out", out, ref_o)
+    close("decode S", S, ref_S)
+
+
+def test_recurrent_rows_and_decode_of_many():
+    x, rn = draw(9, 2, 2, 64, 64, io="f32", seed=13)
+    pool = torch.zeros(1, 2, 64, 64).cuda()
+    out = torch.full((9, 2, 64), 3.0).cuda()
+    cu = torch.tensor([1, 4, 4, 6], dtype=torch.int32).cuda()
+    args = [on(x[n]) for n in "qkvg"]
+    lib.lin_recurrent(*args, pool, None, None, cu, out=out)
+    assert (out[0] == 3).all() and (out[6:] == 3).all() and (pool == 0).all()
+    fresh = lib.lin_recurrent(*args, pool, None, None, cu)
+    assert (fresh[0] == 0).all() and (fresh[6:] == 0).all() and torch.equal(fresh[1:6], out[1:6])
+    x, rn = draw(700, 8, 1, 128, 128, seed=14)
+    S = (rn(700, 8, 128, 128) * 0.1)
+    pick = [0, 350, 699]
+    sub = {n: x[n][pick] for n in "qkvg"}
+    ref_o, ref_S = recurrent_reference(sub, [0, 1, 2, 3], S[pick], [0, 1, 2], [0, 1, 2])
+    Sd = S.cuda()
+    out = lib.lin_decode(*(on(x[n]) for n in "qkvg"), Sd)
+    close("out", out[pick], ref_o)
+    close("S", Sd[pick], ref_S)
+
+
+def test_prefill_then_steps_is_one_prefill():
+    """A prompt, drafted tokens one by one: the states and outputs of one prefill over all of it."""
+    x, _ = draw(333, 4, 2, 128, 64, 1, "bf16", shift=-2.0, seed=15)
+    o, S = reference(x, [0, 333])
+    cut = {n: x[n][:330] for n in "qkvg"}
+    out, state = forward(dict(cut, S0=x["S0"]))
+    for t in range(330, 333):
+        step = lib.lin_decode(*(on(x[n][t:t + 1]) for n in "qkvg"), state, out_dtype=torch.float32)
+        close(f"token {t}", step, o[t:t + 1])
+    close("S", state, S)
