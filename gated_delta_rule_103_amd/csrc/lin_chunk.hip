@@ -45,7 +45,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kMinLog = -104.f;       // e^-104 rounds to zero: a smaller decay is no other
 
-constexpr int kMaxSegment = 1024;
+constexpr int kMaxSegment = 512;
 
 struct Segments {
     const int32_t *cu;      // packed offsets, or nullptr: N sequences of T tokens
@@ -123,6 +123,16 @@ template <int P> __device__ __forceinline__ void cut(f32x8 x, bf16x8 (&p)[P]) {
     }
 }
 
+// Rows in parts, as col_frag leaves them, times their weights W[0 .. 3] and W[8 .. 11], cut in three.
+template <int NI> __device__ __forceinline__ void weigh(const bf16x8 (&x)[NI], const float *W, bf16x8 (&p)[3]) {
+    f32x8 v = __builtin_convertvector(x[NI - 1], f32x8);
+#pragma unroll
+    for (int i = NI - 2; i >= 0; --i) v += __builtin_convertvector(x[i], f32x8);
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(W), b = *reinterpret_cast<const f32x4 *>(W + 8);
+    v *= __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    cut<3>(v, p);
+}
+
 // acc += x y, x in PX parts and y in PY, products of parts whose indices add up to less than the larger count
 template <int PX, int PY>
 __device__ __forceinline__ f32x16 product(const bf16x8 (&x)[PX], const bf16x8 (&y)[PY], f32x16 acc) {
@@ -133,6 +143,13 @@ __device__ __forceinline__ f32x16 product(const bf16x8 (&x)[PX], const bf16x8 (&
         for (int j = PY - 1; j >= 0; --j)
             if (i + j < P) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc, 0, 0, 0);
     return acc;
+}
+
+// The value again, as one the compiler knows nothing of: addresses derived from it are computed where
+// they are used. Held over the chunk loop, as loop invariants, they cost more registers than there are.
+__device__ __forceinline__ int afresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 // ---- tiles in LDS -----------------------------------------------------------
@@ -163,23 +180,44 @@ template <int D> __device__ __forceinline__ bf16x8 col_frag(const bf16_t *tile, 
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// One head of a token-major tensor over a segment's tokens: a load past them reads zeros, a store is dropped.
+template <typename T> struct Strip {
+    __amdgpu_buffer_rsrc_t r;
+    int stride;                                             // bytes from a token to the next
+    __device__ __forceinline__ Strip(const T *p, int start, int len, int heads, int h, int D)
+        : r(buf_rsrc(p + ((size_t)start * heads + h) * D, len > 0 ? ((len - 1) * heads + 1) * D * (int)sizeof(T) : 0)),
+          stride(heads * D * (int)sizeof(T)) {}
+    // four values of the token `token` places behind the segment's first
+    __device__ __forceinline__ f32x4 load4(int token, int c) const {
+        const int off = token * stride + c * (int)sizeof(T);
+        if constexpr (sizeof(T) == 2)
+            return __builtin_convertvector(__builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0)), f32x4);
+        else
+            return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    }
+    __device__ __forceinline__ void store4(int token, int c, f32x4 x) const {
+        const int off = token * stride + c * (int)sizeof(T);
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4)), r, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, 0);
+    }
+};
+
 // A chunk's rows of one tensor on their way from memory to LDS: C rows of D values by NT threads.
 template <typename T, int D, int C, int NT, int NI> struct Rows {
     static constexpr int PER = 16 / sizeof(T);              // values of a 16-byte load
     static constexpr int N = C * D / PER / NT;              // loads of a thread
+    static constexpr int PASS = NT * PER / D;               // rows between them
     static_assert(C * D % (PER * NT) == 0, "chunk rows per thread");
     u32x4 x[N];
 
-    // rows i0 .. i0 + C - 1 of a segment; row i is token first + i * step where lo <= i < hi, zeros elsewhere
-    __device__ __forceinline__ void load(const T *p, size_t stride, long long first, int step, int i0, int lo, int hi, int t) {
+    // the rows of tokens token0, token0 + step, ..., counted from the segment's first
+    __device__ __forceinline__ void load(const Strip<T> &s, int token0, int step, int t) {
+        const int off = (token0 + step * (t / (D / PER))) * s.stride + t % (D / PER) * 16;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int u = t + n * NT, row = i0 + u / (D / PER);
-            x[n] = u32x4{0u, 0u, 0u, 0u};
-            if (row >= lo && row < hi)
-                x[n] = *reinterpret_cast<const u32x4 *>(p + (size_t)(first + (long long)row * step) * stride +
-                                                        (u % (D / PER)) * PER);
-        }
+        for (int n = 0; n < N; ++n)
+            x[n] = __builtin_amdgcn_raw_buffer_load_b128(s.r, off + n * (step * PASS * s.stride), 0, 0);
     }
     __device__ __forceinline__ void store(bf16_t *tile, int t) const {
 #pragma unroll
@@ -218,16 +256,17 @@ __device__ __forceinline__ float gate_at(const Gate &g, long long token, int h, 
 }
 
 // Cumulative log2-decays of a segment's rows lo .. hi - 1: whole part in A[i].x, fraction in A[i].y (rows
-// before lo: none). Row i is token first + i * step. Backwards (step -1) the decay of row i is that of
-// the token before it in walking order, and row lo has none. Returns the sum over the segment's tokens.
-template <int NT>
-__device__ __forceinline__ double segment_decays(const Gate &g, int h, int H, long long first, int step, int lo, int hi,
+// before lo: none; rows behind hi - 1, to the end of their chunk of C: as row hi - 1). Row i is the
+// segment's token first + i * step. Backwards (step -1) the decay of row i is that of the token before it
+// in walking order, and row lo has none. Returns the sum over the segment's tokens.
+template <int NT, int C>
+__device__ __forceinline__ double segment_decays(const Gate &g, int h, int H, int start, int first, int step, int lo, int hi,
                                                  float2 *A, double *waves, int t) {
     constexpr int NW = NT / 64;
-    const int per = (hi + NT - 1) / NT, i0 = t * per, i1 = min(i0 + per, hi);
+    const int rows = (hi + C - 1) / C * C, per = (rows + NT - 1) / NT, i0 = t * per, i1 = min(i0 + per, rows);
     auto at = [&](int i) {
-        if (i < lo || (step < 0 && i == lo)) return 0.;
-        return (double)gate_at(g, first + (long long)(step > 0 ? i : 1 - i), h, H) * 1.4426950408889634;
+        if (i < lo || i >= hi || (step < 0 && i == lo)) return 0.;
+        return (double)gate_at(g, start + (first + (step > 0 ? i : 1 - i)), h, H) * 1.4426950408889634;
     };
     double sum = 0.;
     for (int i = i0; i < i1; ++i) sum += at(i);
@@ -245,7 +284,7 @@ __device__ __forceinline__ double segment_decays(const Gate &g, int h, int H, lo
         const double whole = floor(run);
         A[i] = float2{(float)whole, (float)(run - whole)};
     }
-    if (step < 0 && hi > lo) total += (double)gate_at(g, first - (hi - 1), h, H) * 1.4426950408889634;
+    if (step < 0 && hi > lo) total += (double)gate_at(g, start, h, H) * 1.4426950408889634;
     __syncthreads();
     return total;
 }
@@ -262,57 +301,50 @@ __global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate ga
     constexpr int NT = DC * 2, ND = DA / 32;
     __shared__ bf16_t Y[NI * C * DA], Z[NI * C * DC];
     __shared__ float2 A[kMaxSegment];
+    __shared__ float W[kMaxSegment];
     __shared__ double waves[NT / 64];
     const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5;
     Segment x;
     if (!find_segment(segs, id, x)) return;
     const StateJob &job = jobs.job[blockIdx.y];
     if (job.skip_last && x.b == x.blocks - 1) return;
-    const long long first = x.begin + (long long)x.b * segs.L;
-    const int len = min(segs.L, x.end - (int)first);
-    const double total = segment_decays<NT>(gate, h, H, first, 1, 0, len, A, waves, t);
+    const int start = x.begin + x.b * segs.L, len = min(segs.L, x.end - start), hs = h / group, HS = H / group;
+    const Strip<T> y(static_cast<const T *>(job.y), start, len, job.y_shared ? HS : H, job.y_shared ? hs : h, DA);
+    const Strip<T> z(static_cast<const T *>(job.z), start, len, job.z_shared ? HS : H, job.z_shared ? hs : h, DC);
+    Rows<T, DA, C, NT, NI> ry;
+    Rows<T, DC, C, NT, NI> rz;
+    ry.load(y, 0, 1, t);
+    rz.load(z, 0, 1, t);
+    const double total = segment_decays<NT, C>(gate, h, H, start, 0, 1, 0, len, A, waves, t);
     if (t == 0 && blockIdx.y == 0) whole[(size_t)id * H + h] = (float)exp2(total);
-
-    const T *y = static_cast<const T *>(job.y) + (job.y_shared ? h / group : h) * DA;
-    const T *z = static_cast<const T *>(job.z) + (job.z_shared ? h / group : h) * DC;
-    const size_t ys = (size_t)(job.y_shared ? H / group : H) * DA, zs = (size_t)(job.z_shared ? H / group : H) * DC;
     const double tw = floor(total);
     const float2 end = float2{(float)tw, (float)(total - tw)};
+    for (int i = t; i < (len + C - 1) / C * C; i += NT) W[i] = job.tail ? decay(end, A[i]) : decay(A[i], float2{0.f, 0.f});
 
     f32x16 S[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) S[d] = f32x16{};
-    Rows<T, DA, C, NT, NI> ry;
-    Rows<T, DC, C, NT, NI> rz;
-    ry.load(y, ys, first, 1, 0, 0, len, t);
-    rz.load(z, zs, first, 1, 0, 0, len, t);
     for (int c0 = 0; c0 < len; c0 += C) {
         __syncthreads();
         ry.store(Y, t);
         rz.store(Z, t);
         __syncthreads();
         if (c0 + C < len) {
-            ry.load(y, ys, first, 1, c0 + C, 0, len, t);
-            rz.load(z, zs, first, 1, c0 + C, 0, len, t);
+            ry.load(y, c0 + C, 1, t);
+            rz.load(z, c0 + C, 1, t);
         }
+        const int lane2 = afresh(lane);
 #pragma unroll
         for (int m = 0; m < C / 16; ++m) {
-            f32x8 zw = {};
+            bf16x8 zv[NI], zp[3];
 #pragma unroll
-            for (int i = NI - 1; i >= 0; --i)
-                zw += __builtin_convertvector(col_frag<DC>(Z + i * C * DC, w, m, lane), f32x8);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = min(c0 + 16 * m + 8 * (e >> 2) + 4 * half + (e & 3), len - 1);
-                zw[e] *= job.tail ? decay(end, A[i]) : __builtin_amdgcn_exp2f(A[i].x + A[i].y);
-            }
-            bf16x8 zp[3];
-            cut<3>(zw, zp);
+            for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane2);
+            weigh(zv, W + c0 + 16 * m + 4 * half, zp);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 bf16x8 yp[NI];
 #pragma unroll
-                for (int i = 0; i < NI; ++i) yp[i] = col_frag<DA>(Y + i * C * DA, d, m, lane);
+                for (int i = 0; i < NI; ++i) yp[i] = col_frag<DA>(Y + i * C * DA, d, m, lane2);
                 S[d] = product<NI, 3>(yp, zp, S[d]);
             }
         }
@@ -379,11 +411,6 @@ template <> __device__ __forceinline__ void store4<float>(float *p, f32x4 x) { *
 template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
     *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(x, bf16x4);
 }
-template <typename T> __device__ __forceinline__ f32x4 load4(const T *p);
-template <> __device__ __forceinline__ f32x4 load4<float>(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-template <> __device__ __forceinline__ f32x4 load4<bf16_t>(const bf16_t *p) {
-    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
-}
 
 // F(x, y, z): queries x and keys y of DA channels, values z of DC. T: the tensors' type, in NI
 // bf16 parts; TO the outputs'; NX parts of states and scores; chunks of 32 NC tokens; DOT: the
@@ -394,6 +421,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     __shared__ bf16_t X[NI * C * DA], Y[NI * C * DA], Z[NI * C * DC];
     __shared__ bf16x8 P[TILES][2][NX][64];
     __shared__ float2 A[kMaxSegment];
+    __shared__ float R[kMaxSegment], W[kMaxSegment];       // decays from the chunk's start through a row, and from a row to its end
     __shared__ double waves[NW];
     __shared__ float own[DOT ? C : 1], dots[DOT ? NW : 1][DOT ? C : 1], past[DOT ? NW : 1];
     const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5,
@@ -402,10 +430,10 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     if (!find_segment(segs, id, s)) return;
     const OutputJob &job = jobs.job[blockIdx.y];
     const int hs = h / group, HS = H / group;
-    TO *out = static_cast<TO *>(job.out) + (job.out_shared ? hs : h) * DC;
-    const size_t os = (size_t)(job.out_shared ? HS : H) * DC;
     if (job.zero_rows) {
         // rows of no sequence lie before the first one and behind the last one
+        TO *out = static_cast<TO *>(job.out) + (job.out_shared ? hs : h) * DC;
+        const size_t os = (size_t)(job.out_shared ? HS : H) * DC;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         if (s.n == 0 && s.b == 0)
             for (size_t u = t; u < (size_t)s.begin * (DC / 4); u += NT) store4(out + u / (DC / 4) * os + u % (DC / 4) * 4, zero);
@@ -415,41 +443,47 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     }
     // rows lo .. hi - 1; backwards the empty rows come first, so that chunks have the same borders both ways
     const int start = s.begin + s.b * segs.L, len = min(segs.L, s.end - start), step = job.back ? -1 : 1;
-    const int hi = job.back ? (len + C - 1) / C * C : len, lo = hi - len;
-    const long long first = job.back ? start + hi - 1 : start;
-    segment_decays<NT>(gate, h, H, first, step, lo, hi, A, waves, t);
-
-    const T *x = static_cast<const T *>(job.x) + (job.x_shared ? hs : h) * DA;
-    const T *y = static_cast<const T *>(job.y) + (job.y_shared ? hs : h) * DA;
-    const T *z = static_cast<const T *>(job.z) + (job.z_shared ? hs : h) * DC;
-    const size_t xs = (size_t)(job.x_shared ? HS : H) * DA, ys = (size_t)(job.y_shared ? HS : H) * DA,
-                 zs = (size_t)(job.z_shared ? HS : H) * DC;
+    const int hi = job.back ? (len + C - 1) / C * C : len, lo = hi - len, first = job.back ? hi - 1 : 0;
+    const Strip<T> x(static_cast<const T *>(job.x), start, len, job.x_shared ? HS : H, job.x_shared ? hs : h, DA);
+    const Strip<T> y(static_cast<const T *>(job.y), start, len, job.y_shared ? HS : H, job.y_shared ? hs : h, DA);
+    const Strip<T> z(static_cast<const T *>(job.z), start, len, job.z_shared ? HS : H, job.z_shared ? hs : h, DC);
+    const Strip<TO> out(static_cast<const TO *>(job.out), start, len, job.out_shared ? HS : H, job.out_shared ? hs : h, DC);
+    const Strip<T> with(static_cast<const T *>(DOT ? job.with : job.z), start, DOT ? len : 0, HS, hs, DC);
     Rows<T, DA, C, NT, NI> rx, ry;
     Rows<T, DC, C, NT, NI> rz;
-    rx.load(x, xs, first, step, 0, lo, hi, t);
-    ry.load(y, ys, first, step, 0, lo, hi, t);
-    rz.load(z, zs, first, step, 0, lo, hi, t);
+    rx.load(x, first, step, t);
+    ry.load(y, first, step, t);
+    rz.load(z, first, step, t);
+    segment_decays<NT, C>(gate, h, H, start, first, step, lo, hi, A, waves, t);
+    for (int i = t; i < (hi + C - 1) / C * C; i += NT) {
+        const int c = i / C * C;
+        R[i] = decay(A[i], c ? A[c - 1] : float2{0.f, 0.f});
+        W[i] = decay(A[c + C - 1], A[i]);
+    }
 
     // the state before the segment, transposed: column = value channel, rows = key channels
     f32x16 S[ND];
-    const size_t cell = ((size_t)(job.border ? id : s.n) * H + h) * DA * DC;
+    const float *Sp = job.S + ((size_t)(job.border ? id : s.n) * H + h) * DA * DC;
+    if (!job.S) {
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+        for (int d = 0; d < ND; ++d) S[d] = f32x16{};
+    } else if (job.key_rows) {                             // as it lies: a row per key channel
+        const float *p = Sp + 4 * half * DC + 32 * w + col;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            const int r = 32 * d + 8 * i + 4 * half, c = 32 * w + col;
-            if (job.S) {
-                if (job.key_rows) {                        // as it lies: a row per key channel
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = job.S[cell + (size_t)(r + e) * DC + c];
-                } else {
-                    v = *reinterpret_cast<const f32x4 *>(job.S + cell + (size_t)c * DA + r);
-                }
+            for (int i = 0; i < 16; ++i) S[d][i] = p[(32 * d + 8 * (i >> 2) + (i & 3)) * DC];
+    } else {
+        const float *p = Sp + (32 * w + col) * DA + 4 * half;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(p + 32 * d + 8 * i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[d][4 * i + e] = v[e];
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[d][4 * i + e] = v[e];
-        }
+    }
     const bool last = job.back ? s.b == 0 : s.b == s.blocks - 1;
     const bool keep = last && job.S_out;
 
@@ -459,16 +493,10 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
         ry.store(Y, t);
         rz.store(Z, t);
         __syncthreads();
-        if (c0 + C < hi) {
-            rx.load(x, xs, first, step, c0 + C, lo, hi, t);
-            ry.load(y, ys, first, step, c0 + C, lo, hi, t);
-            rz.load(z, zs, first, step, c0 + C, lo, hi, t);
-        }
-        const float2 base = c0 ? A[c0 - 1] : float2{0.f, 0.f};
-        const float2 end = A[min(c0 + C, hi) - 1];
 
         // scores, transposed (rows = key tokens s, column = query token i), a tile or two of 32 x 32 a wavefront
         for (int tile = w; tile < TILES; tile += NW) {
+            const int lane2 = afresh(lane), c2 = lane2 & 31, h2 = lane2 >> 5;
             const int ti = NC == 1 ? 0 : (tile + 1) / 2, ts = tile / 2;     // (ts, ti): 00, 01, 11
             f32x16 acc = {};
 #pragma unroll
@@ -476,17 +504,17 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
                 bf16x8 ky[NI], qx[NI];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    ky[i] = row_frag<DA>(Y + i * C * DA, 32 * ts + col, m, half);
-                    qx[i] = row_frag<DA>(X + i * C * DA, 32 * ti + col, m, half);
+                    ky[i] = row_frag<DA>(Y + i * C * DA, 32 * ts + c2, m, h2);
+                    qx[i] = row_frag<DA>(X + i * C * DA, 32 * ti + c2, m, h2);
                 }
                 acc = product<NI, NI>(ky, qx, acc);
             }
             const int i = 32 * ti + col;
-            const float2 ai = A[min(c0 + i, hi - 1)];
+            const float2 ai = A[c0 + i];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int sr = 32 * ts + 8 * (r >> 2) + 4 * half + (r & 3);
-                const float dec = decay(ai, A[min(c0 + sr, hi - 1)]);
+                const float dec = decay(ai, A[c0 + sr]);
                 if (DOT && sr == i) own[i] = acc[r];
                 acc[r] = (DOT ? sr < i : sr <= i) ? acc[r] * dec : 0.f;
             }
@@ -503,6 +531,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
         }
         // e^{a_i} S x_i
         f32x16 O[NC];
+        const int lane2 = afresh(lane), c2 = lane2 & 31, h2 = lane2 >> 5;
 #pragma unroll
         for (int i = 0; i < NC; ++i) O[i] = f32x16{};
 #pragma unroll
@@ -516,35 +545,37 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
             for (int i = 0; i < NC; ++i) {
                 bf16x8 qx[NI];
 #pragma unroll
-                for (int j = 0; j < NI; ++j) qx[j] = row_frag<DA>(X + j * C * DA, 32 * i + col, m, half);
+                for (int j = 0; j < NI; ++j) qx[j] = row_frag<DA>(X + j * C * DA, 32 * i + c2, m, h2);
                 O[i] = product<NX, NI>(sp, qx, O[i]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < NC; ++i) O[i] *= decay(A[min(c0 + 32 * i + col, hi - 1)], base);
+        for (int i = 0; i < NC; ++i) O[i] *= R[c0 + 32 * i + col];
         if constexpr (DOT) {
             // what the chunk's rows have from the state, against `with`
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int row = c0 + 32 * i + col;
-                if (row < lo || row >= hi) continue;
-                const T *with = static_cast<const T *>(job.with) + hs * DC + 32 * w + 4 * half +
-                                (size_t)(first + (long long)row * step) * ((size_t)HS * DC);
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f32x4 y4 = load4(with + 8 * j);
+                    const f32x4 y4 = with.load4(first + step * (c0 + 32 * i + col), 32 * w + 8 * j + 4 * half);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum += O[i][4 * j + e] * y4[e];
                 }
-            }
             sum = warp_sum(sum);
             if (lane == 0) past[w] = sum;
         }
         __syncthreads();
-        // the values: scores times them, and their share of the state
-        const float over = decay(end, base);
-        const bool carry = c0 + C < hi || keep;
+        // the next chunk's rows come while the values are summed: scores times them, and their share of the state
+        const bool more = c0 + C < hi;
+        if (more) {
+            rx.load(x, first + step * (c0 + C), step, t);
+            ry.load(y, first + step * (c0 + C), step, t);
+            rz.load(z, first + step * (c0 + C), step, t);
+        }
+        const bool carry = more || keep;
+        const int lane3 = afresh(lane);
+        const float over = R[c0 + C - 1];
         if (carry) {
 #pragma unroll
             for (int d = 0; d < ND; ++d) S[d] *= over;
@@ -553,7 +584,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
         for (int m = 0; m < C / 16; ++m) {
             bf16x8 zv[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane);
+            for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane3);
 #pragma unroll
             for (int i = m / 2; i < NC; ++i) {
                 bf16x8 p[NX];
@@ -562,37 +593,27 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
                 O[i] = product<NI, NX>(zv, p, O[i]);
             }
             if (carry) {
-                f32x8 zw = {};
-#pragma unroll
-                for (int i = NI - 1; i >= 0; --i) zw += __builtin_convertvector(zv[i], f32x8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    zw[e] *= decay(end, A[min(c0 + 16 * m + 8 * (e >> 2) + 4 * half + (e & 3), hi - 1)]);
                 bf16x8 zp[3];
-                cut<3>(zw, zp);
+                weigh(zv, W + c0 + 16 * m + 4 * half, zp);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     bf16x8 ky[NI];
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) ky[i] = col_frag<DA>(Y + i * C * DA, d, m, lane);
+                    for (int i = 0; i < NI; ++i) ky[i] = col_frag<DA>(Y + i * C * DA, d, m, lane3);
                     S[d] = product<NI, 3>(ky, zp, S[d]);
                 }
             }
         }
-        // out: a lane has token i's channels in groups of four
+        // out: a lane has token i's channels in groups of four; rows of no token fall behind the segment's end
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int row = c0 + 32 * i + col;
-            const bool live = row >= lo && row < hi;
-            const size_t token = (size_t)(first + (long long)row * step);
+            const int token = first + step * (c0 + 32 * i + col);
             if constexpr (DOT) {
-                const T *with = static_cast<const T *>(job.with) + hs * DC + 32 * w + 4 * half;
                 float dot = 0.f;
                 const float mine = own[32 * i + col];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    f32x4 y4 = {0.f, 0.f, 0.f, 0.f};
-                    if (live) y4 = load4(with + token * ((size_t)HS * DC) + 8 * j);
+                    const f32x4 y4 = with.load4(token, 32 * w + 8 * j + 4 * half);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dot += O[i][4 * j + e] * y4[e];
                     f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
@@ -606,12 +627,10 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
                 dot += __shfl_xor(dot, 32, 64);
                 if (half == 0) dots[w][32 * i + col] = dot;
             }
-            if (live) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    store4(out + token * os + 32 * w + 8 * j + 4 * half,
+            for (int j = 0; j < 4; ++j)
+                out.store4(token, 32 * w + 8 * j + 4 * half,
                            f32x4{O[i][4 * j], O[i][4 * j + 1], O[i][4 * j + 2], O[i][4 * j + 3]});
-            }
         }
         if constexpr (DOT) {
             __syncthreads();
@@ -619,7 +638,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
                 float d = 0.f;
 #pragma unroll
                 for (int i = 0; i < NW; ++i) d += dots[i][t];
-                job.dot[(size_t)h * segs.T_total + (size_t)(first + (long long)(c0 + t) * step)] = d;
+                job.dot[(size_t)h * segs.T_total + (size_t)(start + first + step * (c0 + t))] = d;
             }
             if (t == 0) {
                 float d = 0.f;
@@ -632,7 +651,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     }
     if (keep) {
         // backwards, the decay of the segment's first token is still to be applied
-        const float more = job.back && len > 0 ? expf(gate_at(gate, start, h, H)) : 1.f;
+        const float rest = job.back && len > 0 ? expf(gate_at(gate, start, h, H)) : 1.f;
         float *so = job.S_out + ((size_t)s.n * H + h) * DA * DC;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -640,7 +659,7 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
             for (int i = 0; i < 4; ++i) {
                 const int r = 32 * d + 8 * i + 4 * half, c = 32 * w + col;
                 *reinterpret_cast<f32x4 *>(so + (size_t)c * DA + r) =
-                    f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]} * more;
+                    f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]} * rest;
             }
     }
 }
@@ -933,8 +952,8 @@ size_t lin_backward_workspace(int N, long long T_total, int H, int Hk, int Dk, i
     return c.used;
 }
 bool lin_chunk_fits(int N, long long T_total, int H) {
-    // workgroups of a launch times their threads stay below 2^32
-    return id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
+    // workgroups of a launch times their threads stay below 2^32, a segment's tokens below 2^31 bytes
+    return H <= 8192 && id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
 }
 hipError_t launch_lin_prefill(const LinPrefillArgs &a) {
     if ((long long)a.B * a.T == 0) return pass(a.S0, a.S_out, (size_t)a.N * a.H * a.Dk * a.Dv, a.stream);
