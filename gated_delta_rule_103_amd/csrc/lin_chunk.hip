@@ -24,11 +24,12 @@
 // that are taken in 64 bits and held as whole and fractional part in base 2, so that no
 // difference loses bits and no factor exceeds the decay that it stands for.
 //
-// A wavefront owns 32 value channels: its part of the state, transposed, stays in accumulator
-// layout (32 x 32 tiles: column = value channel, rows = key channels), whose registers are,
-// up to the order of the summed index, the A operand of the product with q^T; the score tile
-// q k^T is formed transposed for the same reason. Only scores go through LDS, because the
-// wavefronts share them.
+// A wavefront owns 16 value channels: its part of the state, transposed, stays in accumulator
+// layout (16 x 16 tiles: column = value channel, rows = key channels), whose registers are, up
+// to the order of the summed index, the A operand of the product with q^T; the scores q k^T are
+// formed transposed for the same reason, a lane's four values being a lane's four values of the next
+// product's operand. Only scores go through LDS, because the wavefronts share them. Eight wavefronts of
+// 16 channels rather than four of 32 leave four to a SIMD, which the chunk's barriers and LDS reads need.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -37,15 +38,16 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kMinLog = -104.f;       // e^-104 rounds to zero: a smaller decay is no other
 
-constexpr int kMaxSegment = 512;
+constexpr int kMaxSegment = 1024;
 
 struct Segments {
     const int32_t *cu;      // packed offsets, or nullptr: N sequences of T tokens
@@ -115,33 +117,55 @@ __device__ __forceinline__ bool find_segment(const Segments &s, int id, Segment 
 }
 
 // ---- cutting ----------------------------------------------------------------
+// Pairs at a time: one conversion instruction rounds two values into a word, whose halves are the rounded values.
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ f32x8 widen(bf16x8 x) {
+    const u32x4 w = __builtin_bit_cast(u32x4, x);
+    return f32x8{low(w[0]), high(w[0]), low(w[1]), high(w[1]), low(w[2]), high(w[2]), low(w[3]), high(w[3])};
+}
+__device__ __forceinline__ f32x4 widen(bf16x4 x) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return f32x4{low(w[0]), high(w[0]), low(w[1]), high(w[1])};
+}
+__device__ __forceinline__ bf16x4 narrow(f32x4 x) { return __builtin_bit_cast(bf16x4, u32x2{pack(x[0], x[1]), pack(x[2], x[3])}); }
+
 template <int P> __device__ __forceinline__ void cut(f32x8 x, bf16x8 (&p)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        p[i] = __builtin_convertvector(x, bf16x8);
-        if (i + 1 < P) x -= __builtin_convertvector(p[i], f32x8);
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = pack(x[2 * e], x[2 * e + 1]);
+            x[2 * e] -= low(w[e]);
+            x[2 * e + 1] -= high(w[e]);
+        }
+        p[i] = __builtin_bit_cast(bf16x8, w);
     }
 }
 
-// Rows in parts, as col_frag leaves them, times their weights W[0 .. 3] and W[8 .. 11], cut in three.
+// Rows in parts, as col_frag leaves them, times their weights W[0 .. 3] and W[16 .. 19], cut in three.
 template <int NI> __device__ __forceinline__ void weigh(const bf16x8 (&x)[NI], const float *W, bf16x8 (&p)[3]) {
-    f32x8 v = __builtin_convertvector(x[NI - 1], f32x8);
+    f32x8 v = widen(x[NI - 1]);
 #pragma unroll
-    for (int i = NI - 2; i >= 0; --i) v += __builtin_convertvector(x[i], f32x8);
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(W), b = *reinterpret_cast<const f32x4 *>(W + 8);
+    for (int i = NI - 2; i >= 0; --i) v += widen(x[i]);
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(W), b = *reinterpret_cast<const f32x4 *>(W + 16);
     v *= __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     cut<3>(v, p);
 }
 
 // acc += x y, x in PX parts and y in PY, products of parts whose indices add up to less than the larger count
 template <int PX, int PY>
-__device__ __forceinline__ f32x16 product(const bf16x8 (&x)[PX], const bf16x8 (&y)[PY], f32x16 acc) {
+__device__ __forceinline__ f32x4 product(const bf16x8 (&x)[PX], const bf16x8 (&y)[PY], f32x4 acc) {
     constexpr int P = PX > PY ? PX : PY;
 #pragma unroll
     for (int i = PX - 1; i >= 0; --i)
 #pragma unroll
         for (int j = PY - 1; j >= 0; --j)
-            if (i + j < P) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc, 0, 0, 0);
+            if (i + j < P) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc, 0, 0, 0);
     return acc;
 }
 
@@ -153,30 +177,37 @@ __device__ __forceinline__ int afresh(int x) {
 }
 
 // ---- tiles in LDS -----------------------------------------------------------
-// Rows of D bf16 values in blocks of four, a row's blocks permuted by an exclusive or with
-// swz(row): 32 rows at one block, and four rows at eight neighbouring blocks (the transposing
-// read), both touch every bank once.
+// Rows of D bf16 values in blocks of four, a row's blocks permuted by an exclusive or with swz(row), which
+// keeps pairs of blocks together, so that 32 lanes touch every bank once, whether they read two neighbouring blocks of 16 rows or (the transposing
+// read) four blocks of eight rows.
 template <int D> __device__ __forceinline__ int swz(int row) {
-    return D == 128 ? ((row & 3) << 3) | ((row >> 2) & 7) : (((row >> 1) & 1) << 3) | ((row >> 2) & 7);
+    return D == 128 ? ((row & 3) << 3) | (row & 4) | ((row >> 2) & 2) : ((row & 2) << 2) | (row & 4) | ((row >> 2) & 2);
 }
 template <int D> __device__ __forceinline__ int at(int row, int block) { return row * D + ((block ^ swz<D>(row)) << 2); }
 
-// The 16 values of a k-step m (of 16 channels) that a lane holds of a row, in the order of an
-// accumulator's rows: 16m + 4h .. + 3 and 16m + 8 + 4h .. + 3, h = lane / 32.
-template <int D> __device__ __forceinline__ bf16x8 row_frag(const bf16_t *tile, int row, int m, int h) {
-    const bf16x4 x = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 4 * m + h));
-    const bf16x4 y = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 4 * m + 2 + h));
+// A sum over 32 channels (k-step m) runs in the order that a state's accumulator tiles dictate: lane group g
+// (lane / 16) holds rows 4g .. 4g + 3 of two tiles. Keys lie in LDS so that those rows are channels 32m + 8g .. + 7:
+// their block b at place(b). Queries then are read 16 bytes at a time, as they come.
+__device__ __forceinline__ int place(int b) { return (b & ~7) | ((b & 1) << 2) | ((b >> 1) & 3); }
+// The first of the four channels that lane group g holds in a state's tile d.
+__device__ __forceinline__ int channel(int d, int g) { return 32 * (d >> 1) + 4 * (d & 1) + 8 * g; }
+template <int D> __device__ __forceinline__ bf16x8 query_frag(const bf16_t *tile, int row, int m, int g) {
+    return *reinterpret_cast<const bf16x8 *>(tile + at<D>(row, 8 * m + 2 * g));
+}
+template <int D> __device__ __forceinline__ bf16x8 key_frag(const bf16_t *tile, int row, int m, int g) {
+    const bf16x4 x = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 8 * m + g));
+    const bf16x4 y = *reinterpret_cast<const bf16x4 *>(tile + at<D>(row, 8 * m + 4 + g));
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// The transpose: channel 32c + lane % 32 of tokens 16m + 4h .. + 3 and 16m + 8 + 4h .. + 3.
+// The transpose: channel 16c + lane % 16 of tokens 32m + 4g .. + 3 and 32m + 16 + 4g .. + 3. Sixteen lanes read a
+// 4 x 16 tile, lane j the four values of row j / 4 from column 4 (j % 4) on, and receive its column j.
 __device__ __forceinline__ bf16x4 read_tr(const bf16_t *p) {
     const i16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)p);
     return __builtin_bit_cast(bf16x4, r);
 }
 template <int D> __device__ __forceinline__ bf16x8 col_frag(const bf16_t *tile, int c, int m, int lane) {
-    const int h = lane >> 5, j = lane & 15, block = 8 * c + ((lane >> 4) & 1) * 4 + (j & 3);
-    const bf16x4 x = read_tr(tile + at<D>(16 * m + 4 * h + (j >> 2), block));
-    const bf16x4 y = read_tr(tile + at<D>(16 * m + 8 + 4 * h + (j >> 2), block));
+    const int row = 32 * m + 4 * (lane >> 4) + ((lane >> 2) & 3), block = 4 * c + (lane & 3);
+    const bf16x4 x = read_tr(tile + at<D>(row, block)), y = read_tr(tile + at<D>(row + 16, block));
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -191,14 +222,14 @@ template <typename T> struct Strip {
     __device__ __forceinline__ f32x4 load4(int token, int c) const {
         const int off = token * stride + c * (int)sizeof(T);
         if constexpr (sizeof(T) == 2)
-            return __builtin_convertvector(__builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0)), f32x4);
+            return widen(__builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0)));
         else
             return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
     }
     __device__ __forceinline__ void store4(int token, int c, f32x4 x) const {
         const int off = token * stride + c * (int)sizeof(T);
         if constexpr (sizeof(T) == 2)
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4)), r, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, narrow(x)), r, off, 0, 0);
         else
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, 0);
     }
@@ -219,20 +250,25 @@ template <typename T, int D, int C, int NT, int NI> struct Rows {
         for (int n = 0; n < N; ++n)
             x[n] = __builtin_amdgcn_raw_buffer_load_b128(s.r, off + n * (step * PASS * s.stride), 0, 0);
     }
-    __device__ __forceinline__ void store(bf16_t *tile, int t) const {
+    // KEYS: blocks at their places
+    template <bool KEYS = false> __device__ __forceinline__ void store(bf16_t *tile, int t) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int u = t + n * NT, row = u / (D / PER), e = u % (D / PER);
             if constexpr (NI == 1) {
-                *reinterpret_cast<u32x2 *>(tile + at<D>(row, 2 * e)) = u32x2{x[n][0], x[n][1]};
-                *reinterpret_cast<u32x2 *>(tile + at<D>(row, 2 * e + 1)) = u32x2{x[n][2], x[n][3]};
+                if constexpr (KEYS) {
+                    *reinterpret_cast<u32x2 *>(tile + at<D>(row, place(2 * e))) = u32x2{x[n][0], x[n][1]};
+                    *reinterpret_cast<u32x2 *>(tile + at<D>(row, place(2 * e + 1))) = u32x2{x[n][2], x[n][3]};
+                } else {
+                    *reinterpret_cast<u32x4 *>(tile + at<D>(row, 2 * e)) = x[n];
+                }
             } else {
                 f32x4 y = __builtin_bit_cast(f32x4, x[n]);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const bf16x4 p = __builtin_convertvector(y, bf16x4);
-                    *reinterpret_cast<bf16x4 *>(tile + i * C * D + at<D>(row, e)) = p;
-                    y -= __builtin_convertvector(p, f32x4);
+                    const bf16x4 p = narrow(y);
+                    *reinterpret_cast<bf16x4 *>(tile + i * C * D + at<D>(row, KEYS ? place(e) : e)) = p;
+                    y -= widen(p);
                 }
             }
         }
@@ -258,36 +294,50 @@ __device__ __forceinline__ float gate_at(const Gate &g, long long token, int h, 
 // Cumulative log2-decays of a segment's rows lo .. hi - 1: whole part in A[i].x, fraction in A[i].y (rows
 // before lo: none; rows behind hi - 1, to the end of their chunk of C: as row hi - 1). Row i is the
 // segment's token first + i * step. Backwards (step -1) the decay of row i is that of the token before it
-// in walking order, and row lo has none. Returns the sum over the segment's tokens.
-template <int NT, int C>
-__device__ __forceinline__ double segment_decays(const Gate &g, int h, int H, int start, int first, int step, int lo, int hi,
-                                                 float2 *A, double *waves, int t) {
-    constexpr int NW = NT / 64;
-    const int rows = (hi + C - 1) / C * C, per = (rows + NT - 1) / NT, i0 = t * per, i1 = min(i0 + per, rows);
-    auto at = [&](int i) {
-        if (i < lo || i >= hi || (step < 0 && i == lo)) return 0.;
-        return (double)gate_at(g, start + (first + (step > 0 ? i : 1 - i)), h, H) * 1.4426950408889634;
-    };
-    double sum = 0.;
-    for (int i = i0; i < i1; ++i) sum += at(i);
-    const double incl = wave_prefix(sum, t & 63);
-    if ((t & 63) == 63) waves[t >> 6] = incl;
-    __syncthreads();
-    double run = incl - sum, total = 0.;
+// in walking order, and row lo has none. The gates are read by the constructor, ahead of the rows that
+// would keep them waiting.
+template <int NT, int C> struct SegmentDecays {
+    static constexpr int PER = kMaxSegment / NT;            // rows of a thread, at most
+    float g[PER];
+    int rows, per;
+    __device__ __forceinline__ SegmentDecays(const Gate &gate, int h, int H, int start, int first, int step, int lo, int hi,
+                                             int t) {
+        rows = (hi + C - 1) / C * C;
+        per = (rows + NT - 1) / NT;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < (t >> 6)) run += waves[w];
-        total += waves[w];
+        for (int n = 0; n < PER; ++n) {
+            const int i = t * per + n;
+            const bool none = n >= per || i < lo || i >= hi || (step < 0 && i == lo);
+            g[n] = none ? 0.f : gate_at(gate, start + (first + (step > 0 ? i : 1 - i)), h, H);
+        }
     }
-    for (int i = i0; i < i1; ++i) {
-        run += at(i);
-        const double whole = floor(run);
-        A[i] = float2{(float)whole, (float)(run - whole)};
+    // returns the sum
+    __device__ __forceinline__ double write(float2 *A, double *waves, int t) const {
+        constexpr int NW = NT / 64;
+        const double log2e = 1.4426950408889634;
+        double sum = 0.;
+#pragma unroll
+        for (int n = 0; n < PER; ++n) sum += (double)g[n] * log2e;
+        const double incl = wave_prefix(sum, t & 63);
+        if ((t & 63) == 63) waves[t >> 6] = incl;
+        __syncthreads();
+        double run = incl - sum, total = 0.;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < (t >> 6)) run += waves[w];
+            total += waves[w];
+        }
+#pragma unroll
+        for (int n = 0; n < PER; ++n) {
+            const int i = t * per + n;
+            run += (double)g[n] * log2e;
+            const double whole = floor(run);
+            if (n < per && i < rows) A[i] = float2{(float)whole, (float)(run - whole)};
+        }
+        __syncthreads();
+        return total;
     }
-    if (step < 0 && hi > lo) total += (double)gate_at(g, start, h, H) * 1.4426950408889634;
-    __syncthreads();
-    return total;
-}
+};
 __device__ __forceinline__ float decay(float2 to, float2 from) {
     return __builtin_amdgcn_exp2f((to.x - from.x) + (to.y - from.y));
 }
@@ -296,14 +346,14 @@ __device__ __forceinline__ float decay(float2 to, float2 from) {
 // S^T = sum_i w_i y_i z_i^T over the segment, y [DA] keys and z [DC] values; w_i is the decay
 // from row i to the segment's end (`tail`), or from its start through row i.
 template <typename T, int DA, int DC, int NI, int C>
-__global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate gate, StateJobs jobs, float *whole, int H,
+__global__ __launch_bounds__(DC * 4, 4) void state_kernel(Segments segs, Gate gate, StateJobs jobs, float *whole, int H,
                                                           int group) {
-    constexpr int NT = DC * 2, ND = DA / 32;
+    constexpr int NT = DC * 4, ND = DA / 16;
     __shared__ bf16_t Y[NI * C * DA], Z[NI * C * DC];
     __shared__ float2 A[kMaxSegment];
-    __shared__ float W[kMaxSegment];
+    __shared__ float W[C];
     __shared__ double waves[NT / 64];
-    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5;
+    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, g = lane >> 4;
     Segment x;
     if (!find_segment(segs, id, x)) return;
     const StateJob &job = jobs.job[blockIdx.y];
@@ -311,23 +361,24 @@ __global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate ga
     const int start = x.begin + x.b * segs.L, len = min(segs.L, x.end - start), hs = h / group, HS = H / group;
     const Strip<T> y(static_cast<const T *>(job.y), start, len, job.y_shared ? HS : H, job.y_shared ? hs : h, DA);
     const Strip<T> z(static_cast<const T *>(job.z), start, len, job.z_shared ? HS : H, job.z_shared ? hs : h, DC);
+    const SegmentDecays<NT, C> decays(gate, h, H, start, 0, 1, 0, len, t);
     Rows<T, DA, C, NT, NI> ry;
     Rows<T, DC, C, NT, NI> rz;
     ry.load(y, 0, 1, t);
     rz.load(z, 0, 1, t);
-    const double total = segment_decays<NT, C>(gate, h, H, start, 0, 1, 0, len, A, waves, t);
+    const double total = decays.write(A, waves, t);
     if (t == 0 && blockIdx.y == 0) whole[(size_t)id * H + h] = (float)exp2(total);
     const double tw = floor(total);
     const float2 end = float2{(float)tw, (float)(total - tw)};
-    for (int i = t; i < (len + C - 1) / C * C; i += NT) W[i] = job.tail ? decay(end, A[i]) : decay(A[i], float2{0.f, 0.f});
 
-    f32x16 S[ND];
+    f32x4 S[ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) S[d] = f32x16{};
+    for (int d = 0; d < ND; ++d) S[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < len; c0 += C) {
         __syncthreads();
         ry.store(Y, t);
         rz.store(Z, t);
+        if (t < C) W[t] = job.tail ? decay(end, A[c0 + t]) : decay(A[c0 + t], float2{0.f, 0.f});
         __syncthreads();
         if (c0 + C < len) {
             ry.load(y, c0 + C, 1, t);
@@ -335,11 +386,11 @@ __global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate ga
         }
         const int lane2 = afresh(lane);
 #pragma unroll
-        for (int m = 0; m < C / 16; ++m) {
+        for (int m = 0; m < C / 32; ++m) {
             bf16x8 zv[NI], zp[3];
 #pragma unroll
             for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane2);
-            weigh(zv, W + c0 + 16 * m + 4 * half, zp);
+            weigh(zv, W + 32 * m + 4 * g, zp);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 bf16x8 yp[NI];
@@ -349,13 +400,9 @@ __global__ __launch_bounds__(DC * 2, 2) void state_kernel(Segments segs, Gate ga
             }
         }
     }
-    float *out = job.out + ((size_t)id * H + h) * DA * DC + (size_t)(32 * w + (lane & 31)) * DA + 4 * half;
+    float *out = job.out + ((size_t)id * H + h) * DA * DC + (size_t)(16 * w + (lane & 15)) * DA + 4 * g;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * i) =
-                f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]};
+    for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(out + 16 * d) = S[d];
 }
 
 // ---- states at the segments' borders ------------------------------------------
@@ -409,23 +456,24 @@ __global__ __launch_bounds__(256) void border_kernel(Segments segs, BorderArgs a
 template <typename TO> __device__ __forceinline__ void store4(TO *p, f32x4 x);
 template <> __device__ __forceinline__ void store4<float>(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
 template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
-    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(x, bf16x4);
+    *reinterpret_cast<bf16x4 *>(p) = narrow(x);
 }
 
 // F(x, y, z): queries x and keys y of DA channels, values z of DC. T: the tensors' type, in NI
-// bf16 parts; TO the outputs'; NX parts of states and scores; chunks of 32 NC tokens; DOT: the
+// bf16 parts; TO the outputs'; NX parts of states and scores; chunks of C tokens; DOT: the
 // sum over channels of each output row (its own token's share left out) times a row of `with`.
-template <typename T, typename TO, int DA, int DC, int NI, int NX, int NC, bool DOT>
-__global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate gate, OutputJobs jobs, int H, int group) {
-    constexpr int NT = DC * 2, NW = DC / 32, C = 32 * NC, ND = DA / 32, TILES = NC * (NC + 1) / 2;
+template <typename T, typename TO, int DA, int DC, int NI, int NX, int C, bool DOT>
+__global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate gate, OutputJobs jobs, int H, int group) {
+    constexpr int NT = DC * 4, NW = DC / 16, NC = C / 16, ND = DA / 16, TILES = NC * (NC + 1) / 2;
     __shared__ bf16_t X[NI * C * DA], Y[NI * C * DA], Z[NI * C * DC];
-    __shared__ bf16x8 P[TILES][2][NX][64];
+    __shared__ bf16x4 P[NC * NC / 4 + NC / 2][NX][64][2];  // scores(i, m): 16 query tokens, 32 key tokens, the two halves of the latter
+    auto scores = [](int i, int m) { return (i / 2) * (i / 2 + 1) + (i & 1) * (i / 2 + 1) + m; };
     __shared__ float2 A[kMaxSegment];
-    __shared__ float R[kMaxSegment], W[kMaxSegment];       // decays from the chunk's start through a row, and from a row to its end
+    __shared__ float R[C], W[C];                           // decays from the chunk's start through a row, and from a row to its end
     __shared__ double waves[NW];
     __shared__ float own[DOT ? C : 1], dots[DOT ? NW : 1][DOT ? C : 1], past[DOT ? NW : 1];
-    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, half = lane >> 5,
-              col = lane & 31;
+    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6, g = lane >> 4,
+              col = lane & 15;
     Segment s;
     if (!find_segment(segs, id, s)) return;
     const OutputJob &job = jobs.job[blockIdx.y];
@@ -449,122 +497,108 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     const Strip<T> z(static_cast<const T *>(job.z), start, len, job.z_shared ? HS : H, job.z_shared ? hs : h, DC);
     const Strip<TO> out(static_cast<const TO *>(job.out), start, len, job.out_shared ? HS : H, job.out_shared ? hs : h, DC);
     const Strip<T> with(static_cast<const T *>(DOT ? job.with : job.z), start, DOT ? len : 0, HS, hs, DC);
+    const SegmentDecays<NT, C> decays(gate, h, H, start, first, step, lo, hi, t);
+    // the state before the segment, transposed: column = value channel, rows = key channels
+    f32x4 S[ND];
+    const float *Sp = job.S + ((size_t)(job.border ? id : s.n) * H + h) * DA * DC;
+    if (!job.S) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) S[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    } else if (job.key_rows) {                             // as it lies: a row per key channel
+        const float *p = Sp + 8 * g * DC + 16 * w + col;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[d][e] = p[(channel(d, 0) + e) * DC];
+    } else {
+        const float *p = Sp + (16 * w + col) * DA + 8 * g;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) S[d] = *reinterpret_cast<const f32x4 *>(p + channel(d, 0));
+    }
     Rows<T, DA, C, NT, NI> rx, ry;
     Rows<T, DC, C, NT, NI> rz;
     rx.load(x, first, step, t);
     ry.load(y, first, step, t);
     rz.load(z, first, step, t);
-    segment_decays<NT, C>(gate, h, H, start, first, step, lo, hi, A, waves, t);
-    for (int i = t; i < (hi + C - 1) / C * C; i += NT) {
-        const int c = i / C * C;
-        R[i] = decay(A[i], c ? A[c - 1] : float2{0.f, 0.f});
-        W[i] = decay(A[c + C - 1], A[i]);
-    }
-
-    // the state before the segment, transposed: column = value channel, rows = key channels
-    f32x16 S[ND];
-    const float *Sp = job.S + ((size_t)(job.border ? id : s.n) * H + h) * DA * DC;
-    if (!job.S) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d) S[d] = f32x16{};
-    } else if (job.key_rows) {                             // as it lies: a row per key channel
-        const float *p = Sp + 4 * half * DC + 32 * w + col;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[d][i] = p[(32 * d + 8 * (i >> 2) + (i & 3)) * DC];
-    } else {
-        const float *p = Sp + (32 * w + col) * DA + 4 * half;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(p + 32 * d + 8 * i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[d][4 * i + e] = v[e];
-            }
-    }
+    decays.write(A, waves, t);
     const bool last = job.back ? s.b == 0 : s.b == s.blocks - 1;
     const bool keep = last && job.S_out;
 
     for (int c0 = 0; c0 < hi; c0 += C) {
         __syncthreads();
         rx.store(X, t);
-        ry.store(Y, t);
+        ry.template store<true>(Y, t);
         rz.store(Z, t);
+        if (t < C) {
+            R[t] = decay(A[c0 + t], c0 ? A[c0 - 1] : float2{0.f, 0.f});
+            W[t] = decay(A[c0 + C - 1], A[c0 + t]);
+        }
         __syncthreads();
 
-        // scores, transposed (rows = key tokens s, column = query token i), a tile or two of 32 x 32 a wavefront
+        // scores, transposed: rows = key tokens, column = query token
         for (int tile = w; tile < TILES; tile += NW) {
-            const int lane2 = afresh(lane), c2 = lane2 & 31, h2 = lane2 >> 5;
-            const int ti = NC == 1 ? 0 : (tile + 1) / 2, ts = tile / 2;     // (ts, ti): 00, 01, 11
-            f32x16 acc = {};
+            const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, ts = tile - ti * (ti + 1) / 2;
+            const int lane2 = afresh(lane), c2 = lane2 & 15, g2 = lane2 >> 4;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int m = 0; m < DA / 16; ++m) {
+            for (int m = 0; m < DA / 32; ++m) {
                 bf16x8 ky[NI], qx[NI];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    ky[i] = row_frag<DA>(Y + i * C * DA, 32 * ts + c2, m, h2);
-                    qx[i] = row_frag<DA>(X + i * C * DA, 32 * ti + c2, m, h2);
+                    ky[i] = key_frag<DA>(Y + i * C * DA, 16 * ts + c2, m, g2);
+                    qx[i] = query_frag<DA>(X + i * C * DA, 16 * ti + c2, m, g2);
                 }
                 acc = product<NI, NI>(ky, qx, acc);
             }
-            const int i = 32 * ti + col;
+            const int i = 16 * ti + col, sr = 16 * ts + 4 * g;
             const float2 ai = A[c0 + i];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int sr = 32 * ts + 8 * (r >> 2) + 4 * half + (r & 3);
-                const float dec = decay(ai, A[c0 + sr]);
-                if (DOT && sr == i) own[i] = acc[r];
-                acc[r] = (DOT ? sr < i : sr <= i) ? acc[r] * dec : 0.f;
+            for (int r = 0; r < 4; ++r) {
+                const float dec = decay(ai, A[c0 + sr + r]);
+                if (DOT && sr + r == i) own[i] = acc[r];
+                acc[r] = (DOT ? sr + r < i : sr + r <= i) ? acc[r] * dec : 0.f;
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                f32x8 v;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = acc[8 * m + e];
-                bf16x8 p[NX];
-                cut<NX>(v, p);
-#pragma unroll
-                for (int j = 0; j < NX; ++j) P[tile][m][j][lane] = p[j];
+            for (int j = 0; j < NX; ++j) {
+                const bf16x4 p = narrow(acc);
+                P[scores(ti, ts / 2)][j][lane][ts & 1] = p;
+                if (ts == ti && !(ts & 1)) P[scores(ti, ts / 2)][j][lane][1] = bf16x4{};     // later keys than any query's
+                acc -= widen(p);
             }
         }
         // e^{a_i} S x_i
-        f32x16 O[NC];
-        const int lane2 = afresh(lane), c2 = lane2 & 31, h2 = lane2 >> 5;
+        f32x4 O[NC];
+        const int lane2 = afresh(lane), c2 = lane2 & 15, g2 = lane2 >> 4;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) O[i] = f32x16{};
+        for (int i = 0; i < NC; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < DA / 16; ++m) {
-            f32x8 v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = S[m >> 1][8 * (m & 1) + e];
+        for (int m = 0; m < DA / 32; ++m) {
             bf16x8 sp[NX];
-            cut<NX>(v, sp);
+            cut<NX>(__builtin_shufflevector(S[2 * m], S[2 * m + 1], 0, 1, 2, 3, 4, 5, 6, 7), sp);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 bf16x8 qx[NI];
 #pragma unroll
-                for (int j = 0; j < NI; ++j) qx[j] = row_frag<DA>(X + j * C * DA, 32 * i + c2, m, h2);
+                for (int j = 0; j < NI; ++j) qx[j] = query_frag<DA>(X + j * C * DA, 16 * i + c2, m, g2);
                 O[i] = product<NX, NI>(sp, qx, O[i]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < NC; ++i) O[i] *= R[c0 + 32 * i + col];
+        for (int i = 0; i < NC; ++i) O[i] *= R[16 * i + col];
         if constexpr (DOT) {
             // what the chunk's rows have from the state, against `with`
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i) {
+                const f32x4 y4 = with.load4(first + step * (c0 + 16 * i + col), 16 * w + 4 * g);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 y4 = with.load4(first + step * (c0 + 32 * i + col), 32 * w + 8 * j + 4 * half);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum += O[i][4 * j + e] * y4[e];
-                }
+                for (int e = 0; e < 4; ++e) sum += O[i][e] * y4[e];
+            }
             sum = warp_sum(sum);
             if (lane == 0) past[w] = sum;
         }
+        const float over = R[C - 1];
         __syncthreads();
         // the next chunk's rows come while the values are summed: scores times them, and their share of the state
         const bool more = c0 + C < hi;
@@ -573,64 +607,60 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
             ry.load(y, first + step * (c0 + C), step, t);
             rz.load(z, first + step * (c0 + C), step, t);
         }
-        const bool carry = more || keep;
         const int lane3 = afresh(lane);
-        const float over = R[c0 + C - 1];
-        if (carry) {
 #pragma unroll
-            for (int d = 0; d < ND; ++d) S[d] *= over;
-        }
-#pragma unroll
-        for (int m = 0; m < C / 16; ++m) {
+        for (int m = 0; m < C / 32; ++m) {
             bf16x8 zv[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane3);
 #pragma unroll
-            for (int i = m / 2; i < NC; ++i) {
+            for (int i = 2 * m; i < NC; ++i) {
                 bf16x8 p[NX];
 #pragma unroll
-                for (int j = 0; j < NX; ++j) p[j] = P[m / 2 + i][m & 1][j][lane];
+                for (int j = 0; j < NX; ++j) p[j] = *reinterpret_cast<const bf16x8 *>(P[scores(i, m)][j][lane]);
                 O[i] = product<NI, NX>(zv, p, O[i]);
             }
-            if (carry) {
-                bf16x8 zp[3];
-                weigh(zv, W + c0 + 16 * m + 4 * half, zp);
+        }
+        // out: a lane has four channels of token i; rows of no token fall behind the segment's end
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int token = first + step * (c0 + 16 * i + col), c = 16 * w + 4 * g;
+            if constexpr (DOT) {
+                const f32x4 y4 = with.load4(token, c);
+                float dot = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot += O[i][e] * y4[e];
+                dot += __shfl_xor(dot, 16, 64);
+                dot += __shfl_xor(dot, 32, 64);
+                if (g == 0) dots[w][16 * i + col] = dot;
+                f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int p = NI - 1; p >= 0; --p)
+                    z4 += widen(*reinterpret_cast<const bf16x4 *>(Z + p * C * DC + at<DC>(16 * i + col, 4 * w + g)));
+                O[i] += z4 * own[16 * i + col];
+            }
+            out.store4(token, c, O[i]);
+        }
+        if (more || keep) {
+            __builtin_amdgcn_s_setprio(1);
+            const int lane4 = afresh(lane);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[d] *= over;
+#pragma unroll
+            for (int m = 0; m < C / 32; ++m) {
+                bf16x8 zv[NI], zp[3];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) zv[i] = col_frag<DC>(Z + i * C * DC, w, m, lane4);
+                weigh(zv, W + 32 * m + 4 * g, zp);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     bf16x8 ky[NI];
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) ky[i] = col_frag<DA>(Y + i * C * DA, d, m, lane3);
+                    for (int i = 0; i < NI; ++i) ky[i] = col_frag<DA>(Y + i * C * DA, d, m, lane4);
                     S[d] = product<NI, 3>(ky, zp, S[d]);
                 }
             }
-        }
-        // out: a lane has token i's channels in groups of four; rows of no token fall behind the segment's end
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int token = first + step * (c0 + 32 * i + col);
-            if constexpr (DOT) {
-                float dot = 0.f;
-                const float mine = own[32 * i + col];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 y4 = with.load4(token, 32 * w + 8 * j + 4 * half);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dot += O[i][4 * j + e] * y4[e];
-                    f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int p = NI - 1; p >= 0; --p)
-                        z4 += __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(
-                                  Z + p * C * DC + at<DC>(32 * i + col, 8 * w + 2 * j + half)), f32x4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) O[i][4 * j + e] += mine * z4[e];
-                }
-                dot += __shfl_xor(dot, 32, 64);
-                if (half == 0) dots[w][32 * i + col] = dot;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                out.store4(token, 32 * w + 8 * j + 4 * half,
-                           f32x4{O[i][4 * j], O[i][4 * j + 1], O[i][4 * j + 2], O[i][4 * j + 3]});
+            __builtin_amdgcn_s_setprio(0);
         }
         if constexpr (DOT) {
             __syncthreads();
@@ -652,15 +682,9 @@ __global__ __launch_bounds__(DC * 2, 2) void output_kernel(Segments segs, Gate g
     if (keep) {
         // backwards, the decay of the segment's first token is still to be applied
         const float rest = job.back && len > 0 ? expf(gate_at(gate, start, h, H)) : 1.f;
-        float *so = job.S_out + ((size_t)s.n * H + h) * DA * DC;
+        float *so = job.S_out + ((size_t)s.n * H + h) * DA * DC + (size_t)(16 * w + col) * DA + 8 * g;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 32 * d + 8 * i + 4 * half, c = 32 * w + col;
-                *reinterpret_cast<f32x4 *>(so + (size_t)c * DA + r) =
-                    f32x4{S[d][4 * i], S[d][4 * i + 1], S[d][4 * i + 2], S[d][4 * i + 3]} * rest;
-            }
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(so + channel(d, 0)) = S[d] * rest;
     }
 }
 
@@ -746,11 +770,13 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
 }
 
 // ---- host -----------------------------------------------------------------------
-// Tokens a segment: enough segments for a few workgroups on every CU, while the states between
-// them (8 D^2 bytes a segment and pass, 0.5 KB a token at 256) stay below the tokens' own bytes.
+// Tokens a segment: as many segments and heads as there are places for workgroups (two a CU), while
+// the states between them are traffic of their own (8 D^2 bytes a segment and pass). 8192 tokens x 32
+// heads with 256, 512, 1024 tokens a segment: 156, 136, 161 us; 65536 x 16 630, 525, 486 us; 2048 x 4 with 64,
+// 128, 256: 32, 34, 47 us; 512 x 8 with 64 and 128: 24, 31 us.
 int segment_length(long long T_total, int H) {
-    long long L = T_total * H / 1024;
-    int p = 128;
+    const long long L = T_total * H / 512;
+    int p = 64;
     while (p < kMaxSegment && 2 * p <= L) p *= 2;
     return p;
 }
@@ -806,7 +832,7 @@ template <typename T, int DA, int DC>
 hipError_t run_states(const Segments &segs, const Gate &gate, const StateJobs &jobs, int n, float *whole, int H, int group,
                       hipStream_t stream) {
     const unsigned ids = (unsigned)id_count(segs.T_total, segs.N, segs.L);
-    hipLaunchKernelGGL((state_kernel<T, DA, DC, Parts<T>::N, Parts<T>::C>), dim3(ids * H, n), dim3(DC * 2), 0, stream, segs,
+    hipLaunchKernelGGL((state_kernel<T, DA, DC, Parts<T>::N, Parts<T>::C>), dim3(ids * H, n), dim3(DC * 4), 0, stream, segs,
                        gate, jobs, whole, H, group);
     return hipGetLastError();
 }
@@ -818,7 +844,7 @@ template <typename T, typename TO, int DA, int DC, int NX, bool DOT>
 hipError_t run_outputs(const Segments &segs, const Gate &gate, const OutputJobs &jobs, int n, int H, int group,
                        hipStream_t stream) {
     const unsigned ids = (unsigned)id_count(segs.T_total, segs.N, segs.L);
-    hipLaunchKernelGGL((output_kernel<T, TO, DA, DC, Parts<T>::N, NX, Parts<T>::C / 32, DOT>), dim3(ids * H, n), dim3(DC * 2),
+    hipLaunchKernelGGL((output_kernel<T, TO, DA, DC, Parts<T>::N, NX, Parts<T>::C, DOT>), dim3(ids * H, n), dim3(DC * 4),
                        0, stream, segs, gate, jobs, H, group);
     return hipGetLastError();
 }
@@ -953,7 +979,7 @@ size_t lin_backward_workspace(int N, long long T_total, int H, int Hk, int Dk, i
 }
 bool lin_chunk_fits(int N, long long T_total, int H) {
     // workgroups of a launch times their threads stay below 2^32, a segment's tokens below 2^31 bytes
-    return H <= 8192 && id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
+    return H <= 4096 && id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
 }
 hipError_t launch_lin_prefill(const LinPrefillArgs &a) {
     if ((long long)a.B * a.T == 0) return pass(a.S0, a.S_out, (size_t)a.N * a.H * a.Dk * a.Dv, a.stream);

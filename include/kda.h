@@ -507,7 +507,7 @@ int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, co
  * be none of the inputs.
  *
  * Support (else KDA_ERR_UNSUPPORTED): Dk and Dv each 64 or 128; io_dtype KDA_F32 with fp32 out, or
- * KDA_BF16 with either; (T_total / 128 + N) * H below 2^23, T_total * H below 2^27. Hk must divide H
+ * KDA_BF16 with either; H at most 4096, N * H below 2^22, T_total * H below 2^27. Hk must divide H
  * (else KDA_ERR_INVALID_ARG).
  * Arithmetic: states in fp32 with products of operands cut in three bf16 parts (fp32 precision),
  * for values whose products stay between about 1e-33 and 3.3e38; an fp32 out likewise; a bf16 out is
@@ -515,7 +515,7 @@ int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, co
  * earlier outputs of its sequence (up to 63 tokens before).
  * workspace: lin_prefill_workspace_size bytes, 256-byte aligned, contents ignored, used by
  * nothing else until the call's work has finished; may be NULL when that is 0 (it is where all
- * tokens together are one segment, 128 to 1024 tokens). It holds a state per segment and head.
+ * tokens together are one segment, 64 to 1024 tokens). It holds a state per segment and head.
  */
 size_t lin_prefill_workspace_size(int N, int T_total, int H, int Dk, int Dv);
 int lin_prefill(const void *q, const void *k, const void *v, const float *g, const float *S0, void *out, float *S_out,
