@@ -573,8 +573,8 @@ int lin_recurrent(const void *q, const void *k, const void *v, const float *g, f
  *          KDA_ERR_INVALID_ARG)
  * slot_in and parent are device arrays. fp32 arithmetic. A NaN or an infinity in a node that is there
  * may reach other nodes of its sequence. opt: gate and qk_l2norm as for kda_decode_ex, no snapshots; may be
- * NULL. Support: 1 <= T <= KDA_TREE_NODES; Dk == Dv in {64, 128}; N * H below 2^22 (else
- * KDA_ERR_UNSUPPORTED). q, k, v, a per-channel g, S and out 16-byte aligned; out none of the other buffers.
+ * NULL. Support: 1 <= T <= KDA_TREE_NODES; Dk == Dv in {64, 128}; N * H below 2^22, H at
+ * most 65536 (else KDA_ERR_UNSUPPORTED). q, k, v, a per-channel g, S and out 16-byte aligned; out none of the other buffers.
  *
  * kda_tree_accept -- the state behind one node of such a tree (or, with node -1, the sequence's own) into
  * a slot: the path to it replayed in fp32.
