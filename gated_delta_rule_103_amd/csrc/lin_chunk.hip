@@ -51,7 +51,8 @@ constexpr int kMaxSegment = 1024;
 
 struct Segments {
     const int32_t *cu;      // packed offsets, or nullptr: N sequences of T tokens
-    int N, T, T_total, L;   // L tokens a segment
+    int N, T, T_total, L;   // L tokens a segment, 2^shift
+    int shift;
 };
 struct Gate {
     const float *g;         // [tokens][H], fixed: [H]; nullptr: none
@@ -83,36 +84,42 @@ struct OutputJobs { OutputJob job[3]; };
 // ---- sequences and segments -------------------------------------------------
 // Segment ids need no table: sequence n starts at id begin_n / L + n, which leaves room for
 // ceil(length / L) ids (one for an empty sequence) and grows with n, so an id's sequence is
-// found by bisection. Ids between two sequences' are holes.
+// found by a search, a wavefront's lanes at a time. Ids between two sequences' are holes.
 struct Segment {
     int n, begin, end;      // the sequence and its tokens
     int b, blocks;          // this segment's index in it, and how many it has
 };
 
-__device__ __forceinline__ void sequence_bounds(const Segments &s, int n, int &begin, int &end) {
-    if (!s.cu) {
-        begin = n * s.T;
-        end = begin + s.T;
-        return;
-    }
-    begin = min(max(s.cu[n], 0), s.T_total);        // offsets outside the packed rows are cut to them
-    end = min(max(s.cu[n + 1], begin), s.T_total);
+// where sequence n begins; offsets outside the packed rows are cut to them
+__device__ __forceinline__ int offset(const Segments &s, int n) {
+    return s.cu ? min(max(s.cu[n], 0), s.T_total) : n * s.T;
 }
-__device__ __forceinline__ int block_count(const Segments &s, int len) { return max(1, (len + s.L - 1) / s.L); }
-__device__ __forceinline__ int first_id(const Segments &s, int n, int begin) { return begin / s.L + n; }
+__device__ __forceinline__ void sequence_bounds(const Segments &s, int n, int &begin, int &end) {
+    begin = offset(s, n);
+    end = max(offset(s, n + 1), begin);
+}
+__device__ __forceinline__ int block_count(const Segments &s, int len) { return max(1, (len + s.L - 1) >> s.shift); }
+__device__ __forceinline__ int first_id(const Segments &s, int n, int begin) { return (begin >> s.shift) + n; }
 
-// false: a hole
+// false: a hole. The same in every lane.
 __device__ __forceinline__ bool find_segment(const Segments &s, int id, Segment &x) {
-    int lo = 0, hi = s.N - 1;
-    while (lo < hi) {                               // the last sequence that starts at or before id
-        const int mid = (lo + hi + 1) / 2;
-        const int at = s.cu ? min(max(s.cu[mid], 0), s.T_total) : mid * s.T;
-        if (first_id(s, mid, at) <= id) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, span = s.N;                         // the sequence is one of span from lo on
+    while (span > 64) {
+        const int each = (span + 63) / 64, i = lo + lane * each;
+        const bool before = lane * each < span && first_id(s, i, offset(s, i)) <= id;
+        const int c = max(__popcll(__ballot(before)) - 1, 0);
+        lo += c * each;
+        span = min(each, span - c * each);
     }
-    x.n = lo;
-    sequence_bounds(s, lo, x.begin, x.end);
+    const int i = min(lo + lane, s.N - 1), begin = offset(s, i), end = max(offset(s, i + 1), begin);
+    const bool before = lane < span && first_id(s, i, begin) <= id;
+    const int c = max(__popcll(__ballot(before)) - 1, 0);
+    x.n = __builtin_amdgcn_readfirstlane(lo + c);
+    x.begin = __builtin_amdgcn_readlane(begin, c);
+    x.end = __builtin_amdgcn_readlane(end, c);
     x.blocks = block_count(s, x.end - x.begin);
-    x.b = id - first_id(s, lo, x.begin);
+    x.b = id - first_id(s, x.n, x.begin);
     return x.b >= 0 && x.b < x.blocks;
 }
 
@@ -274,6 +281,25 @@ template <typename T, int D, int C, int NT, int NI> struct Rows {
         }
     }
 };
+
+// ---- sums over lanes ---------------------------------------------------------
+// over the four groups of 16 lanes, by exchanging rows and halves
+__device__ __forceinline__ float group_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+// over the 16 lanes of a group
+template <int BY> __device__ __forceinline__ float turned(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + BY, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float lane_sum(float x) {
+    x += turned<8>(x);
+    x += turned<4>(x);
+    x += turned<2>(x);
+    return x + turned<1>(x);
+}
 
 // ---- decays -----------------------------------------------------------------
 __device__ __forceinline__ double wave_prefix(double x, int lane) {
@@ -595,7 +621,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum += O[i][e] * y4[e];
             }
-            sum = warp_sum(sum);
+            sum = group_sum(lane_sum(sum));
             if (lane == 0) past[w] = sum;
         }
         const float over = R[C - 1];
@@ -630,8 +656,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
                 float dot = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dot += O[i][e] * y4[e];
-                dot += __shfl_xor(dot, 16, 64);
-                dot += __shfl_xor(dot, 32, 64);
+                dot = group_sum(dot);
                 if (g == 0) dots[w][16 * i + col] = dot;
                 f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -852,7 +877,7 @@ hipError_t run_outputs(const Segments &segs, const Gate &gate, const OutputJobs 
 template <typename T, int DK, int DV> hipError_t prefill(const LinPrefillArgs &a) {
     const long long T_total = (long long)a.B * a.T;
     const int L = segment_length(T_total, a.H), group = a.H / a.Hk;
-    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L};
+    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L, __builtin_ctz((unsigned)L)};
     const Gate gate{a.g, a.fixed};
     Carver c{static_cast<char *>(a.ws)};
     const ForwardSpace ws = carve_forward(c, a.N, T_total, a.H, DK, DV, L);
@@ -881,7 +906,7 @@ template <typename T, int DK, int DV> hipError_t prefill(const LinPrefillArgs &a
 template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs &a) {
     const long long T_total = (long long)a.B * a.T;
     const int L = segment_length(T_total, a.H), group = a.H / a.Hk, ids = (int)id_count(T_total, a.N, L);
-    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L};
+    const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L, __builtin_ctz((unsigned)L)};
     const Gate gate{a.g, a.fixed};
     Carver c{static_cast<char *>(a.ws)};
     const BackwardSpace ws = carve_backward(c, a.N, T_total, a.H, group, DK, DV, L);

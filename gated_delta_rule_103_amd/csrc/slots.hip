@@ -3,7 +3,9 @@
 //
 // A pool [layers][slots] of equal states and a count of uses per slot (0: free). A state is
 // moved whole, so the copies are bound by memory, two bytes of traffic a byte: 16-byte loads
-// and stores, eight in flight a thread, with the non-temporal hint (nothing is read twice).
+// and stores with the non-temporal hint (nothing is read twice), 16 KB a workgroup. 96 states of 2 MB:
+// 402 MB in 71 us, 5.6 TB/s (32 KB a workgroup 103 us, 8 KB 71, without the hint 77); the call with its
+// release and acquire 78 us. 144 states moved by compaction: 118 us.
 // The index work is a few thousand whole numbers at most: one workgroup, prefix sums by
 // ballots, every result independent of the order in which threads run.
 #include "kda_device.h"
@@ -14,7 +16,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int NT = 256, PER = 8;
+constexpr int NT = 512, PER = 2;
 constexpr size_t CHUNK = (size_t)NT * PER * 16;      // bytes a workgroup moves at a time
 
 // One chunk of a state; from == nullptr: zeros.
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(NT) void moves_kernel(char *pool, const int32_t *__
 bool slots_copy_fits(long long n, int layers, size_t slot_bytes) {
     // workgroups times their threads stay below 2^32
     const double chunks = (double)(slot_bytes / CHUNK + 1);
-    return (double)n * layers * chunks < (double)(1 << 24);
+    return (double)n * layers * chunks < (double)(1 << 23);
 }
 
 hipError_t launch_slots_copy(const SlotsCopyArgs &a) {
