@@ -795,14 +795,14 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
 }
 
 // ---- host -----------------------------------------------------------------------
-// Tokens a segment: as many segments and heads as there are places for workgroups (two a CU), while
-// the states between them are traffic of their own (8 D^2 bytes a segment and pass). 8192 tokens x 32
-// heads with 256, 512, 1024 tokens a segment: 156, 136, 161 us; 65536 x 16 630, 525, 486 us; 2048 x 4 with 64,
-// 128, 256: 32, 34, 47 us; 512 x 8 with 64 and 128: 24, 31 us.
+// Tokens a segment, a power of two: the least that leaves one round of workgroups, two a CU; more segments
+// would be traffic (8 D^2 bytes each and pass) for nothing. 8192 tokens x 32 heads with 256, 512, 1024 tokens a
+// segment: 156, 136, 161 us; 65536 x 16 630, 525, 486; 2048 x 4 with 64, 128, 256: 32, 34, 47; 5000 x 8 with 64 and
+// 128: 59, 45 us.
 int segment_length(long long T_total, int H) {
     const long long L = T_total * H / 512;
     int p = 64;
-    while (p < kMaxSegment && 2 * p <= L) p *= 2;
+    while (p < kMaxSegment && p < L) p *= 2;
     return p;
 }
 long long id_count(long long T_total, int N, int L) { return T_total / L + N; }
