@@ -799,10 +799,18 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
 // would be traffic (8 D^2 bytes each and pass) for nothing. 8192 tokens x 32 heads with 256, 512, 1024 tokens a
 // segment: 156, 136, 161 us; 65536 x 16 630, 525, 486; 2048 x 4 with 64, 128, 256: 32, 34, 47; 5000 x 8 with 64 and
 // 128: 59, 45 us.
-int segment_length(long long T_total, int H) {
+//
+// Short sequences (`longest`: no sequence has more tokens) are one segment each, and their states need no passes
+// of their own: 64 x 256 tokens x 32 heads 216 -> 160 us, 16 x 200 x 8 37 -> 25, 128 x 8 22 -> 15; one of 256 x 8
+// has too few workgroups that way (gradient 34 -> 55 us). A longest below T_total never makes segments shorter
+// than T_total alone would, which the workspace is sized by.
+int segment_length(long long longest, long long T_total, int H) {
     const long long L = T_total * H / 512;
     int p = 64;
     while (p < kMaxSegment && p < L) p *= 2;
+    const long long few = T_total * H >= 64 * 256 ? 256 : 128;
+    const long long whole = T_total <= few ? T_total : longest <= few ? longest : 0;
+    while (p < whole) p *= 2;
     return p;
 }
 long long id_count(long long T_total, int N, int L) { return T_total / L + N; }
@@ -823,9 +831,9 @@ struct BackwardSpace {
     float *states, *grads, *whole, *dots, *rows, *cols, *read, *past, *dq, *dk;
     double *sums;
 };
-ForwardSpace carve_forward(Carver &c, int N, long long T_total, int H, int Dk, int Dv, int L) {
+ForwardSpace carve_forward(Carver &c, int N, long long longest, long long T_total, int H, int Dk, int Dv, int L) {
     ForwardSpace s{};
-    if (T_total <= L) return s;                             // every sequence is one segment
+    if (longest <= L) return s;                             // every sequence is one segment
     const size_t cells = (size_t)id_count(T_total, N, L) * H;
     s.states = c.take<float>(cells * Dk * Dv);
     s.whole = c.take<float>(cells);
@@ -876,11 +884,12 @@ hipError_t run_outputs(const Segments &segs, const Gate &gate, const OutputJobs 
 
 template <typename T, int DK, int DV> hipError_t prefill(const LinPrefillArgs &a) {
     const long long T_total = (long long)a.B * a.T;
-    const int L = segment_length(T_total, a.H), group = a.H / a.Hk;
+    const long long longest = a.cu_seqlens ? T_total : a.T;
+    const int L = segment_length(longest, T_total, a.H), group = a.H / a.Hk;
     const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L, __builtin_ctz((unsigned)L)};
     const Gate gate{a.g, a.fixed};
     Carver c{static_cast<char *>(a.ws)};
-    const ForwardSpace ws = carve_forward(c, a.N, T_total, a.H, DK, DV, L);
+    const ForwardSpace ws = carve_forward(c, a.N, longest, T_total, a.H, DK, DV, L);
     OutputJobs out{};
     OutputJob &o = out.job[0];
     o.x = a.q; o.y = a.k; o.z = a.v; o.out = a.out; o.S = a.S0; o.S_out = a.S_out;
@@ -905,30 +914,38 @@ template <typename T, int DK, int DV> hipError_t prefill(const LinPrefillArgs &a
 
 template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs &a) {
     const long long T_total = (long long)a.B * a.T;
-    const int L = segment_length(T_total, a.H), group = a.H / a.Hk, ids = (int)id_count(T_total, a.N, L);
+    const long long longest = a.cu_seqlens ? T_total : a.T;
+    const int L = segment_length(longest, T_total, a.H), group = a.H / a.Hk, ids = (int)id_count(T_total, a.N, L);
+    // sequences of one segment, whose last state has no gradient: states and gradients start from what the caller gives
+    const bool borders = longest > L || a.dS_out;
     const Segments segs{a.cu_seqlens, a.N, a.T, (int)T_total, L, __builtin_ctz((unsigned)L)};
     const Gate gate{a.g, a.fixed};
     Carver c{static_cast<char *>(a.ws)};
     const BackwardSpace ws = carve_backward(c, a.N, T_total, a.H, group, DK, DV, L);
-    StateJobs st{};
-    st.job[0] = StateJob{a.k, a.v, ws.states, true, false, true, false};
-    st.job[1] = StateJob{a.q, a.dout, ws.grads, true, false, false, false};
-    hipError_t e = run_states<T, DK, DV>(segs, gate, st, 2, ws.whole, a.H, group, a.stream);
-    if (e != hipSuccess) return e;
-    BorderArgs b{};
-    b.S0 = a.S0; b.dS_out = a.dS_out; b.states = ws.states; b.grads = ws.grads; b.dS0 = a.dS0; b.dots = ws.dots;
-    b.whole = ws.whole; b.all = true;
-    e = run_borders(segs, b, a.H, DK * DV, a.stream);
-    if (e != hipSuccess) return e;
+    hipError_t e = hipSuccess;
+    if (borders) {
+        StateJobs st{};
+        st.job[0] = StateJob{a.k, a.v, ws.states, true, false, true, false};
+        st.job[1] = StateJob{a.q, a.dout, ws.grads, true, false, false, false};
+        e = run_states<T, DK, DV>(segs, gate, st, 2, ws.whole, a.H, group, a.stream);
+        if (e != hipSuccess) return e;
+        BorderArgs b{};
+        b.S0 = a.S0; b.dS_out = a.dS_out; b.states = ws.states; b.grads = ws.grads; b.dS0 = a.dS0; b.dots = ws.dots;
+        b.whole = ws.whole; b.all = true;
+        e = run_borders(segs, b, a.H, DK * DV, a.stream);
+        if (e != hipSuccess) return e;
+    }
 
     // dq = F(dout, v, k) from the states, dk = F(v, dout, q) and dv = F(k, q, dout) from their gradients
     OutputJobs qk{}, vj{};
     OutputJob &q = qk.job[0], &k = qk.job[1], &v = vj.job[0];
-    q.x = a.dout; q.y = a.v; q.z = a.k; q.with = a.q; q.dot = ws.rows; q.past = ws.read; q.S = ws.states;
-    k.x = a.v; k.y = a.dout; k.z = a.q; k.with = a.k; k.dot = ws.cols; k.past = ws.past; k.S = ws.grads;
-    v.x = a.k; v.y = a.q; v.z = a.dout; v.S = ws.grads; v.out = a.dv;
+    q.x = a.dout; q.y = a.v; q.z = a.k; q.with = a.q; q.dot = ws.rows; q.past = ws.read; q.S = borders ? ws.states : a.S0;
+    k.x = a.v; k.y = a.dout; k.z = a.q; k.with = a.k; k.dot = ws.cols; k.past = ws.past; k.S = borders ? ws.grads : nullptr;
+    v.x = a.k; v.y = a.q; v.z = a.dout; v.S = borders ? ws.grads : nullptr; v.out = a.dv;
+    v.S_out = borders ? nullptr : a.dS0;
     q.z_shared = k.z_shared = v.x_shared = v.y_shared = true;
-    q.border = k.border = v.border = q.key_rows = k.key_rows = k.back = v.back = true;
+    q.border = k.border = v.border = borders;
+    q.key_rows = k.key_rows = k.back = v.back = true;
     v.zero_rows = a.zero_rows & 4;
     if (group == 1) {
         q.out = a.dq; k.out = a.dk;
@@ -962,7 +979,7 @@ template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs 
     }
     if (a.g) {
         hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(ids * a.H)), dim3(64), 0, a.stream, segs, gate, ws.rows, ws.cols,
-                           ws.read, ws.past, ws.dots, DK * DV / 1024, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
+                           ws.read, ws.past, ws.dots, borders ? DK * DV / 1024 : 0, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.fixed) {
             hipLaunchKernelGGL(fixed_grad_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, ws.sums, a.dg, ids, a.H);
@@ -993,18 +1010,18 @@ struct Backward { template <typename T, int DK, int DV> static hipError_t run(co
 
 size_t lin_prefill_workspace(int N, long long T_total, int H, int Dk, int Dv) {
     Carver c{nullptr};
-    carve_forward(c, N, T_total, H, Dk, Dv, segment_length(T_total, H));
+    carve_forward(c, N, T_total, T_total, H, Dk, Dv, segment_length(T_total, T_total, H));
     return c.used;
 }
 size_t lin_backward_workspace(int N, long long T_total, int H, int Hk, int Dk, int Dv) {
     if (T_total == 0) return 0;
     Carver c{nullptr};
-    carve_backward(c, N, T_total, H, H / Hk, Dk, Dv, segment_length(T_total, H));
+    carve_backward(c, N, T_total, H, H / Hk, Dk, Dv, segment_length(T_total, T_total, H));
     return c.used;
 }
 bool lin_chunk_fits(int N, long long T_total, int H) {
     // workgroups of a launch times their threads stay below 2^32, a segment's tokens below 2^31 bytes
-    return H <= 4096 && id_count(T_total, N, segment_length(T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
+    return H <= 4096 && id_count(T_total, N, segment_length(T_total, T_total, H)) * H < (1ll << 23) && T_total * H < (1ll << 27);
 }
 hipError_t launch_lin_prefill(const LinPrefillArgs &a) {
     if ((long long)a.B * a.T == 0) return pass(a.S0, a.S_out, (size_t)a.N * a.H * a.Dk * a.Dv, a.stream);

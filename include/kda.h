@@ -514,8 +514,8 @@ int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, co
  * rounded from sums whose operands are cut in two (2^-17). A NaN or an infinity in a token may reach
  * earlier outputs of its sequence (up to 63 tokens before).
  * workspace: lin_prefill_workspace_size bytes, 256-byte aligned, contents ignored, used by
- * nothing else until the call's work has finished; may be NULL when that is 0 (it is where all
- * tokens together are one segment, 64 to 1024 tokens). It holds a state per segment and head.
+ * nothing else until the call's work has finished; may be NULL when that is 0 (all tokens together
+ * are one segment, 64 to 1024 tokens). It holds a state per segment and head.
  */
 size_t lin_prefill_workspace_size(int N, int T_total, int H, int Dk, int Dv);
 int lin_prefill(const void *q, const void *k, const void *v, const float *g, const float *S0, void *out, float *S_out,
