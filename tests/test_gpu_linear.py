@@ -20,8 +20,9 @@ BAR = 1e-4
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def close(name, got, ref, bar=BAR):
-    half = 2.0 ** -8 if got.dtype == torch.bfloat16 else 0.0
+def close(name, got, ref, bar=BAR, rounded=1):
+    """``rounded`` 2: ref has been rounded to bf16 too, so that the two may lie half a step each from the same value."""
+    half = rounded * 2.0 ** -8 if got.dtype == torch.bfloat16 else 0.0
     err = np.abs(host64(got).reshape(ref.shape) - ref) - half * np.abs(ref)
     rms = np.sqrt(np.mean(ref * ref))
     print(f"  {name}: {err.max():.2e} of rms {rms:.2e}", file=sys.stderr, flush=True)
