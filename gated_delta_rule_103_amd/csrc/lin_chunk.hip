@@ -506,6 +506,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
     Segment s;
     if (!find_segment(segs, id, s)) return;
     const OutputJob &job = jobs.job[blockIdx.y];
+    const bool dot = DOT && (sizeof(T) == 2 || job.with);   // uniform; in fp32 a job may do without
     const int hs = h / group, HS = H / group;
     if (job.zero_rows) {
         // rows of no sequence lie before the first one and behind the last one
@@ -525,7 +526,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
     const Strip<T> y(static_cast<const T *>(job.y), start, len, job.y_shared ? HS : H, job.y_shared ? hs : h, DA);
     const Strip<T> z(static_cast<const T *>(job.z), start, len, job.z_shared ? HS : H, job.z_shared ? hs : h, DC);
     const Strip<TO> out(static_cast<const TO *>(job.out), start, len, job.out_shared ? HS : H, job.out_shared ? hs : h, DC);
-    const Strip<T> with(static_cast<const T *>(DOT ? job.with : job.z), start, DOT ? len : 0, HS, hs, DC);
+    const Strip<T> with(static_cast<const T *>(dot ? job.with : job.z), start, dot ? len : 0, HS, hs, DC);
     const SegmentDecays<NT, C> decays(gate, h, H, start, first, step, lo, hi, t);
     // the state before the segment, transposed: column = value channel, rows = key channels
     f32x4 S[ND];
@@ -584,8 +585,8 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float dec = decay(ai, A[c0 + sr + r]);
-                if (DOT && sr + r == i) own[i] = acc[r];
-                acc[r] = (DOT ? sr + r < i : sr + r <= i) ? acc[r] * dec : 0.f;
+                if (dot && sr + r == i) own[i] = acc[r];
+                acc[r] = sr + r < i + !dot ? acc[r] * dec : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < NX; ++j) {
@@ -615,7 +616,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) O[i] *= R[16 * i + col];
-        if constexpr (DOT) {
+        if (dot) {
             // what the chunk's rows have from the state, against `with`
             float sum = 0.f;
 #pragma unroll
@@ -654,13 +655,13 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int token = first + step * (c0 + 16 * i + col), c = 16 * w + 4 * g;
-            if constexpr (DOT) {
+            if (dot) {
                 const f32x4 y4 = with.load4(token, c);
-                float dot = 0.f;
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dot += O[i][e] * y4[e];
-                dot = group_sum(dot);
-                if (g == 0) dots[w][16 * i + col] = dot;
+                for (int e = 0; e < 4; ++e) sum += O[i][e] * y4[e];
+                sum = group_sum(sum);
+                if (g == 0) dots[w][16 * i + col] = sum;
                 f32x4 z4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int p = NI - 1; p >= 0; --p)
@@ -700,7 +701,7 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
             }
             __builtin_amdgcn_s_setprio(0);
         }
-        if constexpr (DOT) {
+        if (dot) {
             __syncthreads();
             if (t < C && c0 + t >= lo && c0 + t < hi) {
                 float d = 0.f;
@@ -733,45 +734,55 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 // not, so it never runs further than a chunk: G at the chunks' borders follows from G at the segment's
 // end by what the chunks' tokens have from the state (read, q . dq) and from its gradient (past,
 // k . dk) alone, and inside a chunk the sums from both of its borders are weighted by their
-// nearness. C tokens a chunk; a wavefront a (segment, head), sums in 64 bits.
-__global__ __launch_bounds__(64) void decay_grad_kernel(Segments segs, Gate gate, const float *__restrict__ rows,
-                                                        const float *__restrict__ cols, const float *__restrict__ read,
-                                                        const float *__restrict__ past, const float *__restrict__ dots,
-                                                        int parts, int C, float *__restrict__ dg, double *__restrict__ sums,
-                                                        int H, int zero_rows) {
-    const int id = blockIdx.x / H, h = blockIdx.x % H, lane = threadIdx.x;
+// nearness. C tokens a chunk, a wavefront each; a workgroup a (segment, head); sums in 64 bits and a fixed order.
+__global__ __launch_bounds__(256) void decay_grad_kernel(Segments segs, Gate gate, const float *__restrict__ rows,
+                                                         const float *__restrict__ cols, const float *__restrict__ read,
+                                                         const float *__restrict__ past, const float *__restrict__ dots,
+                                                         int parts, int C, float *__restrict__ dg, double *__restrict__ sums,
+                                                         int H, int zero_rows) {
+    __shared__ double chunk_sums[kMaxSegment / 32];
+    const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6;
     Segment s;
     if (!find_segment(segs, id, s)) {
-        if (gate.fixed && lane == 0) sums[(size_t)id * H + h] = 0.;
+        if (gate.fixed && t == 0) sums[(size_t)id * H + h] = 0.;
         return;
     }
     if (zero_rows && !gate.fixed) {
         if (s.n == 0 && s.b == 0)
-            for (int i = lane; i < s.begin; i += 64) dg[(size_t)i * H + h] = 0.f;
+            for (int i = t; i < s.begin; i += 256) dg[(size_t)i * H + h] = 0.f;
         if (s.n == segs.N - 1 && s.b == s.blocks - 1)
-            for (int i = s.end + lane; i < segs.T_total; i += 64) dg[(size_t)i * H + h] = 0.f;
+            for (int i = s.end + t; i < segs.T_total; i += 256) dg[(size_t)i * H + h] = 0.f;
     }
     const int start = s.begin + s.b * segs.L, len = min(segs.L, s.end - start);
     const size_t at = (size_t)h * segs.T_total + start, cell = (size_t)id * H + h;
-    double G = 0., sum = 0.;
-    for (int i = 0; i < parts; ++i) G += dots[cell * parts + i];
-    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {       // C <= 64 tokens, one a lane
+    const int chunks = (len + C - 1) / C;
+    const float *rd = read + cell * (segs.L / C), *pt = past + cell * (segs.L / C);
+    for (int c = w; c < chunks; c += 4) {                    // C <= 64 tokens, one a lane
+        double G = 0.;
+        for (int i = 0; i < parts; ++i) G += dots[cell * parts + i];
+        for (int i = chunks - 1; i > c; --i) G += (double)rd[i] - (double)pt[i];
+        const double before = G + (double)rd[c] - (double)pt[c];
         const int i = c * C + lane, n = min(C, len - c * C);
-        const double before = G + (double)read[cell * (segs.L / C) + c] - (double)past[cell * (segs.L / C) + c];
         const double x = lane < n ? (double)rows[at + i] - (double)cols[at + i] : 0.;
         const double upto = wave_prefix(x, lane), all = __shfl(upto, 63, 64);
         const double near = (double)lane / n;
-        const double d = near * (G + (all - upto) + x) + (1. - near) * (before - (upto - x));
-        if (lane < n) {
-            // at -104 the decay is zero, and its gradient too
-            const bool none = gate.g[gate.fixed ? h : (size_t)(start + i) * H + h] <= kMinLog;
-            if (gate.fixed) sum += none ? 0. : d; else dg[(size_t)(start + i) * H + h] = none ? 0.f : (float)d;
+        double d = near * (G + (all - upto) + x) + (1. - near) * (before - (upto - x));
+        // at -104 the decay is zero, and its gradient too
+        if (lane >= n || gate.g[gate.fixed ? h : (size_t)(start + i) * H + h] <= kMinLog) d = 0.;
+        if (gate.fixed) {
+            d = wave_prefix(d, lane);
+            if (lane == 63) chunk_sums[c] = d;
+        } else if (lane < n) {
+            dg[(size_t)(start + i) * H + h] = (float)d;
         }
-        G = before;
     }
     if (gate.fixed) {
-        sum = wave_prefix(sum, lane);
-        if (lane == 63) sums[(size_t)id * H + h] = sum;
+        __syncthreads();
+        if (t == 0) {
+            double sum = 0.;
+            for (int c = 0; c < chunks; ++c) sum += chunk_sums[c];
+            sums[cell] = sum;
+        }
     }
 }
 
@@ -784,10 +795,13 @@ __global__ __launch_bounds__(64) void fixed_grad_kernel(const double *__restrict
     if (lane == 63) dg[h] = (float)x;
 }
 
-// The gradient of a shared query or key head: the sum over its group's heads.
+// The gradients of shared query and key heads: the sums over their groups' heads.
 template <typename TO>
-__global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *__restrict__ part, TO *__restrict__ out, int H,
-                                                    int group, int D, int zero_rows) {
+__global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *part0, const float *part1, TO *out0, TO *out1,
+                                                    int H, int group, int D, int zero_bits) {
+    const float *part = blockIdx.y ? part1 : part0;
+    TO *out = blockIdx.y ? out1 : out0;
+    const bool zero_rows = (zero_bits >> blockIdx.y) & 1;
     const size_t u = (size_t)blockIdx.x * 256 + threadIdx.x;
     const int HS = H / group, q = D / 4;
     const size_t token = u / ((size_t)HS * q);
@@ -968,30 +982,29 @@ template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs 
     } else {
         q.out = ws.dq; k.out = ws.dk;
     }
+    // fp32, square states: all three in one launch (their precision is the same), which small batches feel
+    const bool together = sizeof(T) == 4 && DK == DV && a.g;
+    if (together) qk.job[2] = v;
     if (group == 1 && sizeof(T) == 2) {
         if constexpr (sizeof(T) == 2)
             e = a.g ? run_outputs<T, bf16_t, DV, DK, 3, true>(segs, gate, qk, 2, a.H, group, a.stream)
                     : run_outputs<T, bf16_t, DV, DK, 2, false>(segs, gate, qk, 2, a.H, group, a.stream);
     } else {
-        e = a.g ? run_outputs<T, float, DV, DK, 3, true>(segs, gate, qk, 2, a.H, group, a.stream)
+        e = a.g ? run_outputs<T, float, DV, DK, 3, true>(segs, gate, qk, together ? 3 : 2, a.H, group, a.stream)
                 : run_outputs<T, float, DV, DK, 3, false>(segs, gate, qk, 2, a.H, group, a.stream);
     }
     if (e != hipSuccess) return e;
     if constexpr (sizeof(T) == 2) e = run_outputs<T, bf16_t, DK, DV, 2, false>(segs, gate, vj, 1, a.H, group, a.stream);
-    else e = run_outputs<T, float, DK, DV, 3, false>(segs, gate, vj, 1, a.H, group, a.stream);
+    else if (!together) e = run_outputs<T, float, DK, DV, 3, false>(segs, gate, vj, 1, a.H, group, a.stream);
     if (e != hipSuccess) return e;
     if (group > 1) {
         const unsigned blocks = (unsigned)(((size_t)T_total * a.Hk * (DK / 4) + 255) / 256);
-        const float *part[2] = {ws.dq, ws.dk};
-        void *to[2] = {a.dq, a.dk};
-        for (int i = 0; i < 2; ++i) {
-            hipLaunchKernelGGL((share_kernel<T>), dim3(blocks), dim3(256), 0, a.stream, segs, part[i], static_cast<T *>(to[i]),
-                               a.H, group, DK, a.zero_rows & (1 << i));
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        hipLaunchKernelGGL((share_kernel<T>), dim3(blocks, 2), dim3(256), 0, a.stream, segs, ws.dq, ws.dk, static_cast<T *>(a.dq),
+                           static_cast<T *>(a.dk), a.H, group, DK, a.zero_rows & 3);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.g) {
-        hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(ids * a.H)), dim3(64), 0, a.stream, segs, gate, ws.rows, ws.cols,
+        hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(ids * a.H)), dim3(256), 0, a.stream, segs, gate, ws.rows, ws.cols,
                            ws.read, ws.past, ws.dots, borders ? DK * DV / 1024 : 0, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.fixed) {
