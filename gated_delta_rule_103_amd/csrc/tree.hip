@@ -12,7 +12,7 @@
 // formed: memory bounds the kernel, 4 Dk Dv bytes a (sequence, head). The decays only ever
 // multiply down a path, so no exponent is cut or inverted.
 //
-// A workgroup takes one (sequence, head), or a part of its value channels. Sixteen lanes, whose sums
+// A workgroup takes one (sequence, head). Sixteen lanes, whose sums
 // need no LDS, walk from a node to its root. The products with the state run on the bf16 matrix
 // instructions with all operands cut in three (2^-25, the six products that matter): the fp32 ones
 // would take five times as long, which is more than the state's way from memory for more than 16 nodes.
@@ -21,9 +21,9 @@
 // which is the operand layout of the fp32 products that follow, and (I + L) is inverted in its 16 x 16
 // diagonal blocks only.
 //
-// 128 trees of 16 nodes x 32 heads x 128 channels: 83 us, 369 MB, 4.4 TB/s (fp32 matrix instructions 89); 64 of 32 76 us, 32
-// of 64 92 us (all their Kd and Qd in LDS at once: 104 and 110, for want of workgroups a CU); linear
-// attention's 69 us. One tree of 61 nodes x 16 heads: 22 us, latency.
+// 128 trees of 16 nodes x 32 heads x 128 channels: 83 us, 369 MB, 4.4 TB/s (fp32 matrix instructions 89); 64 of 32 75 us, 32
+// of 64 91 us (all their Kd and Qd in LDS at once: 104 and 110, for want of workgroups a CU); linear
+// attention's 68 us. One tree of 61 nodes x 16 heads: 21 us, latency.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -132,13 +132,13 @@ __device__ __forceinline__ float row_sum(float x) {
 constexpr int kPad = 8, kTile = 20;      // values of padding a row; floats a row of a 16 x 16 tile
 __device__ __forceinline__ constexpr int tile_of(int a, int b) { return a * (a + 1) / 2 + b; }
 
-// TT: tiles of 16 nodes; NW wavefronts of CT tiles of 16 value channels each
-template <int DK, int DV, typename T, bool DELTA, int TT, int NW, int CT>
+// TT: tiles of 16 nodes; NW wavefronts
+template <int DK, int DV, typename T, bool DELTA, int TT, int NW>
 __global__ __launch_bounds__(64 * NW, TT == 1 || NW == 8 ? 4 : 2) void tree_kernel(TreeArgs p) {
     constexpr int NODES = 16 * TT, KM = DK / 16, CH = DK / 64, NT = 64 * NW;
     constexpr int GROUPS = NT / 16, NP = (NODES + GROUPS - 1) / GROUPS;      // 16 lanes a node, NP nodes a group
-    constexpr int SPLIT = DV / (16 * NW * CT), PART = 16;   // nodes whose Kd and Qd are in LDS at a time
-    static_assert(SPLIT * NW * CT * 16 == DV && (PART % GROUPS == 0 || GROUPS % PART == 0), "tree tiling");
+    constexpr int CT = DV / (16 * NW), PART = 16;           // tiles of value channels a wavefront; nodes whose Kd and Qd are in LDS at a time
+    static_assert(NW * CT * 16 == DV && (PART % GROUPS == 0 || GROUPS % PART == 0), "tree tiling");
     // keys (as they came) and decays for the walk; then, in their place, Kd and Qd
     struct Walk { T k[NODES][DK]; f32x4 a[NODES][DK / 4]; };
     struct Products { bf16_t k[DELTA ? 3 : 1][DELTA ? PART : 1][DK + kPad], q[3][PART][DK + kPad]; };
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(64 * NW, TT == 1 || NW == 8 ? 4 : 2) void tree_kern
     __shared__ float Lt[DELTA ? tile_of(TT, 0) : 1][16 * kTile], Mt[tile_of(TT, 0)][16 * kTile];
     __shared__ float beta[NODES], kn[NODES];                     // kn: the normalisation's factor
     __shared__ int up[NODES], there[NODES];
-    const int chain = blockIdx.x / SPLIT, n = chain / p.H, h = chain % p.H, hs = h / (p.H / p.Hk);
+    const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, hs = h / (p.H / p.Hk);
     const int t = threadIdx.x, lane = t & 63, w = t >> 6, r16 = lane & 15, q4 = lane >> 4, nodes = p.T;
     // this head's first values of the sequence's first node; offsets from them stay below 2^31
     const size_t row0 = (size_t)n * nodes, kv0 = (row0 * p.Hk + hs) * DK, vo0 = (row0 * p.H + h) * DV;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * NW, TT == 1 || NW == 8 ? 4 : 2) void tree_kern
     const int from = p.slot_in ? p.slot_in[n] : -1;
     const bool live = from >= 0 && from < p.slots;
     const float *S = p.S + ((size_t)(live ? from : 0) * p.H + h) * DK * DV;
-    const unsigned dv0 = (blockIdx.x % SPLIT * NW + w) * 16 * CT + r16, s0 = dv0 * DK + 4 * q4;
+    const unsigned dv0 = 16 * CT * w + r16, s0 = dv0 * DK + 4 * q4;
     f32x4 s[CT][KM];
 #pragma unroll
     for (int c = 0; c < CT; ++c)
@@ -422,7 +422,8 @@ __global__ __launch_bounds__(64 * NW, TT == 1 || NW == 8 ? 4 : 2) void tree_kern
 // ---- the accepted state ---------------------------------------------------------
 // The path from the root to the node, then its tokens one by one: 64 rows (value channels) of a
 // state a workgroup, Dk / 4 lanes a row, as the recurrent form does; each state is read and
-// written once, 8 Dk Dv bytes a (sequence, head).
+// written once, 8 Dk Dv bytes a (sequence, head), which bounds it: 128 trees of 16 nodes x 32 heads x 128
+// channels in 113 us, 4.9 TB/s.
 template <int DK, int DV, typename T, bool DELTA>
 __global__ __launch_bounds__(DK * 4) void accept_kernel(TreeArgs p) {
     constexpr int LPR = DK / 4, R = 4, ROWS = 64, PASS = ROWS / R, SPLIT = DV / ROWS;
@@ -485,28 +486,17 @@ __global__ __launch_bounds__(DK * 4) void accept_kernel(TreeArgs p) {
 }
 
 // ---- host -----------------------------------------------------------------------
-template <int DK, int DV, typename T, bool DELTA, int TT, int NW, int CT> hipError_t tree_nodes(const TreeArgs &a) {
-    const unsigned grid = (unsigned)(a.N * a.H * (DV / (16 * NW * CT)));
-    hipLaunchKernelGGL((tree_kernel<DK, DV, T, DELTA, TT, NW, CT>), dim3(grid), dim3(64 * NW), 0, a.stream, a);
+template <int DK, int DV, typename T, bool DELTA, int TT, int NW> hipError_t tree_nodes(const TreeArgs &a) {
+    hipLaunchKernelGGL((tree_kernel<DK, DV, T, DELTA, TT, NW>), dim3((unsigned)(a.N * a.H)), dim3(64 * NW), 0, a.stream, a);
     return hipGetLastError();
 }
+// Four wavefronts for 16 nodes; for more, whose LDS leaves two workgroups a CU and whose walks want the wavefronts, one
+// for each 16 value channels. The other way round, at 128 channels: 128 x 16 nodes 83 -> 103 us, 64 x 32 75 -> 91, 32 x 64
+// 91 -> 109. Half of a state a workgroup gains nothing for few trees either (8 heads x 64 nodes 29 -> 33 us).
 template <int DK, int DV, typename T, bool DELTA> hipError_t tree_t(const TreeArgs &a) {
-    if constexpr (DV == 128) {
-        // Few trees: half of a state's value channels a workgroup, as long as each has a CU. Many: wavefronts of 32 value
-        // channels for 16 nodes, which share a walk's work among more products; of 16 and twice as many for more
-        // nodes, whose LDS leaves two workgroups a CU.
-        const long long chains = (long long)a.N * a.H;
-        if (chains <= 128)
-            return a.T <= 16   ? tree_nodes<DK, DV, T, DELTA, 1, 4, 1>(a)
-                   : a.T <= 32 ? tree_nodes<DK, DV, T, DELTA, 2, 4, 1>(a)
-                               : tree_nodes<DK, DV, T, DELTA, 4, 4, 1>(a);
-        return a.T <= 16   ? tree_nodes<DK, DV, T, DELTA, 1, 4, 2>(a)
-               : a.T <= 32 ? tree_nodes<DK, DV, T, DELTA, 2, 8, 1>(a)
-                           : tree_nodes<DK, DV, T, DELTA, 4, 8, 1>(a);
-    }
-    return a.T <= 16   ? tree_nodes<DK, DV, T, DELTA, 1, 4, 1>(a)
-           : a.T <= 32 ? tree_nodes<DK, DV, T, DELTA, 2, 4, 1>(a)
-                       : tree_nodes<DK, DV, T, DELTA, 4, 4, 1>(a);
+    return a.T <= 16   ? tree_nodes<DK, DV, T, DELTA, 1, 4>(a)
+           : a.T <= 32 ? tree_nodes<DK, DV, T, DELTA, 2, DV / 16>(a)
+                       : tree_nodes<DK, DV, T, DELTA, 4, DV / 16>(a);
 }
 template <int DK, int DV, typename T, bool DELTA> hipError_t accept_t(const TreeArgs &a) {
     hipLaunchKernelGGL((accept_kernel<DK, DV, T, DELTA>), dim3((unsigned)(a.N * a.H * (DV / 64))), dim3(DK * 4), 0, a.stream, a);

@@ -530,9 +530,9 @@ int lin_prefill(const void *q, const void *k, const void *v, const float *g, con
  *   dS0    [N][H][Dv][Dk] fp32, or NULL to skip it
  *   zero_rows  KDA_ZERO_DQ .. KDA_ZERO_DG added up: the gradients whose rows of tokens in no sequence
  *          become zero; other bits: KDA_ERR_INVALID_ARG
- * A log-decay of -104 or less has gradient 0. A zero-length sequence gives dS0 = dS_out. fp32 precision
- * as above, for dq, dk and dv of bf16 tensors before they are rounded. Results repeat bit for bit. No gradient may
- * be any other buffer of the call. Support, alignment and workspace as for lin_prefill.
+ * A log-decay of -104 or less has gradient 0. A zero-length sequence gives dS0 = dS_out. Products of operands cut
+ * in three (fp32 precision, as above); in two (2^-17) for bf16 gradients that nothing is summed from: dv, and dq and dk
+ * without a decay and without shared heads. Results repeat bit for bit. No gradient may be any other buffer of the call. Support, alignment and workspace as for lin_prefill.
  */
 size_t lin_prefill_backward_workspace_size(int N, int T_total, int H, int Hk, int Dk, int Dv);
 int lin_prefill_backward(const void *q, const void *k, const void *v, const float *g, const void *dout, const float *S0,
