@@ -279,6 +279,7 @@ hipError_t launch_tree_accept(const TreeArgs &a);
 
 // the slots of a state pool. fits: the launch stays within the runtime's limits.
 bool slots_copy_fits(long long n, int layers, size_t slot_bytes);
+bool slots_compact_fits(int slots, size_t slot_bytes);
 hipError_t launch_slots_copy(const SlotsCopyArgs &a);
 hipError_t launch_slots_count(int32_t *uses, const int32_t *which, int n, int slots, int add, hipStream_t stream);
 hipError_t launch_slots_acquire(int32_t *uses, int slots, int32_t *taken, int n, hipStream_t stream);

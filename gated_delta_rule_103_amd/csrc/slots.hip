@@ -155,11 +155,14 @@ __global__ __launch_bounds__(NT) void moves_kernel(char *pool, const int32_t *__
 
 }  // namespace
 
+// a copy's workgroups times their threads stay below 2^32
 bool slots_copy_fits(long long n, int layers, size_t slot_bytes) {
-    // workgroups times their threads stay below 2^32
     const double chunks = (double)(slot_bytes / CHUNK + 1);
     return (double)n * layers * chunks < (double)(1 << 23);
 }
+
+// compaction's workgroups take chunks in turn, so only its counts have to fit
+bool slots_compact_fits(int slots, size_t slot_bytes) { return slots < (1 << 25) && slot_bytes / CHUNK < (1u << 31); }
 
 hipError_t launch_slots_copy(const SlotsCopyArgs &a) {
     const unsigned chunks = (unsigned)((a.slot_bytes + CHUNK - 1) / CHUNK);

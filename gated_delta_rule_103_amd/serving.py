@@ -143,9 +143,16 @@ def _pool(pool, name):
     return layers, slots, pool.numel() // (layers * slots) * pool.element_size()
 
 
+def _few(x, name):
+    """The library counts entries in 32 bits."""
+    if x.numel() >= 2 ** 30:
+        raise ValueError(f"{name} must have fewer than 2^30 entries")
+
+
 def _counts(uses):
     if not isinstance(uses, torch.Tensor) or uses.dim() != 1 or uses.numel() == 0:
         raise ValueError("uses must be a 1-D tensor of counts, one per slot")
+    _few(uses, "uses")
     _expect(uses, "uses", uses.shape, _I32)
 
 
@@ -153,6 +160,7 @@ def _indices(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 1:
         raise ValueError(f"{name} must be a 1-D tensor")
     _expect(x, name, x.shape, _I32)
+    _few(x, name)
 
 
 def kda_slots_copy(pool, src, dst, *, to=None, stream=None):
@@ -202,7 +210,7 @@ def kda_slots_acquire(uses, n: int, *, taken=None, stream=None):
     """Takes the n lowest free slots, whose uses become 1. Returns them, int32 [n] ascending, -1 where there are no more."""
     lib = load_library()
     _counts(uses)
-    if not isinstance(n, int) or not 0 <= n < 2 ** 31:
+    if not isinstance(n, int) or not 0 <= n < 2 ** 30:
         raise ValueError("n must be a count of slots")
     _expect(taken, "taken", (n,), _I32, optional=True)
     dev = _same_gpu(uses=uses, taken=taken)
@@ -226,6 +234,7 @@ def kda_slots_compact(pool, uses, table=None, *, count=None, workspace=None, str
     _expect(uses, "uses", (slots,), _I32)
     if table is not None:
         _expect(table, "table", getattr(table, "shape", None), _I32)
+        _few(table, "table")
     _expect(count, "count", (1,), _I32, optional=True)
     _expect_workspace(workspace)
     dev = _same_gpu(pool=pool, uses=uses, table=table, count=count, workspace=workspace)

@@ -622,6 +622,8 @@ int lin_tree_accept(const void *k, const void *v, const float *g, float *S, cons
  * the slot's new place, -1 for one that was free. count int32 [1] = c. workspace:
  * kda_slots_compact_workspace_size bytes, 256-byte aligned.
  * A negative count is free to acquire and compact alike.
+ * Support (else KDA_ERR_UNSUPPORTED): n * layers * (slot_bytes / 16384 + 1) of a copy below 2^23; slots of a
+ * compaction below 2^25. n, slots and table_n of the others at most 2^30 - 1 (else KDA_ERR_INVALID_ARG).
  */
 int kda_slots_copy(const void *from, void *to, const int32_t *src, const int32_t *dst, int n, int layers, int from_slots,
                    int to_slots, size_t slot_bytes, void *stream);

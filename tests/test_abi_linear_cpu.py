@@ -146,6 +146,23 @@ def test_counts(lib, name):
         assert f(*bad, None) == INVALID
 
 
+def test_largest_counts(lib):
+    big = 2 ** 31 - 1                                       # an index a stride further would pass 32 bits
+    for name in ("kda_slots_share", "kda_slots_release", "kda_slots_acquire"):
+        assert getattr(lib, name)(P[0], P[1], big, 4, None) == INVALID
+    assert lib.kda_slots_acquire(P[0], P[1], 1, big, None) == INVALID
+    assert compact(lib, dict(tn=big)) == INVALID
+    # 9000 states of 32 MB, 302 GB: refused for the missing workspace only
+    assert compact(lib, dict(slots=9000, size=32 << 20, ws=None)) == WORKSPACE
+    with pytest.raises(ValueError, match="n must be a count"):
+        lib_py.kda_slots_acquire(torch.zeros(4, dtype=torch.int32), 2 ** 30)
+    with pytest.raises(ValueError, match="which must have fewer than"):
+        lib_py.kda_slots_share(torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32).expand(2 ** 30))
+    with pytest.raises(ValueError, match="table must have fewer than"):
+        lib_py.kda_slots_compact(torch.zeros(4, 1, 64, 64), torch.zeros(4, dtype=torch.int32),
+                                 torch.zeros(1, dtype=torch.int32).expand(2, 2 ** 30))
+
+
 def test_binding_refuses():
     z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d)
     f, i = torch.float32, torch.int32
