@@ -71,7 +71,7 @@ struct StateJob {
 struct StateJobs { StateJob job[2]; };
 struct BorderArgs {
     const float *S0, *dS_out;
-    float *states, *grads, *dS0, *dots;
+    float *states, *grads, *dS0, *dots, *starts;
     const float *whole;     // each segment's decay
     bool all;               // the gradients' states too
 };
@@ -469,18 +469,21 @@ __global__ __launch_bounds__(256) void border_kernel(Segments segs, BorderArgs a
     cur = a.dS_out ? load(a.dS_out + own) : zero;
     float *d = a.grads + ((size_t)id0 * H + h) * DD + e;
     float *dots = a.dots + (((size_t)id0 * H + h) * gridDim.y + blockIdx.y);
+    auto inner = [&](float *to) {
+        const float x = warp_sum(cur.x * after.x + cur.y * after.y + cur.z * after.z + cur.w * after.w);
+        if ((t & 63) == 0) sums[t >> 6] = x;
+        __syncthreads();
+        if (t == 0) *to = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        __syncthreads();
+    };
     for (int b = blocks - 1; b >= 0; --b) {
         const f32x4 add = load(d + b * step), before = load(p + b * step);
         *reinterpret_cast<f32x4 *>(d + b * step) = cur;
-        float x = cur.x * after.x + cur.y * after.y + cur.z * after.z + cur.w * after.w;
-        x = warp_sum(x);
-        if ((t & 63) == 0) sums[t >> 6] = x;
-        __syncthreads();
-        if (t == 0) dots[(size_t)b * H * gridDim.y] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-        __syncthreads();
+        inner(dots + (size_t)b * H * gridDim.y);
         after = before;
         cur = cur * g[(size_t)b * H] + add;
     }
+    inner(a.starts + ((size_t)n * H + h) * gridDim.y + blockIdx.y);
     if (a.dS0) *reinterpret_cast<f32x4 *>(a.dS0 + own) = cur;
 }
 
@@ -738,13 +741,17 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 // (a token's own share left out of both). The terms of a long sum cancel, and their rounding would
 // not, so it never runs further than a chunk: G at the chunks' borders follows from G at the segment's
 // end by what the chunks' tokens have from the state (read, q . dq) and from its gradient (past,
-// k . dk) alone, and inside a chunk the sums from both of its borders are weighted by their
-// nearness. C tokens a chunk, a wavefront each; a workgroup a (segment, head); sums in 64 bits and a fixed order.
+// k . dk) alone, likewise from the segment's start, and inside a chunk from both of its borders; the two
+// sums are weighted by the nearness of where they come from, so that each keeps the precision of its own end
+// (a first token's gradient is what the initial state leaves of itself, however much the segment adds later).
+// C tokens a chunk, a wavefront each; a workgroup a (segment, head); sums in 64 bits and a fixed order. `starts`: G before each
+// sequence's first token, nullptr: zero, or (only_end) not known.
 __global__ __launch_bounds__(256) void decay_grad_kernel(Segments segs, Gate gate, const float *__restrict__ rows,
                                                          const float *__restrict__ cols, const float *__restrict__ read,
                                                          const float *__restrict__ past, const float *__restrict__ dots,
-                                                         int parts, int C, float *__restrict__ dg, double *__restrict__ sums,
-                                                         int H, int zero_rows) {
+                                                         const float *__restrict__ starts, bool only_end, int parts, int C,
+                                                         float *__restrict__ dg, double *__restrict__ sums, int H,
+                                                         int zero_rows) {
     __shared__ double chunk_sums[kMaxSegment / 32];
     const int id = blockIdx.x / H, h = blockIdx.x % H, t = threadIdx.x, lane = t & 63, w = t >> 6;
     Segment s;
@@ -762,11 +769,22 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(Segments segs, Gate gat
     const size_t at = (size_t)h * segs.T_total + start, cell = (size_t)id * H + h;
     const int chunks = (len + C - 1) / C;
     const float *rd = read + cell * (segs.L / C), *pt = past + cell * (segs.L / C);
+    auto total = [&](const float *p) {
+        double x = 0.;
+        for (int i = 0; i < parts; ++i) x += p[i];
+        return x;
+    };
+    const double last = total(dots + cell * parts);
+    const double first = s.b > 0 ? total(dots + (cell - H) * parts) : starts ? total(starts + ((size_t)s.n * H + h) * parts) : 0.;
     for (int c = w; c < chunks; c += 4) {                    // C <= 64 tokens, one a lane
-        double G = 0.;
-        for (int i = 0; i < parts; ++i) G += dots[cell * parts + i];
-        for (int i = chunks - 1; i > c; --i) G += (double)rd[i] - (double)pt[i];
-        const double before = G + (double)rd[c] - (double)pt[c];
+        double to_c = 0., behind = 0.;                       // what G loses up to this chunk, and behind it
+        for (int i = 0; i < c; ++i) to_c += (double)rd[i] - (double)pt[i];
+        for (int i = chunks - 1; i > c; --i) behind += (double)rd[i] - (double)pt[i];
+        const double own = (double)rd[c] - (double)pt[c], all_of_it = to_c + own + behind;
+        const double begin = only_end ? last + all_of_it : first;
+        const double u0 = (double)c / chunks, u1 = (double)(c + 1) / chunks;
+        const double before = (1. - u0) * (begin - to_c) + u0 * (last + own + behind);
+        const double G = (1. - u1) * (begin - to_c - own) + u1 * (last + behind);
         const int i = c * C + lane, n = min(C, len - c * C);
         const double x = lane < n ? (double)rows[at + i] - (double)cols[at + i] : 0.;
         const double upto = wave_prefix(x, lane), all = __shfl(upto, 63, 64);
@@ -860,7 +878,7 @@ struct Carver {
 };
 struct ForwardSpace { float *states, *whole; };
 struct BackwardSpace {
-    float *states, *grads, *whole, *dots, *rows, *cols, *read, *past, *dq, *dk;
+    float *states, *grads, *whole, *dots, *starts, *rows, *cols, *read, *past, *dq, *dk;
     double *sums;
 };
 ForwardSpace carve_forward(Carver &c, int N, long long longest, long long T_total, int H, int Dk, int Dv, int L) {
@@ -878,6 +896,7 @@ BackwardSpace carve_backward(Carver &c, int N, long long T_total, int H, int gro
     s.grads = c.take<float>(cells * Dk * Dv);
     s.whole = c.take<float>(cells);
     s.dots = c.take<float>(cells * (Dk * Dv / 1024));
+    s.starts = c.take<float>((size_t)N * H * (Dk * Dv / 1024));
     s.sums = c.take<double>(cells);
     s.rows = c.take<float>((size_t)T_total * H);
     s.cols = c.take<float>((size_t)T_total * H);
@@ -962,7 +981,7 @@ template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs 
         e = run_states<T, DK, DV>(segs, gate, st, 2, ws.whole, a.H, group, a.stream);
         if (e != hipSuccess) return e;
         BorderArgs b{};
-        b.S0 = a.S0; b.dS_out = a.dS_out; b.states = ws.states; b.grads = ws.grads; b.dS0 = a.dS0; b.dots = ws.dots;
+        b.S0 = a.S0; b.dS_out = a.dS_out; b.states = ws.states; b.grads = ws.grads; b.dS0 = a.dS0; b.dots = ws.dots; b.starts = ws.starts;
         b.whole = ws.whole; b.all = true;
         e = run_borders(segs, b, a.H, DK * DV, a.stream);
         if (e != hipSuccess) return e;
@@ -1010,7 +1029,7 @@ template <typename T, int DK, int DV> hipError_t backward(const LinBackwardArgs 
     }
     if (a.g) {
         hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(ids * a.H)), dim3(256), 0, a.stream, segs, gate, ws.rows, ws.cols,
-                           ws.read, ws.past, ws.dots, borders ? DK * DV / 1024 : 0, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
+                           ws.read, ws.past, ws.dots, borders ? ws.starts : nullptr, !borders && a.S0, borders ? DK * DV / 1024 : 0, Parts<T>::C, a.dg, ws.sums, a.H, a.zero_rows & 8);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.fixed) {
             hipLaunchKernelGGL(fixed_grad_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, ws.sums, a.dg, ids, a.H);

@@ -5,6 +5,7 @@ and sums of at most a few thousand terms are taken in fp32: 1e-4, the bar of the
 fp32 paths. bf16 results are off by half a step, 2^-8 relative, besides; their operands, cut in two
 (2^-17, with terms no larger than a few times the sum's RMS), stay under the same 1e-4.
 """
+import math
 import sys
 
 import numpy as np
@@ -359,3 +360,21 @@ def test_prefill_then_steps_is_one_prefill():
         step = lib.lin_decode(*(on(x[n][t:t + 1]) for n in "qkvg"), state, out_dtype=torch.float32)
         close(f"token {t}", step, o[t:t + 1])
     close("S", state, S)
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+def test_decay_gradient_of_what_a_state_leaves(io):
+    """Sequences of one token: the decay's gradient is e^g <S0, dS>, whatever the token adds to the state behind it (here
+    3000 times as much). Off by at most 24 half steps of the sum of its terms' magnitudes: 4 for the cut product and the decay of
+    dS, 3 for its sum, its product with the decay and the term, 12 for sums over 4 values, 64 lanes and 4 wavefronts, 5 spare."""
+    gen = torch.Generator().manual_seed(11)
+    N, H, Dk, Dv = 5, 3, 64, 128
+    rn = lambda *s, dt=torch.float32: torch.randn(*s, generator=gen).to(dt).cuda()
+    q, k, v, dout = rn(1, N, 1, Dk, dt=io), rn(1, N, 1, Dk, dt=io), rn(1, N, H, Dv, dt=io), rn(1, N, H, Dv, dt=io)
+    g = torch.full((1, N, H), -8., device="cuda")
+    S0, dS = rn(N, H, Dv, Dk), rn(N, H, Dv, Dk)
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    dg = lib.lin_prefill_backward(q, k, v, g, dout, S0, dS, cu_seqlens=cu)[3][0].double()
+    terms = S0.double() * (dS.double() + dout[0].double()[..., None] * q[0].double()[:, :, None]) * math.exp(-8.)
+    want, size = terms.sum((-1, -2)), terms.abs().sum((-1, -2))
+    assert ((dg - want).abs() <= 24 * 2. ** -24 * size).all()
