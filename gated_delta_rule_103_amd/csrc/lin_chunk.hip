@@ -32,7 +32,7 @@
 // 16 channels rather than four of 32 leave four to a SIMD, which the chunk's barriers and LDS reads need.
 //
 // 8192 tokens x 32 heads x 128, bf16: forward 115 us (states 37, 4.5 TB/s; borders 11; outputs 76, bound by instruction issue
-// and barriers: vector 46%, matrix 31%, LDS 43% of their cycles, and no less with q and k from cache), gradient 372 us
+// and barriers: vector 46%, matrix 31%, LDS 43% of their cycles, and no less with q and k from cache), gradient 372-379 us
 // (states 78, borders 25, dq and dk 235, dv 81, decays 10).
 #include "kda_device.h"
 #include "kda_launch.h"
