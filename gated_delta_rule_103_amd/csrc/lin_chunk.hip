@@ -741,11 +741,18 @@ __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate g
 // (a token's own share left out of both). The terms of a long sum cancel, and their rounding would
 // not, so it never runs further than a chunk: G at the chunks' borders follows from G at the segment's
 // end by what the chunks' tokens have from the state (read, q . dq) and from its gradient (past,
-// k . dk) alone, likewise from the segment's start, and inside a chunk from both of its borders; the two
-// sums are weighted by the nearness of where they come from, so that each keeps the precision of its own end
-// (a first token's gradient is what the initial state leaves of itself, however much the segment adds later).
+// k . dk) alone, likewise from the segment's start, and inside a chunk from both of its borders. Either sum is off by
+// some 2^-24 of what went into it, G and all terms, which strong decays make e^g times as much from a token to the
+// next (in opposite directions), so the two are weighted by the squares of those magnitudes, each end's sum by the
+// other's: 64 tokens of g = -8 and -16 between two states 2.5e-4 and 2.6 (weights by distance) -> 6e-7 relative.
 // C tokens a chunk, a wavefront each; a workgroup a (segment, head); sums in 64 bits and a fixed order. `starts`: G before each
 // sequence's first token, nullptr: zero, or (only_end) not known.
+struct Carried { double x, size; };         // a sum, and the magnitudes that went into it
+__device__ __forceinline__ Carried joined(Carried a, Carried b) {
+    const double aa = a.size * a.size, bb = b.size * b.size;
+    const double w = aa + bb > 0. ? aa / (aa + bb) : 0.5;
+    return Carried{(1. - w) * a.x + w * b.x, fmin(a.size, b.size)};
+}
 __global__ __launch_bounds__(256) void decay_grad_kernel(Segments segs, Gate gate, const float *__restrict__ rows,
                                                          const float *__restrict__ cols, const float *__restrict__ read,
                                                          const float *__restrict__ past, const float *__restrict__ dots,
@@ -770,26 +777,31 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(Segments segs, Gate gat
     const int chunks = (len + C - 1) / C;
     const float *rd = read + cell * (segs.L / C), *pt = past + cell * (segs.L / C);
     auto total = [&](const float *p) {
-        double x = 0.;
-        for (int i = 0; i < parts; ++i) x += p[i];
+        Carried x{0., 0.};
+        for (int i = 0; i < parts; ++i) x = Carried{x.x + p[i], x.size + fabs((double)p[i])};
         return x;
     };
-    const double last = total(dots + cell * parts);
-    const double first = s.b > 0 ? total(dots + (cell - H) * parts) : starts ? total(starts + ((size_t)s.n * H + h) * parts) : 0.;
+    // from c onwards by chunk i's tokens, and back
+    auto term = [&](int i) { return Carried{(double)rd[i] - (double)pt[i], fabs((double)rd[i]) + fabs((double)pt[i])}; };
+    auto plus = [](Carried a, Carried b) { return Carried{a.x + b.x, a.size + b.size}; };
+    auto minus = [](Carried a, Carried b) { return Carried{a.x - b.x, a.size + b.size}; };
+    const Carried last = total(dots + cell * parts);
+    const Carried first = s.b > 0 ? total(dots + (cell - H) * parts)
+                          : starts ? total(starts + ((size_t)s.n * H + h) * parts) : Carried{0., 0.};
     for (int c = w; c < chunks; c += 4) {                    // C <= 64 tokens, one a lane
-        double to_c = 0., behind = 0.;                       // what G loses up to this chunk, and behind it
-        for (int i = 0; i < c; ++i) to_c += (double)rd[i] - (double)pt[i];
-        for (int i = chunks - 1; i > c; --i) behind += (double)rd[i] - (double)pt[i];
-        const double own = (double)rd[c] - (double)pt[c], all_of_it = to_c + own + behind;
-        const double begin = only_end ? last + all_of_it : first;
-        const double u0 = (double)c / chunks, u1 = (double)(c + 1) / chunks;
-        const double before = (1. - u0) * (begin - to_c) + u0 * (last + own + behind);
-        const double G = (1. - u1) * (begin - to_c - own) + u1 * (last + behind);
+        Carried to_c{0., 0.}, behind{0., 0.};                // what G loses up to this chunk, and behind it
+        for (int i = 0; i < c; ++i) to_c = plus(to_c, term(i));
+        for (int i = chunks - 1; i > c; --i) behind = plus(behind, term(i));
+        const Carried own = term(c), from_end = plus(last, behind);
+        const Carried begin = only_end ? plus(plus(from_end, own), to_c) : first, from_start = minus(begin, to_c);
+        const Carried before = joined(from_start, plus(from_end, own)), after = joined(minus(from_start, own), from_end);
         const int i = c * C + lane, n = min(C, len - c * C);
-        const double x = lane < n ? (double)rows[at + i] - (double)cols[at + i] : 0.;
-        const double upto = wave_prefix(x, lane), all = __shfl(upto, 63, 64);
-        const double near = (double)lane / n;
-        double d = near * (G + (all - upto) + x) + (1. - near) * (before - (upto - x));
+        const double rw = lane < n ? rows[at + i] : 0., cl = lane < n ? cols[at + i] : 0.;
+        const Carried x{rw - cl, fabs(rw) + fabs(cl)};
+        const Carried upto{wave_prefix(x.x, lane), wave_prefix(x.size, lane)};
+        const Carried rest{__shfl(upto.x, 63, 64) - upto.x, __shfl(upto.size, 63, 64) - upto.size};
+        double d = joined(Carried{before.x - (upto.x - x.x), before.size + (upto.size - x.size)},
+                          Carried{after.x + rest.x + x.x, after.size + rest.size + x.size}).x;
         // at -104 the decay is zero, and its gradient too
         if (lane >= n || gate.g[gate.fixed ? h : (size_t)(start + i) * H + h] <= kMinLog) d = 0.;
         if (gate.fixed) {
