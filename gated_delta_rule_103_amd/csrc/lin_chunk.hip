@@ -98,9 +98,25 @@ struct Segment {
 __device__ __forceinline__ int offset(const Segments &s, int n) {
     return s.cu ? min(max(s.cu[n], 0), s.T_total) : n * s.T;
 }
+// Where sequence i, one a lane, begins and ends. An offset below an earlier one would make sequences share ids; in a call
+// of up to 64 sequences (i: the lane, or the last one) it is cut to it, so that every one has segments of its own and its
+// state is written. With more there is no such look at all of them, and offsets that fall give undefined results (in bounds).
+__device__ __forceinline__ void lane_bounds(const Segments &s, int i, int &begin, int &end) {
+    begin = offset(s, i);
+    const int next = offset(s, i + 1);
+    if (s.cu && s.N <= 64 && __any(next < begin)) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) begin = max(begin, __shfl_up(begin, o, 64));
+    }
+    end = max(next, begin);
+}
+// The same for one sequence, in every lane of a whole wavefront.
 __device__ __forceinline__ void sequence_bounds(const Segments &s, int n, int &begin, int &end) {
-    begin = offset(s, n);
-    end = max(offset(s, n + 1), begin);
+    const bool all = s.cu && s.N <= 64;                     // uniform
+    lane_bounds(s, all ? min((int)(threadIdx.x & 63), s.N - 1) : n, begin, end);
+    if (!all) return;
+    begin = __shfl(begin, n, 64);
+    end = __shfl(end, n, 64);
 }
 __device__ __forceinline__ int block_count(const Segments &s, int len) { return max(1, (len + s.L - 1) >> s.shift); }
 __device__ __forceinline__ int first_id(const Segments &s, int n, int begin) { return (begin >> s.shift) + n; }
@@ -116,7 +132,9 @@ __device__ __forceinline__ bool find_segment(const Segments &s, int id, Segment 
         lo += c * each;
         span = min(each, span - c * each);
     }
-    const int i = min(lo + lane, s.N - 1), begin = offset(s, i), end = max(offset(s, i + 1), begin);
+    const int i = min(lo + lane, s.N - 1);
+    int begin, end;
+    lane_bounds(s, i, begin, end);
     const bool before = lane < span && first_id(s, i, begin) <= id;
     const int c = max(__popcll(__ballot(before)) - 1, 0);
     x.n = __builtin_amdgcn_readfirstlane(lo + c);
@@ -840,7 +858,6 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
     const size_t u = (size_t)blockIdx.x * 256 + threadIdx.x;
     const int HS = H / group, q = D / 4;
     const size_t token = u / ((size_t)HS * q);
-    if (token >= (size_t)segs.T_total) return;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     bool live = true;
     if (segs.cu) {
@@ -848,8 +865,8 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
         sequence_bounds(segs, 0, b0, e0);
         sequence_bounds(segs, segs.N - 1, b1, e1);
         live = token >= (size_t)b0 && token < (size_t)e1;
-        if (!live && !zero_rows) return;
     }
+    if (token >= (size_t)segs.T_total || (!live && !zero_rows)) return;
     const int hs = (int)(u / q % HS), c = (int)(u % q) * 4;
     if (live)
         for (int i = 0; i < group; ++i) sum += *reinterpret_cast<const f32x4 *>(part + (token * H + hs * group + i) * D + c);

@@ -499,8 +499,9 @@ int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, co
  *   S0     [N][H][Dv][Dk] fp32 or NULL (zero)   S_out  the final states, or NULL; may be S0
  *   out    [T_total][H][Dv] out_dtype
  *   cu_seqlens, N, B, T  as for kda_prefill. Packed offsets may start behind 0 and end before
- *          T_total; offsets outside [0, T_total] or below the one before them are cut. Offsets
- *          that fall make sequences share tokens: those rows are undefined (no fault)
+ *          T_total; offsets outside [0, T_total] are cut to it, and in a call of N <= 64 one below
+ *          an earlier one to that one. With more sequences, offsets that fall leave every output,
+ *          state and gradient of the call undefined (no fault)
  *   zero_rows  1: out rows of tokens in no sequence become zero; 0: they stay as they were
  *          (else KDA_ERR_INVALID_ARG)
  * A zero-length sequence gives S_out = S0. q, k, v, out, S0 and S_out 16-byte aligned; out must
