@@ -138,7 +138,7 @@ int kda_slots_copy(const void *from, void *to, const int32_t *src, const int32_t
 namespace {
 
 int count_impl(int32_t *uses, const int32_t *which, int n, int slots, int add, void *stream) {
-    if (n < 0 || n > INT_MAX / 2 || slots < 1 || !uses || (n > 0 && !which) || uses == which) return KDA_ERR_INVALID_ARG;
+    if (n < 0 || n > INT_MAX / 2 || slots < 1 || slots > INT_MAX / 2 || !uses || (n > 0 && !which) || uses == which) return KDA_ERR_INVALID_ARG;
     if (n == 0) return KDA_OK;
     return kda::launch_slots_count(uses, which, n, slots, add, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK
                                                                                                               : KDA_ERR_HIP;
@@ -169,7 +169,7 @@ size_t kda_slots_compact_workspace_size(int slots) {
 
 int kda_slots_compact(void *pool, int32_t *uses, int32_t *table, int32_t *count, int table_n, int layers, int slots,
                       size_t slot_bytes, void *workspace, size_t workspace_bytes, void *stream) {
-    if (layers < 1 || slots < 1 || slots > INT_MAX / 8 || table_n < 0 || table_n > INT_MAX / 2 || slot_bytes == 0 || slot_bytes % 16 != 0)
+    if (layers < 1 || slots < 1 || table_n < 0 || table_n > INT_MAX / 2 || slot_bytes == 0 || slot_bytes % 16 != 0)
         return KDA_ERR_INVALID_ARG;
     if (!pool || !uses || !count || (table_n > 0 && !table) || misaligned(pool, 15)) return KDA_ERR_INVALID_ARG;
     if (uses == count || (table && (table == uses || table == count))) return KDA_ERR_INVALID_ARG;
