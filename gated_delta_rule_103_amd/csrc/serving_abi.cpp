@@ -54,6 +54,10 @@ int tree_impl(kda::TreeArgs &a, kda_dtype io, int beta_dtype, int out_dtype, int
 
 int accept_impl(kda::TreeArgs &a, kda_dtype io, int beta_dtype, bool delta) {
     if (!a.node || !a.slot_out) return KDA_ERR_INVALID_ARG;
+    // the pool is written while other workgroups still read the tokens and the indexes
+    const void *ins[] = {a.k, a.v, a.g, a.beta, a.slot_in, a.slot_out, a.parent, a.node};
+    for (const void *x : ins)
+        if (x && x == a.S) return KDA_ERR_INVALID_ARG;
     const int bad = check(a, io, beta_dtype, delta);
     if (bad != KDA_OK) return bad;
     return kda::launch_tree_accept(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;

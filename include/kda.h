@@ -584,7 +584,7 @@ int lin_recurrent(const void *q, const void *k, const void *v, const float *g, f
  *          [-1, T): nothing is written for the sequence
  *   slot_out int32 [N]: the slot that receives the state (it may be slot_in's); outside [0, slots): none.
  *          A slot that one sequence writes must not be read nor written by another one of the call.
- * opt->qk_l2norm normalises k.
+ * opt->qk_l2norm normalises k. S must be none of the other buffers (else KDA_ERR_INVALID_ARG).
  *
  * lin_tree, lin_tree_accept -- the same for linear attention without the delta rule: no beta, q and k
  * [N][T][Hk][Dk], Dk and Dv each 64 or 128, g [N][T][H], [H] (KDA_GATE_FIXED) or NULL.
