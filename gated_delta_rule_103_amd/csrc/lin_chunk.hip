@@ -110,13 +110,12 @@ __device__ __forceinline__ void lane_bounds(const Segments &s, int i, int &begin
     }
     end = max(next, begin);
 }
-// The same for one sequence, in every lane of a whole wavefront.
+// The same for one sequence, n the same in every lane of a whole wavefront.
 __device__ __forceinline__ void sequence_bounds(const Segments &s, int n, int &begin, int &end) {
     const bool all = s.cu && s.N <= 64;                     // uniform
     lane_bounds(s, all ? min((int)(threadIdx.x & 63), s.N - 1) : n, begin, end);
-    if (!all) return;
-    begin = __shfl(begin, n, 64);
-    end = __shfl(end, n, 64);
+    begin = __builtin_amdgcn_readlane(begin, all ? n : 0);
+    end = __builtin_amdgcn_readlane(end, all ? n : 0);
 }
 __device__ __forceinline__ int block_count(const Segments &s, int len) { return max(1, (len + s.L - 1) >> s.shift); }
 __device__ __forceinline__ int first_id(const Segments &s, int n, int begin) { return (begin >> s.shift) + n; }
