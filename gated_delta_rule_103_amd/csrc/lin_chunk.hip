@@ -31,9 +31,11 @@
 // product's operand. Only scores go through LDS, because the wavefronts share them. Eight wavefronts of
 // 16 channels rather than four of 32 leave four to a SIMD, which the chunk's barriers and LDS reads need.
 //
-// 8192 tokens x 32 heads x 128, bf16: forward 115 us (states 37, 4.5 TB/s; borders 11; outputs 76, bound by instruction issue
-// and barriers: vector 46%, matrix 31%, LDS 43% of their cycles, and no less with q and k from cache), gradient 372-379 us
-// (states 78, borders 25, dq and dk 235, dv 81, decays 10).
+// 8192 tokens x 32 heads x 128, bf16, calls one behind the other: forward 115-119 us, gradient 375-381. Kernel by kernel under
+// the profiler (average, least), whose times add up to more than a call's: forward states 37, 34 (4.5 TB/s), borders 11, 11,
+// outputs 76, 75, bound by instruction issue and barriers (vector instructions 55% of their cycles, 47% without the
+// matrix ones; matrix units 31%, LDS 44%; no less time with q and k from cache); gradient states 79, 72, borders 26, 24, dq
+// and dk 243, 216, dv 84, 73, decays 12, 11.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -518,7 +520,9 @@ template <typename T, typename TO, int DA, int DC, int NI, int NX, int C, bool D
 __global__ __launch_bounds__(DC * 4, 4) void output_kernel(Segments segs, Gate gate, OutputJobs jobs, int H, int group) {
     constexpr int NT = DC * 4, NW = DC / 16, NC = C / 16, ND = DA / 16, TILES = NC * (NC + 1) / 2;
     constexpr bool ROWS = sizeof(TO) == 2 && DC == 128 && DC <= DA && !DOT;
-    // ROWS: outputs leave through the queries' tile, whole rows at a time (8k forward 125 -> 115 us)
+    // ROWS: outputs leave through the queries' tile, whole rows at a time (8k forward 125 -> 115 us). Rows of 64 values are
+    // half as long and gain 1% or nothing (8k x 32 x 64: 62 -> 61 us, 128 x 64 86 either way); with DOT six registers spill at
+    // 128 x 128 (8k gradient 378 -> 400 us)
     __shared__ bf16_t X[NI * C * DA], Y[NI * C * DA], Z[NI * C * DC];
     __shared__ bf16x4 P[NC * NC / 4 + NC / 2][NX][64][2];  // scores(i, m): 16 query tokens, 32 key tokens, the two halves of the latter
     auto scores = [](int i, int m) { return (i / 2) * (i / 2 + 1) + (i & 1) * (i / 2 + 1) + m; };
@@ -873,14 +877,20 @@ __global__ __launch_bounds__(256) void share_kernel(Segments segs, const float *
 }
 
 // ---- host -----------------------------------------------------------------------
-// Tokens a segment, a power of two: the least that leaves one round of workgroups, two a CU; more segments
-// would be traffic (8 D^2 bytes each and pass) for nothing. 8192 tokens x 32 heads with 256, 512, 1024 tokens a
-// segment: 138, 115, 131 us; 4832 packed x 16 (128 x 64) with 128, 256, 512: 54, 51, 61; 5000 x 8 with 64 and 128: 58,
-// 45 us; 65536 x 16 with 512 and 1024: 467, 418.
+// Tokens a segment, a power of two: the least that leaves one round of workgroups at two a CU, which is what the LDS of
+// the bf16 kernels at 128 x 128 allows; more segments would be traffic (8 D^2 bytes each and pass) for nothing. In us, with
+// half as many tokens a segment, these, twice as many:
+//     forward, bf16: 8192 x 32 heads 137, 115, 130; 4832 packed x 16 (128 x 64) 53, 51, 61; 8192 x 32 at 64 x 64 (three workgroups
+//     a CU) 68, 62, 78; 128 x 64 100, 86, 108; 64 x 128 96, 85, 95; 5000 x 8 45 with 64 tokens, 58 with 128
+//     forward, fp32: 4096 x 16 at 128 x 128 (one workgroup a CU, so two rounds) 114, 87, 75; at 64 x 64 51, 41, 44
+//     gradient, whose launches hold two or three jobs: bf16 8192 x 32 431, 378, 378; 64 x 64 218, 219, 225; fp32 4096 x 16 309, 242, 219
+// So fp32 at 128 x 128 would take 10 to 14% less with segments twice as long; the rule is that of the others.
 //
-// Short sequences (`longest`: no sequence has more tokens) are one segment each, and their states need no passes
-// of their own: 16 x 200 tokens x 8 heads 38 -> 25 us, 128 x 8 22 -> 15; one of 256 x 8
-// has too few workgroups that way (gradient 34 -> 54 us). A longest below T_total never makes segments shorter
+// Short sequences of a dense batch (`longest`: no sequence has more tokens) are one segment each, and their states need no
+// passes of their own: 16 x 200 tokens x 8 heads 38 -> 25 us, 128 x 8 22 -> 15. `few`, 256 tokens, or 128 where
+// T_total * H is below 16384: one of 256 x 8 has too few workgroups that way (gradient 34 -> 54 us). The lengths of packed
+// sequences are not known on the host, so T_total stands for the longest: 64 x 256 x 32 heads take 157 us dense and 199
+// packed. The gradient needs the passes where dS_out is given. A longest below T_total never makes segments shorter
 // than T_total alone would, which the workspace is sized by.
 int segment_length(long long longest, long long T_total, int H) {
     const long long L = T_total * H / 512;

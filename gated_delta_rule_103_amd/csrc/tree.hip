@@ -21,9 +21,11 @@
 // which is the operand layout of the fp32 products that follow, and (I + L) is inverted in its 16 x 16
 // diagonal blocks only.
 //
-// 128 trees of 16 nodes x 32 heads x 128 channels: 83 us, 369 MB, 4.4 TB/s (fp32 matrix instructions 89); 64 of 32 75 us, 32
-// of 64 91 us (all their Kd and Qd in LDS at once: 104 and 110, for want of workgroups a CU); linear
-// attention's 68 us. One tree of 61 nodes x 16 heads: 21 us, latency.
+// 128 trees of 16 nodes x 32 heads x 128 channels: 83-88 us, 369 MB, 4.2-4.4 TB/s, against 72 at a copy's rate (fp32 matrix
+// instructions 89); linear attention's 68 against 61. More nodes bring more walks, a step a pair of node and ancestor on the
+// vector units: 64 trees of 32 nodes 75-78 us against 46, 32 of 64 91-98 against 33 (all their Kd and Qd in LDS at once: 104
+// and 110, for want of workgroups a CU), linear attention's 56 against 34 and 64 against 21. One tree of 61 nodes x 16 heads:
+// 21 us, latency.
 #include "kda_device.h"
 #include "kda_launch.h"
 

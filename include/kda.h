@@ -508,7 +508,8 @@ int kda_layer_norm_backward(const void *x, const void *dy, const float *mean, co
  * be none of the inputs.
  *
  * Support (else KDA_ERR_UNSUPPORTED): Dk and Dv each 64 or 128; io_dtype KDA_F32 with fp32 out, or
- * KDA_BF16 with either; H at most 4096, N * H below 2^22, T_total * H below 2^27. Hk must divide H
+ * KDA_BF16 with either; H at most 4096, T_total * H below 2^27, (T_total / L + N) * H below 2^23 with L
+ * tokens a segment, 64 or more (N * H below 2^22 is enough). Hk must divide H
  * (else KDA_ERR_INVALID_ARG).
  * Arithmetic: states in fp32 with products of operands cut in three bf16 parts (fp32 precision),
  * for values whose products stay between about 1e-33 and 3.3e38; an fp32 out likewise; a bf16 out is
@@ -533,7 +534,11 @@ int lin_prefill(const void *q, const void *k, const void *v, const float *g, con
  *          become zero; other bits: KDA_ERR_INVALID_ARG
  * A log-decay of -104 or less has gradient 0. A zero-length sequence gives dS0 = dS_out. Products of operands cut
  * in three (fp32 precision, as above); in two (2^-17) for bf16 gradients that nothing is summed from: dv, and dq and dk
- * without a decay and without shared heads. Results repeat bit for bit. No gradient may be any other buffer of the call. Support, alignment and workspace as for lin_prefill.
+ * without a decay and without shared heads. dg is a difference of sums carried from a segment's ends, weighted by their
+ * magnitudes: off by some 2^-24 of the smaller of what the two hold up to its token, about 1e-6 or less of a tensor in the
+ * 2-norm; a value far below its neighbours' (behind a decay of e^-16 among slow ones) keeps no digits of its own.
+ * Results repeat bit for bit. No gradient may be any other buffer of the call. Support, alignment and workspace as for
+ * lin_prefill.
  */
 size_t lin_prefill_backward_workspace_size(int N, int T_total, int H, int Hk, int Dk, int Dv);
 int lin_prefill_backward(const void *q, const void *k, const void *v, const float *g, const void *dout, const float *S0,
@@ -572,7 +577,8 @@ int lin_recurrent(const void *q, const void *k, const void *v, const float *g, f
  *          the node is absent, and so are those that descend from it. Their inputs do not matter
  *   zero_rows  1: out rows of absent nodes become zero; 0: they stay as they were (else
  *          KDA_ERR_INVALID_ARG)
- * slot_in and parent are device arrays. fp32 arithmetic. A NaN or an infinity in a node that is there
+ * slot_in and parent are device arrays. fp32 arithmetic, the products with the state of operands cut in three
+ * bf16 parts (fp32 precision for values between about 1e-33 and 3.3e38). A NaN or an infinity in a node that is there
  * may reach other nodes of its sequence. opt: gate and qk_l2norm as for kda_decode_ex, no snapshots; may be
  * NULL. Support: 1 <= T <= KDA_TREE_NODES; Dk == Dv in {64, 128}; N * H below 2^22, H at
  * most 65536 (else KDA_ERR_UNSUPPORTED). q, k, v, a per-channel g, S and out 16-byte aligned; out none of the other buffers.
