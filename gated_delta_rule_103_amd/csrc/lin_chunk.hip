@@ -20,7 +20,9 @@
 // value (decayed, a state, fp32 input) is cut into bf16 parts whose sum it is to 2^-17 (two)
 // or 2^-25 (three); of parts i and j the products i + j < the number of parts are taken.
 // States take three always; outputs in bf16 two, outputs in fp32 and those that a decay's
-// gradient is summed from three. The exponents of decays are differences of cumulative sums
+// gradient is summed from three. (bf16 outputs, whose own rounding is 2^-9, are 1.66e-3 from 64 bits either way; with two
+// parts some roundings fall the other way, 1.0e-4 of the norm, with three 1.7e-5, at 127 us instead of 116 for the 8k
+// forward and 386 instead of 375 for its gradient.) The exponents of decays are differences of cumulative sums
 // that are taken in 64 bits and held as whole and fractional part in base 2, so that no
 // difference loses bits and no factor exceeds the decay that it stands for.
 //
